@@ -1,8 +1,8 @@
 /*
  * rn.h — C ABI of a GB300 (sm_103a) library of fused LayerNorm / RMSNorm
- * kernels with FP8 (E4M3), MXFP8 and NVFP4 output quantization, and of the
+ * kernels with FP8 (E4M3), MXFP8 and NVFP4 output quantization, of the
  * scaled activations (SReLU, SwiGLU, clamped SwiGLU) with the same
- * quantized outputs.
+ * quantized outputs, and of the gated feed-forward block between them.
  *
  * What is computed follows the page "Implementation:NVIDIA TransformerEngine
  * PyTorch Ext Normalization": forward functions normalize each row of x and
@@ -323,6 +323,82 @@ rn_status rn_scaled_act_bwd(rn_act act, const void* dy, const void* x, rn_dtype 
                             const float* scales, int64_t N, int64_t H,
                             float limit, float alpha, void* dx, float* dscales,
                             void* stream);
+
+/*
+ * Gated feed-forward block: both projections, the activation and the
+ * product in one call (page "Activation + GroupedLinear Fusion for MOE and
+ * other MOE optimizations", which fuses the scaled activations above with
+ * the products around them; one expert's block here).
+ *   p = x W^T = [a | b],  y[i, j] = s_i * act(a, b)[i, j]
+ * with act RN_ACT_SWIGLU or RN_ACT_CLAMPED_SWIGLU as for rn_scaled_act_fwd
+ * (RN_ACT_SRELU has one projection: RN_ERR_UNSUPPORTED).
+ *   x       bf16 [N, K]
+ *   w       bf16 [2H, K]: the H gate rows, then the H linear rows
+ *   scales  fp32 [N] or NULL (all 1)
+ *   out     `mode` NONE (bf16 or fp32 [N, H]), FP8_DELAYED, or MXFP8 with the
+ *           rowwise blocks only (H % 32 == 0, any N); FP8_CURRENT, NVFP4 and
+ *           the columnwise copy return RN_ERR_UNSUPPORTED.  y is formed in
+ *           fp32 from the fp32 sums a, b and rounded or quantized once.
+ *   pre     bf16 [N, 2H] or NULL: [a | b], each rounded once, for
+ *           rn_gated_ffn_bwd.
+ * dtype must be RN_BF16 (RN_F32 returns RN_ERR_UNSUPPORTED: the tensor cores
+ * have no product that keeps fp32).  K % 8 == 0, H % 8 == 0, any N; x, w,
+ * pre and out->data 16-byte aligned.  Outputs must not overlap inputs.
+ * Results do not depend on earlier calls and are the same from run to run.
+ * Outputs of non-finite inputs are unspecified, and a row of x reaches no
+ * other row's output (amax aside).  No workspace.
+ */
+rn_status rn_gated_ffn_fwd(rn_act act, const void* x, const void* w, rn_dtype dtype,
+                           const float* scales, int64_t N, int64_t K, int64_t H, float limit,
+                           float alpha, rn_quant_mode mode, const rn_output* out, void* pre,
+                           void* stream);
+
+/*
+ * Backward of rn_gated_ffn_fwd at the stored projections `pre`:
+ *   dp [N, 2H]  = s_i * dy * act'(pre), rounded once to bf16 (the tensor
+ *                 cores' operand; the rounding rn_scaled_act_bwd's dx has)
+ *   dx [N, K]   = dp W        bf16, or NULL to skip (w may then be NULL)
+ *   dw [2H, K]  = dp^T x      bf16, or NULL to skip (x may then be NULL)
+ *   dscales [N] = sum_j dy[i, j] * act(pre)[i, j], fp32, or NULL to skip
+ * dy bf16 [N, H]; sums in fp32, each output rounded once.  dw is overwritten
+ * (zeros for N == 0).  Results are the same from run to run.
+ * Workspace protocol as for rn_layernorm_bwd: with workspace, dx, dw and
+ * dscales all NULL the call stores the required byte count in
+ * *workspace_bytes (it depends on N, K and H only); otherwise a missing or
+ * smaller workspace returns RN_ERR_WORKSPACE.  The workspace is 16-byte
+ * aligned, need not be initialized and must not be shared by calls that may
+ * run concurrently.  dtype, sizes and alignment as for the forward.
+ */
+rn_status rn_gated_ffn_bwd(rn_act act, const void* dy, const void* x, const void* w, const void* pre,
+                           rn_dtype dtype, const float* scales, int64_t N, int64_t K, int64_t H,
+                           float limit, float alpha, void* dx, void* dw, float* dscales,
+                           void* workspace, size_t* workspace_bytes, void* stream);
+
+/*
+ * Products of one or a few tokens with NVFP4 weights, as rn_quantize_only
+ * (RN_QUANT_NVFP4) writes them for a weight matrix [R, K]: E2M1 codes
+ * w_codes [R, K/2], E4M3 block scales w_scales [R, K/16] and the device
+ * scalar w_scale_inv = 1/S.  An element stands for E2M1 value *
+ * value(scale code) * w_scale_inv.
+ *   rn_nvfp4_matvec     y [N, R] = x W^T, bf16 or fp32
+ *   rn_nvfp4_gated_ffn  the gated feed-forward block with W [2H, K] (gate
+ *                       rows, then linear rows); act, scales, mode and out as
+ *                       for rn_gated_ffn_fwd
+ * x bf16 [N, K] (dtype RN_BF16; RN_F32 returns RN_ERR_UNSUPPORTED).  The
+ * weights' values (without w_scale_inv) are exact in bf16, the sums are
+ * fp32.  K % 16 == 0, any N, R and H (MXFP8 output: H % 32 == 0); x, w_codes,
+ * w_scales and the output 16-byte aligned.  Made for N of one to a few tens,
+ * where the weights' bytes are the cost; larger N are valid, and read the
+ * weights once per group of tokens.  No workspace.
+ */
+rn_status rn_nvfp4_matvec(const void* x, rn_dtype dtype, const uint8_t* w_codes,
+                          const uint8_t* w_scales, const float* w_scale_inv, int64_t N, int64_t K,
+                          int64_t R, rn_dtype out_dtype, void* y, void* stream);
+
+rn_status rn_nvfp4_gated_ffn(rn_act act, const void* x, rn_dtype dtype, const uint8_t* w_codes,
+                             const uint8_t* w_scales, const float* w_scale_inv, const float* scales,
+                             int64_t N, int64_t K, int64_t H, float limit, float alpha,
+                             rn_quant_mode mode, const rn_output* out, void* stream);
 
 /*
  * Quantization stage alone on caller-given fp32 values y [N, H] (the

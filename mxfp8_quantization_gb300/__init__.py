@@ -22,7 +22,10 @@ PyTorch Ext Normalization" (section "Signature"):
 "mxfp8", "nvfp4"; the page's quantizer object becomes this string plus the
 scale.  ``scaled_act_fwd`` / ``scaled_act_bwd`` are the scaled SReLU, SwiGLU
 and clamped SwiGLU of the page "Activation + GroupedLinear Fusion for MOE
-and other MOE optimizations".
+and other MOE optimizations"; ``gated_ffn_fwd`` / ``gated_ffn_bwd`` are the
+gated feed-forward block around them (both projections, the activation and
+the product), ``nvfp4_matvec`` / ``nvfp4_gated_ffn`` the products of one or a
+few tokens with the NVFP4 weights that ``quantize_only`` makes.
 """
 from __future__ import annotations
 
@@ -38,6 +41,8 @@ __all__ = [
     "bwd_workspace_bytes", "device_error", "Fp8Output", "MXFP8Output", "NVFP4Output", "lib_path",
     "RNError",
     "QUANT_MODES", "ACTS", "scaled_act_fwd", "scaled_act_bwd",
+    "gated_ffn_fwd", "gated_ffn_bwd", "gated_ffn_bwd_workspace_bytes", "nvfp4_matvec",
+    "nvfp4_gated_ffn",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -96,13 +101,20 @@ def _load():
     lib.rn_scaled_act_fwd.argtypes = [i32, vp, i32, vp, i64, i64, f32, f32, i32, outp, vp]
     lib.rn_scaled_act_bwd.argtypes = [i32, vp, vp, i32, vp, i64, i64, f32, f32, vp, vp, vp]
     lib.rn_layernorm_bwd_noalloc.argtypes = [vp, vp, i32, vp, vp, vp, i64, i64, i32, i32, vp, vp, vp, vp]
+    lib.rn_gated_ffn_fwd.argtypes = [i32, vp, vp, i32, vp, i64, i64, i64, f32, f32, i32, outp, vp, vp]
+    lib.rn_gated_ffn_bwd.argtypes = [i32, vp, vp, vp, vp, i32, vp, i64, i64, i64, f32, f32, vp, vp, vp,
+                                     vp, szp, vp]
+    lib.rn_nvfp4_matvec.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, i32, vp, vp]
+    lib.rn_nvfp4_gated_ffn.argtypes = [i32, vp, i32, vp, vp, vp, vp, i64, i64, i64, f32, f32, i32,
+                                       outp, vp]
     lib.rn_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint)]
     lib.rn_status_str.argtypes = [i32]
     lib.rn_status_str.restype = ctypes.c_char_p
     for f in ("rn_layernorm_fwd", "rn_rmsnorm_fwd", "rn_layernorm_bwd", "rn_rmsnorm_bwd",
               "rn_quantize_only", "rn_device_error", "rn_abi_version", "rn_layernorm_bwd_noalloc",
               "rn_layernorm_add_fwd", "rn_rmsnorm_add_fwd", "rn_delayed_scaling_update",
-              "rn_scaled_act_fwd", "rn_scaled_act_bwd"):
+              "rn_scaled_act_fwd", "rn_scaled_act_bwd", "rn_gated_ffn_fwd", "rn_gated_ffn_bwd",
+              "rn_nvfp4_matvec", "rn_nvfp4_gated_ffn"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -364,6 +376,140 @@ def scaled_act_bwd(dy, x, act, scales=None, limit=7.0, alpha=1.702, dscales=True
                                float(limit), float(alpha), _ptr(dx), _ptr(ds), _stream())
     _check(st, "rn_scaled_act_bwd")
     return dx, ds
+
+
+def _gated(act):
+    if act not in ("swiglu", "clamped_swiglu"):
+        raise RNError(f"a gated block takes 'swiglu' or 'clamped_swiglu', got {act!r}")
+    return ACTS[act]
+
+
+def _matrix(t, name, dtype=torch.bfloat16):
+    _need(t, name, dtype)
+    if t.dim() != 2:
+        raise RNError(f"{name} must have 2 dimensions, got {t.dim()}")
+    return t.shape
+
+
+@dataclass
+class _Like:
+    """What ``_make_output`` reads of the tensor it makes an output for."""
+    shape: tuple
+    dtype: torch.dtype
+    device: torch.device
+
+
+def _make_rows_output(x, N, H, quant, out_dtype, scale):
+    """The output of a block with rows of H: ``x`` gives the device and the default dtype."""
+    if quant not in ("none", "fp8_delayed", "mxfp8"):
+        raise RNError(f"a gated block gives 'none', 'fp8_delayed' or 'mxfp8' output, got {quant!r}")
+    return _make_output(_Like((N, H), x.dtype, x.device), quant, out_dtype, scale, True, False)
+
+
+def gated_ffn_fwd(x, w, act="swiglu", scales=None, quant="none", limit=7.0, alpha=1.702, scale=None,
+                  out_dtype=None, save_pre=False):
+    """y = scales[:, None] * act(x @ w[:H].T, x @ w[H:].T): x bf16 [N, K], w bf16 [2H, K] (gate rows,
+    then linear rows), act "swiglu" or "clamped_swiglu" -> (output, pre); output per ``quant``
+    ("none", "fp8_delayed", "mxfp8" rowwise), pre the projections bf16 [N, 2H] for
+    ``gated_ffn_bwd``, or None without ``save_pre``."""
+    lib = _load()
+    code = _gated(act)
+    N, K = _matrix(x, "x")
+    R, _ = _matrix(w, "w")
+    if R % 2 or tuple(w.shape) != (R, K):
+        raise RNError(f"w must have shape (2 H, {K}), got {tuple(w.shape)}")
+    H = R // 2
+    if scales is not None:
+        _need(scales, "scales", torch.float32, (N,))
+    o, res = _make_rows_output(x, N, H, quant, out_dtype, scale)
+    pre = torch.empty((N, R), dtype=x.dtype, device=x.device) if save_pre else None
+    st = lib.rn_gated_ffn_fwd(code, _ptr(x), _ptr(w), _BF16, _ptr(scales), N, K, H, float(limit),
+                              float(alpha), QUANT_MODES[quant], ctypes.byref(o), _ptr(pre), _stream())
+    _check(st, "rn_gated_ffn_fwd")
+    return res, pre
+
+
+def gated_ffn_bwd_workspace_bytes(N, K, H) -> int:
+    """Workspace bytes ``gated_ffn_bwd`` needs (the query step of the protocol)."""
+    n = ctypes.c_size_t(0)
+    st = _load().rn_gated_ffn_bwd(ACTS["swiglu"], None, None, None, None, _BF16, None, N, K, H, 0.0, 0.0,
+                                  None, None, None, None, ctypes.byref(n), None)
+    _check(st, "workspace query")
+    return int(n.value)
+
+
+def gated_ffn_bwd(dy, x, w, pre, act="swiglu", scales=None, limit=7.0, alpha=1.702, dscales=True,
+                  workspace=None, need_dx=True, need_dw=True):
+    """Backward of ``gated_ffn_fwd`` at its ``pre``: dy bf16 [N, H] -> (dx bf16 [N, K] or None, dw
+    bf16 [2H, K] or None, dscales fp32 [N] or None); ``need_dx`` / ``need_dw`` / ``dscales`` select."""
+    lib = _load()
+    code = _gated(act)
+    N, K = _matrix(x, "x")
+    R, _ = _matrix(w, "w")
+    if R % 2 or tuple(w.shape) != (R, K):
+        raise RNError(f"w must have shape (2 H, {K}), got {tuple(w.shape)}")
+    H = R // 2
+    _need(dy, "dy", torch.bfloat16, (N, H))
+    _need(pre, "pre", torch.bfloat16, (N, R))
+    if scales is not None:
+        _need(scales, "scales", torch.float32, (N,))
+    need = gated_ffn_bwd_workspace_bytes(N, K, H)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+    else:
+        _need(workspace, "workspace")
+    n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
+    dx = torch.empty_like(x) if need_dx else None
+    dw = torch.empty_like(w) if need_dw else None
+    ds = torch.empty(N, dtype=torch.float32, device=x.device) if dscales else None
+    if dx is None and dw is None and ds is None:
+        raise RNError("nothing to compute: dx, dw and dscales are all skipped")
+    st = lib.rn_gated_ffn_bwd(code, _ptr(dy), _ptr(x), _ptr(w), _ptr(pre), _BF16, _ptr(scales), N, K, H,
+                              float(limit), float(alpha), _ptr(dx), _ptr(dw), _ptr(ds),
+                              _ptr(workspace), ctypes.byref(n), _stream())
+    _check(st, "rn_gated_ffn_bwd")
+    return dx, dw, ds
+
+
+def _nvfp4_weights(x, w):
+    N, K = _matrix(x, "x")
+    R, half = _matrix(w.data, "w.data", torch.uint8)
+    if K % 16 or half * 2 != K:
+        raise RNError(f"w must hold rows of {K} elements (a multiple of 16), got {2 * half}")
+    _need(w.row_scales, "w.row_scales", torch.uint8, (R, K // 16))
+    _need(w.scale_inv, "w.scale_inv", torch.float32, (1,))
+    return N, K, R
+
+
+def nvfp4_matvec(x, w, out_dtype=None):
+    """y = x @ W.T for one or a few tokens: x bf16 [N, K], w the ``NVFP4Output`` of a weight matrix
+    [R, K] -> y [N, R] in ``out_dtype`` (x's by default, or float32)."""
+    lib = _load()
+    N, K, R = _nvfp4_weights(x, w)
+    y = torch.empty((N, R), dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    st = lib.rn_nvfp4_matvec(_ptr(x), _BF16, _ptr(w.data), _ptr(w.row_scales), _ptr(w.scale_inv), N, K,
+                             R, _dtype_code(y), _ptr(y), _stream())
+    _check(st, "rn_nvfp4_matvec")
+    return y
+
+
+def nvfp4_gated_ffn(x, w, act="swiglu", scales=None, quant="none", limit=7.0, alpha=1.702, scale=None,
+                    out_dtype=None):
+    """``gated_ffn_fwd`` for one or a few tokens with NVFP4 weights: w the ``NVFP4Output`` of a
+    weight matrix [2H, K] (gate rows, then linear rows) -> output per ``quant``."""
+    lib = _load()
+    code = _gated(act)
+    N, K, R = _nvfp4_weights(x, w)
+    if R % 2:
+        raise RNError(f"w must have an even number of rows, got {R}")
+    if scales is not None:
+        _need(scales, "scales", torch.float32, (N,))
+    o, res = _make_rows_output(x, N, R // 2, quant, out_dtype, scale)
+    st = lib.rn_nvfp4_gated_ffn(code, _ptr(x), _BF16, _ptr(w.data), _ptr(w.row_scales),
+                                _ptr(w.scale_inv), _ptr(scales), N, K, R // 2, float(limit),
+                                float(alpha), QUANT_MODES[quant], ctypes.byref(o), _stream())
+    _check(st, "rn_nvfp4_gated_ffn")
+    return res
 
 
 def bwd_workspace_bytes(N, H, dtype, layernorm=True) -> int:

@@ -920,6 +920,195 @@ rn_status rn_scaled_act_bwd(rn_act act, const void* dy, const void* x, rn_dtype 
   return launch_act_bwd(act, dtype == RN_BF16, p, di.sms, static_cast<cudaStream_t>(stream));
 }
 
+// ------------------------------------------- gated feed-forward block
+// Output descriptor of the block's forward forms: NONE, FP8_DELAYED or
+// rowwise MXFP8 (N need not be a multiple of 32).
+static rn_status ffn_out(rn_quant_mode mode, const rn_output* out, int64_t N, int64_t H, int* kind) {
+  switch (mode) {
+    case RN_QUANT_NONE:
+    case RN_QUANT_FP8_DELAYED: {
+      const rn_status st = check_out(mode, out, N, H);
+      if (st != RN_OK) return st;
+      *kind = mode == RN_QUANT_FP8_DELAYED ? kFfnFp8 : (out->out_dtype == RN_F32 ? kFfnF32 : kFfnBf16);
+      return RN_OK;
+    }
+    case RN_QUANT_MXFP8:
+      if (out == nullptr) return RN_ERR_INVALID;
+      if (out->col_data != nullptr || out->col_scales != nullptr) return RN_ERR_UNSUPPORTED;
+      if (N > 0 && !out_fields_only(out, true, true, false, false, false, false, false, false))
+        return RN_ERR_INVALID;
+      if (H % 32 != 0 || (N > 0 && !aligned(out->data, 16))) return RN_ERR_UNSUPPORTED;
+      *kind = kFfnMx;
+      return RN_OK;
+    case RN_QUANT_FP8_CURRENT:  // both need amax before the first code
+    case RN_QUANT_NVFP4:
+      return RN_ERR_UNSUPPORTED;
+    default:
+      return RN_ERR_INVALID;
+  }
+}
+
+// sizes, dtype and activation parameters of the block's entry points
+static rn_status ffn_checks(rn_act act, rn_dtype dt, int64_t N, int64_t K, int64_t H, float limit,
+                            float alpha, const float* scales) {
+  if (act != RN_ACT_SRELU && act != RN_ACT_SWIGLU && act != RN_ACT_CLAMPED_SWIGLU)
+    return RN_ERR_INVALID;
+  if (!dtype_ok(dt) || N < 0 || K < 1 || H < 1 || N > INT32_MAX || K > INT32_MAX ||
+      H > INT32_MAX / 2)
+    return RN_ERR_INVALID;
+  if (act == RN_ACT_CLAMPED_SWIGLU && (!(limit >= 0.0f) || !(alpha == alpha) ||
+                                       alpha > 3.4e38f || alpha < -3.4e38f))
+    return RN_ERR_INVALID;
+  if (act == RN_ACT_SRELU || dt != RN_BF16 || (scales && !aligned(scales, 4)))
+    return RN_ERR_UNSUPPORTED;
+  return RN_OK;
+}
+
+rn_status rn_gated_ffn_fwd(rn_act act, const void* x, const void* w, rn_dtype dtype,
+                           const float* scales, int64_t N, int64_t K, int64_t H, float limit,
+                           float alpha, rn_quant_mode mode, const rn_output* out, void* pre,
+                           void* stream) {
+  rn_status st = ffn_checks(act, dtype, N, K, H, limit, alpha, scales);
+  if (st != RN_OK) return st;
+  if (N > 0 && (x == nullptr || w == nullptr)) return RN_ERR_INVALID;
+  int kind = 0;
+  if ((st = ffn_out(mode, out, N, H, &kind)) != RN_OK) return st;
+  if (K % 8 != 0 || H % 8 != 0 || !aligned(x, 16) || !aligned(w, 16) || !aligned(pre, 16))
+    return RN_ERR_UNSUPPORTED;
+  DeviceInfo di;
+  if ((st = device_info(&di)) != RN_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (kind == kFfnFp8 && (st = launch_fwd_init(out->amax, out->scale, out->scale_inv, s)) != RN_OK)
+    return st;
+  if (N == 0) return RN_OK;
+  FfnParams p{};
+  p.x = x;
+  p.w = w;
+  p.scales = scales;
+  p.out = out->data;
+  p.row_scales = kind == kFfnMx ? out->row_scales : nullptr;
+  p.scale = out->scale;
+  p.amax = out->amax;
+  p.pre = pre;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.H = (int)H;
+  p.limit = limit;
+  p.alpha = alpha;
+  p.mode = kind;
+  return launch_ffn_fwd(act, p, di.sms, s);
+}
+
+rn_status rn_gated_ffn_bwd(rn_act act, const void* dy, const void* x, const void* w, const void* pre,
+                           rn_dtype dtype, const float* scales, int64_t N, int64_t K, int64_t H,
+                           float limit, float alpha, void* dx, void* dw, float* dscales,
+                           void* workspace, size_t* workspace_bytes, void* stream) {
+  rn_status st = ffn_checks(act, dtype, N, K, H, limit, alpha, scales);
+  if (st != RN_OK) return st;
+  if (K % 8 != 0 || H % 8 != 0) return RN_ERR_UNSUPPORTED;
+  const size_t need = (size_t)N * (size_t)H * 4;
+  if (workspace == nullptr && (dx == nullptr && dw == nullptr && dscales == nullptr)) {
+    if (workspace_bytes == nullptr) return RN_ERR_INVALID;
+    *workspace_bytes = need;
+    return RN_OK;
+  }
+  if (N > 0 && (dy == nullptr || pre == nullptr || (dx && w == nullptr) || (dw && x == nullptr)))
+    return RN_ERR_INVALID;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(pre, 16) ||
+      !aligned(dx, 16) || !aligned(dw, 16) || !aligned(dscales, 4) || !aligned(workspace, 16))
+    return RN_ERR_UNSUPPORTED;
+  if (N > 0 && (workspace == nullptr || workspace_bytes == nullptr || *workspace_bytes < need))
+    return RN_ERR_WORKSPACE;
+  DeviceInfo di;
+  if ((st = device_info(&di)) != RN_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0) {
+    if (dw && cudaMemsetAsync(dw, 0, (size_t)H * (size_t)K * 4, s) != cudaSuccess) return RN_ERR_CUDA;
+    return RN_OK;
+  }
+  ActParams a{};
+  a.x = pre;
+  a.dy = dy;
+  a.out = workspace;
+  a.scales = scales;
+  a.dscales = dscales;
+  a.N = (int)N;
+  a.H = (int)H;
+  a.limit = limit;
+  a.alpha = alpha;
+  if ((st = launch_act_bwd(act, true, a, di.sms, s)) != RN_OK) return st;
+  FfnBwdParams p{};
+  p.dp = workspace;
+  p.x = x;
+  p.w = w;
+  p.dx = dx;
+  p.dw = dw;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.H = (int)H;
+  return launch_ffn_bwd(p, di.sms, s);
+}
+
+static rn_status nvfp4_common(int act, const void* x, const uint8_t* w_codes, const uint8_t* w_scales,
+                              const float* w_scale_inv, const float* scales, int64_t N, int64_t K,
+                              int64_t H, float limit, float alpha, int kind, const rn_output* out,
+                              cudaStream_t s) {
+  if (w_scale_inv == nullptr || (N > 0 && (x == nullptr || w_codes == nullptr || w_scales == nullptr)))
+    return RN_ERR_INVALID;
+  if (K % 16 != 0 || !aligned(x, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 16) ||
+      !aligned(w_scale_inv, 4))
+    return RN_ERR_UNSUPPORTED;
+  DeviceInfo di;
+  rn_status st;
+  if ((st = device_info(&di)) != RN_OK) return st;
+  if (kind == kFfnFp8 && (st = launch_fwd_init(out->amax, out->scale, out->scale_inv, s)) != RN_OK)
+    return st;
+  if (N == 0) return RN_OK;
+  MvParams p{};
+  p.x = x;
+  p.codes = w_codes;
+  p.blocks = w_scales;
+  p.scale_inv = w_scale_inv;
+  p.scales = scales;
+  p.out = out->data;
+  p.row_scales = kind == kFfnMx ? out->row_scales : nullptr;
+  p.scale = out->scale;
+  p.amax = out->amax;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.H = (int)H;
+  p.limit = limit;
+  p.alpha = alpha;
+  p.mode = kind;
+  return launch_nvfp4_mv(act, p, di.sms, s);
+}
+
+rn_status rn_nvfp4_matvec(const void* x, rn_dtype dtype, const uint8_t* w_codes,
+                          const uint8_t* w_scales, const float* w_scale_inv, int64_t N, int64_t K,
+                          int64_t R, rn_dtype out_dtype, void* y, void* stream) {
+  rn_output out{};
+  out.data = y;
+  out.out_dtype = out_dtype;
+  int kind = 0;
+  rn_status st = ffn_checks(RN_ACT_SWIGLU, dtype, N, K, R, 0.0f, 0.0f, nullptr);
+  if (st != RN_OK) return st;
+  if ((st = ffn_out(RN_QUANT_NONE, &out, N, R, &kind)) != RN_OK) return st;
+  return nvfp4_common(kActNone, x, w_codes, w_scales, w_scale_inv, nullptr, N, K, R, 0.0f, 0.0f,
+                      kind, &out, static_cast<cudaStream_t>(stream));
+}
+
+rn_status rn_nvfp4_gated_ffn(rn_act act, const void* x, rn_dtype dtype, const uint8_t* w_codes,
+                             const uint8_t* w_scales, const float* w_scale_inv, const float* scales,
+                             int64_t N, int64_t K, int64_t H, float limit, float alpha,
+                             rn_quant_mode mode, const rn_output* out, void* stream) {
+  rn_status st = ffn_checks(act, dtype, N, K, H, limit, alpha, scales);
+  if (st != RN_OK) return st;
+  int kind = 0;
+  if ((st = ffn_out(mode, out, N, H, &kind)) != RN_OK) return st;
+  return nvfp4_common(act, x, w_codes, w_scales, w_scale_inv, scales, N, K, H, limit, alpha, kind,
+                      out, static_cast<cudaStream_t>(stream));
+}
+
 const char* rn_status_str(rn_status s) {
   switch (s) {
     case RN_OK: return "ok";

@@ -119,6 +119,49 @@ struct ActParams {
   int out_f32;            // forward NONE: fp32 output
 };
 
+// gated feed-forward block and the NVFP4 products
+constexpr int kActNone = -1;  // rn_nvfp4_matvec: no activation
+
+enum FfnOut : int { kFfnBf16 = 0, kFfnF32 = 1, kFfnFp8 = 2, kFfnMx = 3 };
+
+struct FfnParams {
+  const void* x;          // bf16 [N, K]
+  const void* w;          // bf16 [2H, K]: H gate rows, H linear rows
+  const float* scales;    // [N] or NULL
+  void* out;              // [N, H]: bf16, fp32 or E4M3 codes
+  uint8_t* row_scales;    // kFfnMx: E8M0 [N, H/32]
+  const float* scale;     // kFfnFp8
+  float* amax;            // kFfnFp8
+  void* pre;              // bf16 [N, 2H] or NULL
+  int N, K, H;
+  float limit, alpha;
+  int mode;               // FfnOut
+};
+
+struct FfnBwdParams {
+  const void* dp;         // bf16 [N, 2H], workspace
+  const void* x;          // bf16 [N, K]
+  const void* w;          // bf16 [2H, K]
+  void* dx;               // bf16 [N, K] or NULL
+  void* dw;               // bf16 [2H, K] or NULL
+  int N, K, H;
+};
+
+struct MvParams {
+  const void* x;          // bf16 [N, K]
+  const uint8_t* codes;   // E2M1 pairs [R, K/2]; R = H, or 2H with an activation
+  const uint8_t* blocks;  // E4M3 scales [R, K/16]
+  const float* scale_inv; // 1 / S
+  const float* scales;    // [N] or NULL
+  void* out;              // [N, H]
+  uint8_t* row_scales;    // kFfnMx
+  const float* scale;     // kFfnFp8
+  float* amax;            // kFfnFp8
+  int N, K, H;
+  float limit, alpha;
+  int mode;               // FfnOut
+};
+
 // launch shape shared by the persistent kernels
 struct Launch {
   int work;             // independent work items (tiles / chunks): grid upper bound
@@ -196,6 +239,12 @@ rn_status launch_colreduce(const ColReduceParams& p, cudaStream_t s);
 rn_status launch_act_fwd(int act, bool bf16, int qmode, const ActParams& p, int sms, bool pdl,
                          cudaStream_t s);
 rn_status launch_act_bwd(int act, bool bf16, const ActParams& p, int sms, cudaStream_t s);
+
+// gated feed-forward block; sms: SMs of the device
+rn_status launch_ffn_fwd(int act, const FfnParams& p, int sms, cudaStream_t s);
+rn_status launch_ffn_bwd(const FfnBwdParams& p, int sms, cudaStream_t s);
+// products with NVFP4 weights (act kActNone: R = H rows, no activation)
+rn_status launch_nvfp4_mv(int act, const MvParams& p, int sms, cudaStream_t s);
 
 // delayed-scaling history step (one CTA; 1 <= L <= kMaxHistory)
 constexpr int kMaxHistory = 1024;

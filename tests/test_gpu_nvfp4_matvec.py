@@ -1,0 +1,214 @@
+"""GPU parity of the products with NVFP4 weights (rn_nvfp4_matvec,
+rn_nvfp4_gated_ffn) against the oracle; the bounds are derived in
+ffn_check.py.  The sums run over E2M1 value * block scale (exact in bf16),
+so 1/S multiplies their bound, and one more rounding of fp32 is added."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import mxfp8_quantization_gb300 as rn
+from ffn_check import ALPHA, LIM, check_codes, check_mx, check_value, ep_bound, y_bound
+from oracle import ffn as F
+from test_gpu_ffn import MODES, f64, np_scales
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    yield
+    assert rn.device_error() == 0
+
+
+def weights(R, K, seed=0, std=2.0):
+    g = torch.Generator().manual_seed(seed)
+    w = torch.randn(R, K, generator=g) * (std / K ** 0.5)
+    return rn.quantize_only(w.cuda(), "nvfp4")
+
+
+def tokens(N, K, seed=0):
+    return torch.randn(N, K, generator=torch.Generator().manual_seed(seed + 100)).bfloat16().cuda()
+
+
+def values(w):
+    return F.nvfp4_values(w.data.cpu().numpy(), w.row_scales.cpu().numpy(), w.scale_inv.cpu().numpy()[0])
+
+
+def proj(x, w):
+    x64, v = f64(x), values(w)
+    p = x64 @ v.T
+    return p, ep_bound(x64, v) + 2.0 ** -23 * np.abs(p)
+
+
+# (N, K, R): K of one block, of an odd number of blocks, across every split; R odd; tokens across groups of 8
+SIZES = [(1, 16, 1), (1, 32, 7), (1, 48, 33), (1, 4096, 64), (1, 2064, 250), (2, 4112, 65), (3, 16384, 17),
+         (4, 128, 513), (7, 1040, 64), (8, 2048, 100), (9, 512, 96), (13, 5136, 40), (16, 256, 31),
+         (17, 1024, 64), (24, 144, 130), (32, 8192, 24), (33, 96, 48), (40, 2080, 66), (100, 1024, 72),
+         (1, 1024, 20000)]
+
+
+@pytest.mark.parametrize("i,size", list(enumerate(SIZES)), ids=lambda v: str(v))
+def test_matvec(i, size):
+    N, K, R = size
+    x, w = tokens(N, K, i), weights(R, K, i)
+    dt = (torch.bfloat16, torch.float32)[i % 2]
+    y = rn.nvfp4_matvec(x, w, out_dtype=dt)
+    p, ep = proj(x, w)
+    assert y.dtype == dt
+    check_value(f64(y), p, ep, dt == torch.bfloat16, "y")
+
+
+@pytest.mark.parametrize("i,size", list(enumerate(SIZES)), ids=lambda v: str(v))
+def test_gated(i, size):
+    N, K, H = size
+    mode = MODES[i % 4]
+    if mode == "mxfp8":
+        H = (H + 31) // 32 * 32
+    _check_gated(N, K, H, ("swiglu", "clamped_swiglu")[(i // 4) % 2], i % 3 == 0, mode, i)
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("act", ["swiglu", "clamped_swiglu"])
+@pytest.mark.parametrize("N,K,H", [(1, 144, 160), (12, 1040, 32)])
+def test_gated_modes(mode, act, N, K, H):
+    _check_gated(N, K, H, act, True, mode, 3)
+
+
+def _check_gated(N, K, H, act, scaled, mode, seed):
+    x, w = tokens(N, K, seed), weights(2 * H, K, seed)
+    s = torch.rand(N, generator=torch.Generator().manual_seed(seed)).cuda() if scaled else None
+    quant = "none" if mode in ("bf16", "f32") else mode
+    out = rn.nvfp4_gated_ffn(x, w, act, s, quant=quant, limit=LIM, alpha=ALPHA,
+                             scale=3.5 if mode == "fp8_delayed" else None,
+                             out_dtype=torch.float32 if mode == "f32" else None)
+    p, ep = proj(x, w)
+    ref = F._act.scaled_act_fwd(p, np_scales(s), act, limit=LIM, alpha=ALPHA)["y"]
+    err = y_bound(p, ep, np_scales(s), act)
+    if mode in ("bf16", "f32"):
+        check_value(f64(out), ref, err, mode == "bf16", "y")
+    elif mode == "fp8_delayed":
+        check_codes(out.data.cpu().numpy(), ref, err, 3.5, "y")
+        assert abs(float(out.amax) - np.max(np.abs(ref))) <= np.max(err) + 2.0 ** -23 * np.max(np.abs(ref))
+        assert float(out.scale_inv) == np.float32(1) / np.float32(3.5)
+    else:
+        check_mx(out.data.cpu().numpy(), out.row_scales.cpu().numpy(), ref, err, "y")
+
+
+def test_every_code_and_scale():
+    """Each E2M1 code under each finite E4M3 scale, subnormal and negative ones too, times powers of two
+    of x that put a single term in the sum: exact."""
+    R, K = 16, 256
+    codes = np.zeros((R, K), np.uint8)
+    codes[np.arange(R), :] = np.arange(R)[:, None]          # row r: code r everywhere
+    blocks = np.array([c for c in range(256) if c & 0x7F != 0x7F], np.uint8)
+    packed = torch.from_numpy(codes[:, 0::2] | codes[:, 1::2] << 4).cuda()
+    si = torch.full((1,), 0.125, device="cuda")
+    for b0 in range(0, len(blocks), 16):
+        b = np.resize(blocks[b0:b0 + 16], 16)
+        bs = np.tile(b, (R, 1))
+        w = rn.NVFP4Output(packed, torch.from_numpy(bs).cuda(), si * 0 + 8, si, si)
+        for k in (0, 1, 15):                                 # one element of each block
+            x = torch.zeros(16, K)
+            x[np.arange(16), np.arange(16) * 16 + k] = 2.0 ** torch.arange(-8, 8).float()
+            x = x.bfloat16().cuda()
+            y = rn.nvfp4_matvec(x, w, out_dtype=torch.float32)
+            assert np.array_equal(f64(y), f64(x) @ F.nvfp4_values(packed.cpu().numpy(), bs, 0.125).T)
+
+
+def test_wide_range_of_inputs():
+    """Activations near bf16's ends keep their products: 2**100 and 2**-100 beside ones whose weight is 0."""
+    K, R = 512, 40
+    w = weights(R, K, 9)
+    w.data[:, :8] = 0                                        # the first block's weights are 0
+    x = tokens(2, K, 9)
+    x[0] *= 2.0 ** -100
+    x[1] *= 2.0 ** 100
+    x[:, :16] = 2.0 ** 110
+    p, ep = proj(x, w)
+    ep = ep_bound(np.where(np.arange(K) < 16, 0, f64(x)), values(w)) + 2.0 ** -23 * np.abs(p)
+    y = rn.nvfp4_matvec(x, w, out_dtype=torch.float32)
+    check_value(f64(y), p, ep, False, "y")
+
+
+def test_non_finite_rows_stay_in_their_rows():
+    x, w = tokens(11, 1040, 1), weights(96, 1040, 1)
+    clean = rn.nvfp4_matvec(x, w)
+    bad = x.clone()
+    bad[3, 7], bad[9, 1] = float("nan"), float("inf")
+    y = rn.nvfp4_matvec(bad, w)
+    keep = [i for i in range(11) if i not in (3, 9)]
+    assert torch.equal(y[keep], clean[keep]) and torch.isnan(y[3]).all()
+    assert not torch.isfinite(y[9].float()).any()
+
+
+def test_empty_batch():
+    w = weights(64, 32)
+    x = torch.empty(0, 32, device="cuda", dtype=torch.bfloat16)
+    assert rn.nvfp4_matvec(x, w).shape == (0, 64)
+    o = rn.nvfp4_gated_ffn(x, w, quant="fp8_delayed", scale=4.0)
+    assert float(o.amax) == 0.0 and float(o.scale_inv) == 0.25
+
+
+@pytest.mark.parametrize("N,R", [(1, 33), (9, 250)])
+def test_nothing_is_written_behind_the_output(N, R):
+    lib = rn._load()
+    x, w = tokens(N, 272, 2), weights(R, 272, 2)
+    y = torch.full((N * R + 64,), -7.75, dtype=torch.float32, device="cuda")
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    assert lib.rn_nvfp4_matvec(p(x), 0, p(w.data), p(w.row_scales), p(w.scale_inv), N, 272, R, 1, p(y),
+                               ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+    assert torch.all(y[N * R:] == -7.75)
+    assert torch.equal(y[:N * R].view(N, R), rn.nvfp4_matvec(x, w, out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("N,K,H", [(1, 1040, 96), (13, 528, 200)])
+def test_repeats_and_replays(N, K, H):
+    x, w = tokens(N, K), weights(2 * H, K)
+    want = rn.nvfp4_matvec(x, w), rn.nvfp4_gated_ffn(x, w)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for st in streams * 3:
+        with torch.cuda.stream(st):
+            got.append((rn.nvfp4_matvec(x, w), rn.nvfp4_gated_ffn(x, w)))
+    torch.cuda.synchronize()
+    for g in got:
+        assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = rn.nvfp4_matvec(x, w), rn.nvfp4_gated_ffn(x, w)
+    x.copy_(tokens(N, K, 5))
+    graph.replay()
+    want = rn.nvfp4_matvec(x, w), rn.nvfp4_gated_ffn(x, w)
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_generation_step_together():
+    """RMSNorm -> gated block -> down projection on NVFP4 weights, as one token is generated; the block
+    with bf16 weights of the same values gives the same result within both bounds."""
+    C, H = 512, 1056
+    x = tokens(1, C, 3)
+    gamma = torch.ones(C, device="cuda")
+    up, down = weights(2 * H, C, 4), weights(C, H, 5)
+    h, _ = rn.rmsnorm_fwd(x, gamma, 1e-5)
+    y = rn.nvfp4_gated_ffn(h, up)
+    z = rn.nvfp4_matvec(y, down)
+    p, ep = proj(h, up)
+    err = y_bound(p, ep, None, "swiglu")
+    check_value(f64(y), F._act.act_value(p, "swiglu"), err, True, "y")
+    pz, ez = proj(y, down)
+    check_value(f64(z), pz, ez, True, "z")
+    # values of the codes times S are exact in bf16; S back in through the activations' own bound
+    one = rn.NVFP4Output(up.data, up.row_scales, up.scale, torch.ones(1, device="cuda"), up.amax)
+    wide = torch.from_numpy(values(one)).bfloat16().cuda()
+    hs = (h.float() * 2.0 ** -12).bfloat16()                     # keeps the projections small; exact
+    a = rn.nvfp4_gated_ffn(hs, one, out_dtype=torch.float32)
+    b, _ = rn.gated_ffn_fwd(hs, wide, out_dtype=torch.float32)
+    p, ep = proj(hs, one)
+    err = y_bound(p, ep, None, "swiglu")
+    ref = F._act.act_value(p, "swiglu")
+    check_value(f64(a), ref, err, False, "nvfp4")
+    check_value(f64(b), ref, err, False, "bf16")
