@@ -1131,7 +1131,9 @@ rn_status rn_device_error(unsigned int* code) {
   if (a == 0) a = a2;
   if ((st = read_clear_error_mx(&b)) != RN_OK) return st;
   if ((st = read_clear_error_bwd(&c)) != RN_OK) return st;
-  *code = a ? a : (b ? b : c);
+  unsigned d = 0;
+  if ((st = read_clear_error_ffn(&d)) != RN_OK) return st;
+  *code = a ? a : (b ? b : (c ? c : d));
   return RN_OK;
 }
 

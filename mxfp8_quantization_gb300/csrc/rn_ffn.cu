@@ -2,133 +2,440 @@
 // and the gradients of the input and the weights (backward).
 //
 //   forward   p = x W^T [N, 2H] = [a | b],  y = s_i act(a, b)
-//   backward  dp = s_i dy act'(pre) (rounded to bf16), dx = dp W,
+//   backward  dp = s_i dy act'(pre) (rounded to bf16, rn_act.cu), dx = dp W,
 //             dW = dp^T x
+//
+// Every product runs on the tensor cores (tcgen05, bf16 operands, fp32
+// accumulators in tensor memory) in one persistent kernel: a cluster of two
+// CTAs works on tiles of 256 x 256 of the result, the reduction in slices of
+// 64.  Each CTA loads its 128 rows of A and its 128 columns of B of a slice
+// by tensor copies (128-byte swizzle, zeros past the ends) into a ring of
+// kStages slots; one thread of the leader CTA issues the products of the
+// pair (M = 256, N = 256, K = 16), which read both CTAs' shared memory and
+// leave 128 rows of the tile in each CTA's tensor memory.  Two accumulators of
+// 256 columns alternate, so that the four epilogue warps of each CTA work on
+// one tile while the next is being summed.
+//
+// Forward tiles hold 128 gate and 128 linear columns: the leader's B is 128
+// gate rows of W, the other CTA's the 128 linear rows that belong to them, so
+// a and b of an output stand in the same lane of tensor memory, 128 columns
+// apart, and the activation needs no exchange.  A thread owns one row of the
+// tile: an MXFP8 block is 32 columns of one thread.
+//
+// Operands are read as they lie: reduction-major ("K-major", x and W in the
+// forward, dp in dx) or the other way ("MN-major", W in dx, dp and x in dW).
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "rn_act_math.cuh"
 #include "rn_device.cuh"
 #include "rn_internal.h"
+#include "rn_tc.cuh"
 
 namespace rn {
 namespace {
 
-__device__ __forceinline__ float bf16_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ unsigned g_err_ffn;
 
-constexpr int kTileRows = 8;  // one warp a row
+constexpr int kStages = 6;
+constexpr int kOperandBytes = 16384;              // 128 x 64 bf16
+constexpr int kStageBytes = 2 * kOperandBytes;    // A and B of one CTA
+constexpr int kThreads = 192;                     // copies, products, 4 epilogue warps
+constexpr size_t kSmemBytes = (size_t)kStages * kStageBytes + 1024;
 
-// One output per thread; a warp holds 32 columns of one row, so an MXFP8
-// block is a warp.
-template <int ACT>
-__global__ void __launch_bounds__(32 * kTileRows) rn_ffn_fwd_kernel(const FfnParams p) {
-  __shared__ float sx[kTileRows][33], sa[32][33], sb[32][33];
-  const int lane = threadIdx.x, ty = threadIdx.y;
-  const int64_t row = (int64_t)blockIdx.y * kTileRows + ty;
-  const int col = (int)blockIdx.x * 32 + lane;
-  const uint16_t* x = static_cast<const uint16_t*>(p.x);
-  const uint16_t* w = static_cast<const uint16_t*>(p.w);
-  float a = 0.0f, b = 0.0f;
-  for (int k0 = 0; k0 < p.K; k0 += 32) {
-    const int k = k0 + lane;
-    sx[ty][lane] = (row < p.N && k < p.K) ? bf16_f32(x[row * p.K + k]) : 0.0f;
-    for (int r = ty; r < 32; r += kTileRows) {
-      const int c = (int)blockIdx.x * 32 + r;
-      const bool ok = c < p.H && k < p.K;
-      sa[r][lane] = ok ? bf16_f32(w[(int64_t)c * p.K + k]) : 0.0f;
-      sb[r][lane] = ok ? bf16_f32(w[((int64_t)p.H + c) * p.K + k]) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll 8
-    for (int q = 0; q < 32; ++q) {
-      a = fmaf(sx[ty][q], sa[lane][q], a);
-      b = fmaf(sx[ty][q], sb[lane][q], b);
-    }
-    __syncthreads();
+// one product of the launch: tiles of 256 x 256 (forward: 256 x 128 outputs)
+struct Job {
+  int tiles_m, tiles_n;
+  int slices;            // of 64 along the reduction
+  bool a_mn, b_mn;
+  void* out;             // dx / dW: bf16 [rows, cols]
+  int rows, cols;
+};
+
+struct GemmParams {
+  Job job[2];
+  int n_jobs;
+  FfnParams f;           // forward
+};
+
+struct Maps {
+  CUtensorMap a[2], b[2];
+};
+
+struct Tile {
+  int job, m, n;
+};
+
+// Tiles in order of their index: jobs one after another, within a job bands
+// of 8 tiles of rows walked along the columns, so that the clusters that run
+// together share operands in L2.
+__device__ __forceinline__ Tile tile_at(const GemmParams& p, int t) {
+  Tile r;
+  r.job = 0;
+  const int n0 = p.job[0].tiles_m * p.job[0].tiles_n;
+  if (t >= n0) {
+    r.job = 1;
+    t -= n0;
   }
-  const bool ok = row < p.N && col < p.H;
-  float y = 0.0f;
-  if (ok) {
-    y = act_value<ACT>(a, b, p.limit, p.alpha) * (p.scales ? p.scales[row] : 1.0f);
-    if (p.pre) {
-      uint16_t* pre = static_cast<uint16_t*>(p.pre) + row * 2 * p.H;
-      const uint32_t v = pack_bf16x2(a, b);
-      pre[col] = (uint16_t)v;
-      pre[p.H + col] = (uint16_t)(v >> 16);
-    }
+  const Job& j = p.job[r.job];
+  const int band = t / (8 * j.tiles_n);
+  const int rest = t - band * 8 * j.tiles_n;
+  const int h = min(8, j.tiles_m - band * 8);
+  r.n = rest / h;
+  r.m = band * 8 + rest - r.n * h;
+  return r;
+}
+
+// 8 columns of one row; `o` is 16-byte aligned
+__device__ __forceinline__ void store8_bf16(void* o, const float* v) {
+  *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// 32 outputs (columns c .. c + 31, of which those below p.H exist) of a row
+template <int ACT, int MODE>
+__device__ __forceinline__ void epilogue32(const FfnParams& p, int64_t row, int c, const float* a,
+                                           const float* b, float s, float fp8_scale, float& amax) {
+  if (p.pre != nullptr) {
+    uint16_t* pre = static_cast<uint16_t*>(p.pre) + row * 2 * p.H + c;
+#pragma unroll
+    for (int q = 0; q < 32; q += 8)
+      if (c + q < p.H) {
+        store8_bf16(pre + q, a + q);
+        store8_bf16(pre + p.H + q, b + q);
+      }
   }
-  const int64_t o = row * p.H + col;
-  if (p.mode == kFfnMx) {
-    const float m = warp_max_nan(fabsf(y));
-    if (ok) {
+  float y[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) y[i] = act_value<ACT>(a[i], b[i], p.limit, p.alpha) * s;
+  const int64_t o = row * p.H + c;
+  if constexpr (MODE == kFfnBf16) {
+#pragma unroll
+    for (int q = 0; q < 32; q += 8)
+      if (c + q < p.H) store8_bf16(static_cast<uint16_t*>(p.out) + o + q, y + q);
+  } else if constexpr (MODE == kFfnF32) {
+#pragma unroll
+    for (int q = 0; q < 32; q += 4)
+      if (c + q < p.H)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o + q) =
+            make_float4(y[q], y[q + 1], y[q + 2], y[q + 3]);
+  } else {
+    float scale = fp8_scale;
+    if constexpr (MODE == kFfnMx) {
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) m = amax_acc2(m, make_float2(y[i], y[i + 1]));
       const uint32_t code = e8m0_code(m);
-      static_cast<uint8_t*>(p.out)[o] = (uint8_t)pack_e4m3x2(y * e8m0_inv_scale(code), 0.0f);
-      if (lane == 0) p.row_scales[row * (p.H / 32) + col / 32] = (uint8_t)code;
+      scale = e8m0_inv_scale(code);
+      p.row_scales[row * (p.H / 32) + c / 32] = (uint8_t)code;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; i += 2)
+        if (c + i < p.H) amax = amax_acc2(amax, make_float2(y[i], y[i + 1]));
     }
-  } else if (p.mode == kFfnFp8) {
-    const float m = warp_max_nan(fabsf(y));
+#pragma unroll
+    for (int q = 0; q < 32; q += 8)
+      if (c + q < p.H) {
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float* v = y + q + 4 * h;
+          const float2 lo = mul2(make_float2(v[0], v[1]), splat2(scale));
+          const float2 hi = mul2(make_float2(v[2], v[3]), splat2(scale));
+          w[h] = pack_e4m3x4(lo.x, lo.y, hi.x, hi.y);
+        }
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + o + q) = make_uint2(w[0], w[1]);
+      }
+  }
+}
+
+// ACT kActNone: the products of the backward, stored as they are
+template <int ACT, int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    rn_ffn_kernel(const GemmParams p, const __grid_constant__ Maps maps) {
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t full_b[kStages], empty_b[kStages], done_b[2], free_b[2];
+  __shared__ uint32_t tmem_at;
+  const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int cluster = (int)(blockIdx.x >> 1), n_clusters = (int)(gridDim.x >> 1);
+  int total = 0;
+  for (int j = 0; j < p.n_jobs; ++j) total += p.job[j].tiles_m * p.job[j].tiles_n;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&full_b[s]), 1);    // the leader's own arrival, with the bytes of both CTAs
+      mbar_init(smem_u32(&empty_b[s]), 1);   // the products that read the slot
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&done_b[i]), 1);    // the products of a tile
+      mbar_init(smem_u32(&free_b[i]), 8);    // the epilogue warps of both CTAs
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc_all(smem_u32(&tmem_at));
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at;
+
+  bool ok = true;
+  if (warp == 0) {
     if (lane == 0) {
-      pdl_wait();
-      atomicMax(reinterpret_cast<unsigned*>(p.amax), abs_bits(m));
+      RingPos r{0, 0};
+      for (int t = cluster; t < total && ok; t += n_clusters) {
+        const Tile tl = tile_at(p, t);
+        const Job& j = p.job[tl.job];
+        const CUtensorMap* ma = &maps.a[tl.job];
+        const CUtensorMap* mb = &maps.b[tl.job];
+        const int m0 = tl.m * 256 + (int)rank * 128;
+        const int n0 = ACT == kActNone ? tl.n * 256 + (int)rank * 128
+                                       : tl.n * 128 + (int)rank * p.f.H;
+        for (int k = 0; k < j.slices; ++k) {
+          if (!mbar_wait(smem_u32(&empty_b[r.slot]), r.phase ^ 1u, &g_err_ffn, kErrEmptyWait)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = map_to_rank(smem_u32(&full_b[r.slot]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_b[r.slot]), 2 * kStageBytes);
+          const uint32_t sa = ring + r.slot * kStageBytes, sb = sa + kOperandBytes;
+          if (j.a_mn) {
+            tma_load_2d(sa, ma, m0, k * 64, bar);
+            tma_load_2d(sa + kOperandBytes / 2, ma, m0 + 64, k * 64, bar);
+          } else {
+            tma_load_2d(sa, ma, k * 64, m0, bar);
+          }
+          if (j.b_mn) {
+            tma_load_2d(sb, mb, n0, k * 64, bar);
+            tma_load_2d(sb + kOperandBytes / 2, mb, n0 + 64, k * 64, bar);
+          } else {
+            tma_load_2d(sb, mb, k * 64, n0, bar);
+          }
+          r.advance(1, kStages);
+        }
+      }
     }
-    if (ok) static_cast<uint8_t*>(p.out)[o] = (uint8_t)pack_e4m3x2(y * *p.scale, 0.0f);
-  } else if (ok) {
-    if (p.mode == kFfnF32)
-      static_cast<float*>(p.out)[o] = y;
-    else
-      static_cast<uint16_t*>(p.out)[o] = (uint16_t)pack_bf16x2(y, 0.0f);
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      RingPos r{0, 0};
+      int it = 0;
+      for (int t = cluster; t < total && ok; t += n_clusters, ++it) {
+        const Job& j = p.job[tile_at(p, t).job];
+        const uint32_t acc = it & 1;
+        const uint32_t idesc =
+            kIdesc256 | (j.a_mn ? kIdescAMN : 0u) | (j.b_mn ? kIdescBMN : 0u);
+        const uint64_t da = smem_desc_step(j.a_mn), db = smem_desc_step(j.b_mn);
+        if (!mbar_wait(smem_u32(&free_b[acc]), ((it >> 1) & 1) ^ 1u, &g_err_ffn, kErrReadyWait)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int k = 0; k < j.slices; ++k) {
+          if (!mbar_wait(smem_u32(&full_b[r.slot]), r.phase, &g_err_ffn, kErrFullWait)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = ring + r.slot * kStageBytes;
+          uint64_t a = smem_desc(sa, j.a_mn), b = smem_desc(sa + kOperandBytes, j.b_mn);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            mma_bf16_pair(tmem + acc * 256, a, b, idesc, k > 0 || q > 0);
+            a += da;
+            b += db;
+          }
+          mma_commit_pair(smem_u32(&empty_b[r.slot]));
+          r.advance(1, kStages);
+        }
+        if (ok) mma_commit_pair(smem_u32(&done_b[acc]));
+      }
+    }
+  } else {
+    // epilogue warp: lanes 32 (warp % 4) .. + 31 of tensor memory
+    const int lb = (warp & 3) * 32;
+    float amax = 0.0f, fp8_scale = 1.0f;
+    if constexpr (MODE == kFfnFp8) fp8_scale = *p.f.scale;
+    int it = 0;
+    for (int t = cluster; t < total && ok; t += n_clusters, ++it) {
+      const Tile tl = tile_at(p, t);
+      const Job& j = p.job[tl.job];
+      const uint32_t acc = it & 1;
+      if (!mbar_wait(smem_u32(&done_b[acc]), (it >> 1) & 1, &g_err_ffn, kErrStatsWait)) ok = false;
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const int64_t row = (int64_t)tl.m * 256 + rank * 128 + lb + lane;
+      const uint32_t ta = tmem + acc * 256 + ((uint32_t)lb << 16);
+      if constexpr (ACT == kActNone) {
+        const int c0 = tl.n * 256;
+        for (int c = 0; c < 256; c += 32) {
+          if (c0 + c >= j.cols) break;
+          float v[32];
+          tmem_load32(ta + c, v);
+          tmem_load_wait();
+          if (row < j.rows) {
+            uint16_t* o = static_cast<uint16_t*>(j.out) + row * j.cols + c0 + c;
+#pragma unroll
+            for (int q = 0; q < 32; q += 8)
+              if (c0 + c + q < j.cols) store8_bf16(o + q, v + q);
+          }
+        }
+      } else {
+        const int c0 = tl.n * 128;
+        const float s = (p.f.scales != nullptr && row < p.f.N) ? __ldg(p.f.scales + row) : 1.0f;
+        for (int c = 0; c < 128; c += 32) {
+          if (c0 + c >= p.f.H) break;
+          float a[32], b[32];
+          tmem_load32(ta + c, a);
+          tmem_load32(ta + 128 + c, b);
+          tmem_load_wait();
+          if (row < p.f.N) epilogue32<ACT, MODE>(p.f, row, c0 + c, a, b, s, fp8_scale, amax);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&free_b[acc]), 0));
+    }
+    if constexpr (MODE == kFfnFp8) {
+      const float m = warp_max_nan(amax);
+      if (lane == 0) {
+        pdl_wait();  // amax was zeroed by the kernel this one depends on
+        atomicMax(reinterpret_cast<unsigned*>(p.f.amax), abs_bits(m));
+      }
+    }
   }
+  // A wait that ran out leaves copies and products in flight: give them a
+  // millisecond to land before the memory they write is given back.
+  if (!ok) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < 2000000) __nanosleep(1000);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_free_all(tmem);
 }
 
-// c[m, n] = sum_k a(m, k) b(k, n), a(m, k) = a[m * am + k * ak],
-// b(k, n) = b[k * bk + n]: bf16 in, fp32 sums, bf16 out
-__global__ void __launch_bounds__(32 * kTileRows)
-    rn_ffn_mm_kernel(const uint16_t* a, const uint16_t* b, uint16_t* c, int64_t M, int64_t Nn,
-                     int64_t Kk, int64_t am, int64_t ak, int64_t bk) {
-  __shared__ float sa[kTileRows][33], sb[32][33];
-  const int lane = threadIdx.x, ty = threadIdx.y;
-  const int64_t m = (int64_t)blockIdx.y * kTileRows + ty, n = (int64_t)blockIdx.x * 32 + lane;
-  float acc = 0.0f;
-  for (int64_t k0 = 0; k0 < Kk; k0 += 32) {
-    const int64_t k = k0 + lane;
-    sa[ty][lane] = (m < M && k < Kk) ? bf16_f32(a[m * am + k * ak]) : 0.0f;
-    for (int r = ty; r < 32; r += kTileRows)
-      sb[r][lane] = (k0 + r < Kk && n < Nn) ? bf16_f32(b[(k0 + r) * bk + n]) : 0.0f;
-    __syncthreads();
-#pragma unroll 8
-    for (int q = 0; q < 32; ++q) acc = fmaf(sa[ty][q], sb[q][lane], acc);
-    __syncthreads();
-  }
-  if (m < M && n < Nn) c[m * Nn + n] = (uint16_t)pack_bf16x2(acc, 0.0f);
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled through the runtime (no link against the driver
+// library); looked up once
+EncodeTiledFn encode_tiled() {
+  static const EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  return fn;
 }
 
-rn_status launch_mm(const void* a, const void* b, void* c, int64_t M, int64_t Nn, int64_t Kk,
-                    int64_t am, int64_t ak, int64_t bk, cudaStream_t s) {
-  const dim3 grid((unsigned)((Nn + 31) / 32), (unsigned)((M + kTileRows - 1) / kTileRows));
-  rn_ffn_mm_kernel<<<grid, dim3(32, kTileRows), 0, s>>>(
-      static_cast<const uint16_t*>(a), static_cast<const uint16_t*>(b), static_cast<uint16_t*>(c), M,
-      Nn, Kk, am, ak, bk);
+// bf16 [rows, cols], boxes of 64 columns x box_rows rows, 128-byte swizzle
+rn_status make_map(CUtensorMap* tm, const void* base, int64_t rows, int64_t cols, int box_rows) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (enc == nullptr) return RN_ERR_CUDA;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? RN_OK
+             : RN_ERR_CUDA;
+}
+
+int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+template <int ACT, int MODE>
+rn_status launch(const GemmParams& p, const Maps& maps, int sms, bool pdl, cudaStream_t s) {
+  auto k = rn_ffn_kernel<ACT, MODE>;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
+      cudaSuccess)
+    return RN_ERR_CUDA;
+  int64_t total = 0;
+  for (int j = 0; j < p.n_jobs; ++j) total += (int64_t)p.job[j].tiles_m * p.job[j].tiles_n;
+  if (total > INT32_MAX / 2) return RN_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cfg.gridDim = dim3((unsigned)sms / 2 * 2);
+  int resident = 0;
+  if (cudaOccupancyMaxActiveClusters(&resident, k, &cfg) != cudaSuccess) return RN_ERR_CUDA;
+  if (resident < 1) return RN_ERR_UNSUPPORTED;
+  cfg.gridDim = dim3(2u * (unsigned)(total < resident ? total : resident));
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, k, p, maps) != cudaSuccess) return RN_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? RN_OK : RN_ERR_CUDA;
+}
+
+template <int ACT>
+rn_status launch_mode(const GemmParams& p, const Maps& maps, int sms, cudaStream_t s) {
+  switch (p.f.mode) {
+    case kFfnBf16: return launch<ACT, kFfnBf16>(p, maps, sms, false, s);
+    case kFfnF32: return launch<ACT, kFfnF32>(p, maps, sms, false, s);
+    case kFfnFp8: return launch<ACT, kFfnFp8>(p, maps, sms, true, s);
+    case kFfnMx: return launch<ACT, kFfnMx>(p, maps, sms, false, s);
+    default: return RN_ERR_INVALID;
+  }
 }
 
 }  // namespace
 
-rn_status launch_ffn_fwd(int act, const FfnParams& p, int sms, cudaStream_t s) {
-  (void)sms;
-  const dim3 grid((unsigned)((p.H + 31) / 32), (unsigned)((p.N + kTileRows - 1) / kTileRows));
-  const dim3 block(32, kTileRows);
-  if (act == kActSwiglu)
-    rn_ffn_fwd_kernel<kActSwiglu><<<grid, block, 0, s>>>(p);
-  else
-    rn_ffn_fwd_kernel<kActClampedSwiglu><<<grid, block, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? RN_OK : RN_ERR_CUDA;
+rn_status launch_ffn_fwd(int act, const FfnParams& f, int sms, cudaStream_t s) {
+  GemmParams p{};
+  p.n_jobs = 1;
+  p.f = f;
+  p.job[0] = Job{cdiv(f.N, 256), cdiv(f.H, 128), cdiv(f.K, 64), false, false, nullptr, 0, 0};
+  Maps m{};
+  rn_status st;
+  if ((st = make_map(&m.a[0], f.x, f.N, f.K, 128)) != RN_OK) return st;
+  if ((st = make_map(&m.b[0], f.w, 2 * (int64_t)f.H, f.K, 128)) != RN_OK) return st;
+  return act == kActSwiglu ? launch_mode<kActSwiglu>(p, m, sms, s)
+                           : launch_mode<kActClampedSwiglu>(p, m, sms, s);
 }
 
-rn_status launch_ffn_bwd(const FfnBwdParams& p, int sms, cudaStream_t s) {
-  (void)sms;
-  const int64_t R = 2 * (int64_t)p.H;
+rn_status launch_ffn_bwd(const FfnBwdParams& b, int sms, cudaStream_t s) {
+  GemmParams p{};
+  Maps m{};
+  const int64_t R = 2 * (int64_t)b.H;
   rn_status st;
-  if (p.dx && (st = launch_mm(p.dp, p.w, p.dx, p.N, p.K, R, R, 1, p.K, s)) != RN_OK) return st;
-  if (p.dw && (st = launch_mm(p.dp, p.x, p.dw, R, p.K, p.N, 1, R, p.K, s)) != RN_OK) return st;
+  if (b.dx != nullptr) {
+    const int i = p.n_jobs++;
+    p.job[i] = Job{cdiv(b.N, 256), cdiv(b.K, 256), cdiv(R, 64), false, true, b.dx, b.N, b.K};
+    if ((st = make_map(&m.a[i], b.dp, b.N, R, 128)) != RN_OK) return st;
+    if ((st = make_map(&m.b[i], b.w, R, b.K, 64)) != RN_OK) return st;
+  }
+  if (b.dw != nullptr) {
+    const int i = p.n_jobs++;
+    p.job[i] = Job{cdiv(R, 256), cdiv(b.K, 256), cdiv(b.N, 64), true, true, b.dw, (int)R, b.K};
+    if ((st = make_map(&m.a[i], b.dp, b.N, R, 64)) != RN_OK) return st;
+    if ((st = make_map(&m.b[i], b.x, b.N, b.K, 64)) != RN_OK) return st;
+  }
+  if (p.n_jobs == 0) return RN_OK;
+  return launch<kActNone, kFfnBf16>(p, m, sms, false, s);
+}
+
+rn_status read_clear_error_ffn(unsigned* code) {
+  unsigned v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_ffn, sizeof(v)) != cudaSuccess) return RN_ERR_CUDA;
+  if (cudaMemcpyToSymbol(g_err_ffn, &zero, sizeof(zero)) != cudaSuccess) return RN_ERR_CUDA;
+  *code = v;
   return RN_OK;
 }
 

@@ -341,7 +341,7 @@ def test_norm_block_and_backward_together(quant):
     # each bf16 intermediate (h, pre, dy, dp, dh and the result) adds an independent relative error of
     # u / sqrt(3) at most; seven of them in a row stay below sqrt(7 / 3) u = 6e-3
     for a, b in ((y, yr), (dw, wr.grad), (dx, xr.grad), (dg, gr.grad)):
-        assert float((a.double() - b).norm() / b.norm()) <= 6e-3
+        assert float((a.double() - b).detach().norm() / b.detach().norm()) <= 6e-3
     if quant == "mxfp8":
         o, _ = rn.gated_ffn_fwd(h, w, quant="mxfp8")
         p = F.projections(f64(h), f64(w))
