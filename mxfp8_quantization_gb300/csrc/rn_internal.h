@@ -122,6 +122,9 @@ struct ActParams {
 // gated feed-forward block and the NVFP4 products
 constexpr int kActNone = -1;  // rn_nvfp4_matvec: no activation
 
+// up to this many tokens the bf16 block takes the few-token kernel
+constexpr int kFewTokens = 32;
+
 enum FfnOut : int { kFfnBf16 = 0, kFfnF32 = 1, kFfnFp8 = 2, kFfnMx = 3 };
 
 struct FfnParams {
@@ -149,14 +152,15 @@ struct FfnBwdParams {
 
 struct MvParams {
   const void* x;          // bf16 [N, K]
-  const uint8_t* codes;   // E2M1 pairs [R, K/2]; R = H, or 2H with an activation
-  const uint8_t* blocks;  // E4M3 scales [R, K/16]
-  const float* scale_inv; // 1 / S
+  const void* w;          // E2M1 pairs [R, K/2] or bf16 [R, K]; R = H, or 2H with an activation
+  const uint8_t* blocks;  // NVFP4: E4M3 scales [R, K/16]
+  const float* scale_inv; // NVFP4: 1 / S
   const float* scales;    // [N] or NULL
   void* out;              // [N, H]
   uint8_t* row_scales;    // kFfnMx
   const float* scale;     // kFfnFp8
   float* amax;            // kFfnFp8
+  void* pre;              // bf16 weights: bf16 [N, 2H] or NULL
   int N, K, H;
   float limit, alpha;
   int mode;               // FfnOut
@@ -245,6 +249,8 @@ rn_status launch_ffn_fwd(int act, const FfnParams& p, int sms, cudaStream_t s);
 rn_status launch_ffn_bwd(const FfnBwdParams& p, int sms, cudaStream_t s);
 // products with NVFP4 weights (act kActNone: R = H rows, no activation)
 rn_status launch_nvfp4_mv(int act, const MvParams& p, int sms, cudaStream_t s);
+// the gated block of few tokens with bf16 weights
+rn_status launch_bf16_mv(int act, const MvParams& p, int sms, cudaStream_t s);
 
 // delayed-scaling history step (one CTA; 1 <= L <= kMaxHistory)
 constexpr int kMaxHistory = 1024;

@@ -24,6 +24,11 @@ def _no_device_error():
 
 def weights(R, K, seed=0, std=2.0):
     g = torch.Generator().manual_seed(seed)
+    if K > 16384:   # wider than rn_quantize_only takes: any codes, block scales in [0.5, 2]
+        si = torch.full((1,), 2.0 ** -9, device="cuda")
+        return rn.NVFP4Output(torch.randint(0, 256, (R, K // 2), generator=g, dtype=torch.uint8).cuda(),
+                              torch.randint(0x30, 0x41, (R, K // 16), generator=g, dtype=torch.uint8).cuda(),
+                              1 / si, si, si)
     w = torch.randn(R, K, generator=g) * (std / K ** 0.5)
     return rn.quantize_only(w.cuda(), "nvfp4")
 
@@ -46,7 +51,7 @@ def proj(x, w):
 SIZES = [(1, 16, 1), (1, 32, 7), (1, 48, 33), (1, 4096, 64), (1, 2064, 250), (2, 4112, 65), (3, 16384, 17),
          (4, 128, 513), (7, 1040, 64), (8, 2048, 100), (9, 512, 96), (13, 5136, 40), (16, 256, 31),
          (17, 1024, 64), (24, 144, 130), (32, 8192, 24), (33, 96, 48), (40, 2080, 66), (100, 1024, 72),
-         (1, 1024, 20000)]
+         (1, 1024, 20000), (3, 65536, 24), (12, 65536, 40), (20, 65520, 16)]
 
 
 @pytest.mark.parametrize("i,size", list(enumerate(SIZES)), ids=lambda v: str(v))
