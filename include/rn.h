@@ -386,9 +386,9 @@ rn_status rn_gated_ffn_bwd(rn_act act, const void* dy, const void* x, const void
  *                       for rn_gated_ffn_fwd
  * x bf16 [N, K] (dtype RN_BF16; RN_F32 returns RN_ERR_UNSUPPORTED).  The
  * weights' values (without w_scale_inv) are exact in bf16, the sums are
- * fp32.  K % 16 == 0 up to 65536 (longer rows return RN_ERR_UNSUPPORTED), any
- * N <= 262144, R and H (MXFP8 output: H % 32 == 0); x, w_codes, w_scales and
- * the output 16-byte aligned.  Made for N of one to a few tens,
+ * fp32.  K % 16 == 0 up to 2^26 and N up to 2^20 (beyond:
+ * RN_ERR_UNSUPPORTED), any R and H (MXFP8 output: H % 32 == 0); x, w_codes,
+ * w_scales and the output 16-byte aligned.  Made for N of one to a few tens,
  * where the weights' bytes are the cost; larger N are valid, and read the
  * weights once per group of tokens.  No workspace.
  */

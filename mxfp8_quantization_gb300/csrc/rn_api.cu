@@ -981,7 +981,7 @@ rn_status rn_gated_ffn_fwd(rn_act act, const void* x, const void* w, rn_dtype dt
   if (kind == kFfnFp8 && (st = launch_fwd_init(out->amax, out->scale, out->scale_inv, s)) != RN_OK)
     return st;
   if (N == 0) return RN_OK;
-  if (N <= kFewTokens) {
+  if (N <= kFewTokens && K <= kMvMaxK) {
     MvParams m{};
     m.x = x;
     m.w = w;
@@ -997,8 +997,7 @@ rn_status rn_gated_ffn_fwd(rn_act act, const void* x, const void* w, rn_dtype dt
     m.limit = limit;
     m.alpha = alpha;
     m.mode = kind;
-    st = launch_bf16_mv(act, m, di.sms, s);
-    if (st != RN_ERR_UNSUPPORTED) return st;  // a K too long for its shared memory
+    return launch_bf16_mv(act, m, di.sms, s);
   }
   FfnParams p{};
   p.x = x;
@@ -1074,7 +1073,7 @@ static rn_status nvfp4_common(int act, const void* x, const uint8_t* w_codes, co
                               cudaStream_t s) {
   if (w_scale_inv == nullptr || (N > 0 && (x == nullptr || w_codes == nullptr || w_scales == nullptr)))
     return RN_ERR_INVALID;
-  if (K % 16 != 0 || K > 65536 || N > 262144 || !aligned(x, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 16) ||
+  if (K % 16 != 0 || K > kMvMaxK || N > kMvMaxN || !aligned(x, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 16) ||
       !aligned(w_scale_inv, 4))
     return RN_ERR_UNSUPPORTED;
   DeviceInfo di;

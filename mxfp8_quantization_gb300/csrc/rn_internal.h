@@ -124,6 +124,8 @@ constexpr int kActNone = -1;  // rn_nvfp4_matvec: no activation
 
 // up to this many tokens the bf16 block takes the few-token kernel
 constexpr int kFewTokens = 32;
+// few-token kernel: 8 rows apart stays within 32 bits; groups of 32 tokens in gridDim.y
+constexpr int64_t kMvMaxK = int64_t(1) << 26, kMvMaxN = int64_t(1) << 20;
 
 enum FfnOut : int { kFfnBf16 = 0, kFfnF32 = 1, kFfnFp8 = 2, kFfnMx = 3 };
 

@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kMvThreads = 256;
 constexpr int kMvWarps = kMvThreads / 32;
-constexpr int kDepth = 4;      // items in flight per warp
+constexpr int kDepth = 2;      // items in flight per warp
 constexpr int kPartStride = 36;  // floats per token of a warp's partial sums (32 rows, no bank conflicts)
 
 enum WeightKind : int { kWBf16 = 0, kWNvfp4 = 1 };
@@ -48,8 +48,10 @@ struct MvPlan {
   int kw;       // warps along the reduction
   int split;    // CTAs of a cluster along the reduction
   int chunks;   // chunks (128 / 32 elements) of the reduction
-  int slab;     // chunks per CTA
+  int part;     // chunks per CTA of the cluster
+  int slab;     // chunks whose tokens are in shared memory at a time
   int steps;    // groups of 8 / kw row tiles
+  int batch;    // steps whose sums are kept while the slabs change (slab < part)
 };
 
 __device__ __forceinline__ uint4 ldg_w16(const void* p) {
@@ -171,41 +173,49 @@ struct Mv {
         for (int h = 0; h < 2; ++h)
           it.w[m][h] = k < p.K ? ldg_w16(r.w[m] + (h ? r.dw[m] : 0) + k * 2) : make_uint4(0, 0, 0, 0);
     } else {
+      // past the row's end the last blocks are read again: the tokens are 0 there
       const int k = chunk * 128 + t * 32;
       if ((p.K & 31) == 0) {  // rows of whole 16-byte pieces
+        const int at = min(k, p.K - 32);
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            it.w[m][h] = k < p.K ? ldg_w16(r.w[m] + (h ? r.dw[m] : 0) + k / 2) : make_uint4(0, 0, 0, 0);
+            it.w[m][h] = ldg_w16(r.w[m] + (h ? r.dw[m] : 0) + at / 2);
             it.s[m][h] =
-                k < p.K ? __ldg(reinterpret_cast<const unsigned short*>(r.s[m] + (h ? r.ds[m] : 0) + k / 16)) : 0u;
+                __ldg(reinterpret_cast<const unsigned short*>(r.s[m] + (h ? r.ds[m] : 0) + at / 16));
           }
-      } else {  // an odd number of blocks: rows on 8 bytes, the last piece half
+      } else {  // an odd number of blocks: rows on 8 bytes
+        const int at0 = min(k, p.K - 16), at1 = min(k + 16, p.K - 16);
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint2 z = make_uint2(0, 0);
-            const uint2 lo = k < p.K ? ldg_w8(r.w[m] + (h ? r.dw[m] : 0) + k / 2) : z;
-            const uint2 hi = k + 16 < p.K ? ldg_w8(r.w[m] + (h ? r.dw[m] : 0) + k / 2 + 8) : z;
+            const uint8_t* w = r.w[m] + (h ? r.dw[m] : 0);
+            const uint8_t* sc = r.s[m] + (h ? r.ds[m] : 0);
+            const uint2 lo = ldg_w8(w + at0 / 2), hi = ldg_w8(w + at1 / 2);
             it.w[m][h] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-            const uint32_t s0 = k < p.K ? __ldg(r.s[m] + (h ? r.ds[m] : 0) + k / 16) : 0u;
-            const uint32_t s1 = k + 16 < p.K ? __ldg(r.s[m] + (h ? r.ds[m] : 0) + k / 16 + 1) : 0u;
-            it.s[m][h] = s0 | s1 << 8;
+            it.s[m][h] = __ldg(sc + at0 / 16) | (uint32_t)__ldg(sc + at1 / 16) << 8;
           }
       }
     }
   }
 
-  // acc += item x tokens; xs: the chunk's fragments of this lane
+  // where this lane's fragments of each group of 8 tokens start in a chunk (in 16 bytes); columns
+  // without a token read the last token's: their sums are dropped
+  __device__ __forceinline__ static void lane_at(int n, int lane, int (&at)[T]) {
+#pragma unroll
+    for (int t = 0; t < T; ++t) at[t] = min(t * 8 + (lane >> 2), n - 1) * 4 + (lane & 3);
+  }
+
+  // acc += item x tokens; xs: the chunk's fragments
   template <bool WIDE>
-  __device__ __forceinline__ static void compute(const Item& it, const uint4* xs,
-                                                 float (&acc)[2][T][4]) {
+  __device__ __forceinline__ static void compute(const Item& it, const uint4* xs, int n,
+                                                 const int (&at)[T], float (&acc)[2][T][4]) {
     if constexpr (WK == kWBf16) {
       uint4 b[T];
 #pragma unroll
-      for (int t = 0; t < T; ++t) b[t] = xs[t * 32];
+      for (int t = 0; t < T; ++t) b[t] = xs[at[t]];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const uint32_t a0[4] = {it.w[m][0].x, it.w[m][1].x, it.w[m][0].y, it.w[m][1].y};
@@ -221,7 +231,7 @@ struct Mv {
       for (int q = 0; q < 4; ++q) {  // 8 codes of each row
         uint4 b[T];
 #pragma unroll
-        for (int t = 0; t < T; ++t) b[t] = xs[(q * T + t) * 32];
+        for (int t = 0; t < T; ++t) b[t] = xs[q * 4 * n + at[t]];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           uint32_t v[2][4];
@@ -251,13 +261,6 @@ struct Mv {
       }
     }
   }
-};
-
-template <int ACT, int WK, int T>
-struct Smem {
-  uint4* xs;       // [slab][J][T][32]
-  float* part;     // [8 warps][T][8 tokens][kPartStride]
-  float* parts;    // split > 1: [split][8 / kw row tiles][T][8][32] sums of the cluster's CTAs
 };
 
 // y of one output column and token: stored as p.mode asks (kFfnMx: the warp
@@ -294,19 +297,18 @@ __device__ __forceinline__ void finish(const MvParams& p, int n, int col, float 
   }
 }
 
-// the tokens of this CTA's part of the reduction, in fragment order; returns
-// whether they had to stay bf16 (NVFP4).  inv: what each token's sums are
+// the tokens' elements of chunks lo .. hi - 1, in fragment order (zeros past
+// the row's end); returns whether they had to stay bf16 (NVFP4).  inv: what each token's sums are
 // multiplied with.
 template <int WK, int T>
-__device__ bool stage_tokens(const MvParams& p, const MvPlan& pl, int rank, int n0, int n, uint4* xs,
-                             float* inv) {
+__device__ bool stage_tokens(const MvParams& p, int lo, int hi, int n0, int n, uint4* xs, float* inv) {
   using M = Mv<WK, T>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int k_lo = rank * pl.slab * M::CK;
-  const int pieces = pl.slab * M::CK / 8;  // per token, 8 elements each
+  const int k_lo = lo * M::CK;
+  const int pieces = (hi - lo) * M::CK / 8;  // per token, 8 elements each
   const auto piece = [&](int tok, int q) {
     const int k = k_lo + q * 8;
-    return tok < n && k < p.K
+    return k < p.K
                ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) +
                                                       (int64_t)(n0 + tok) * p.K + k))
                : make_uint4(0, 0, 0, 0);
@@ -314,22 +316,21 @@ __device__ bool stage_tokens(const MvParams& p, const MvPlan& pl, int rank, int 
   const auto place = [&](int tok, int q) {
     const int chunk = q / (M::CK / 8), in = q % (M::CK / 8);
     const int t = in / M::J, j = in % M::J;
-    return xs + ((chunk * M::J + j) * T + tok / 8) * 32 + (tok & 7) * 4 + t;
+    return xs + ((chunk * M::J + j) * n + tok) * 4 + t;
   };
   bool wide = false;
-  for (int tok = warp; tok < 8 * T; tok += kMvWarps) {
+  for (int tok = warp; tok < n; tok += kMvWarps) {
     if constexpr (WK == kWBf16) {
       for (int q = lane; q < pieces; q += 32) *place(tok, q) = piece(tok, q);
       if (lane == 0) inv[tok] = 1.0f;
     } else {
       uint32_t m = 0;  // largest magnitude, as bf16 bits
-      if (tok < n)
-        for (int q = lane; q < pieces; q += 32) {
-          const uint4 v = piece(tok, q);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int q = lane; q < pieces; q += 32) {
+        const uint4 v = piece(tok, q);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-        }
+        for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+      }
       m = warp_umax(m);
       // 2^c puts it into [2^14, 2^15); c within what fp32 holds
       const int c = m == 0u ? 0 : min(126, max(-126, 14 - ((int)(m >> 7) - 127)));
@@ -354,7 +355,7 @@ __device__ bool stage_tokens(const MvParams& p, const MvPlan& pl, int rank, int 
   if constexpr (WK == kWNvfp4) {
     wide = __syncthreads_or(wide);
     if (wide) {
-      for (int tok = warp; tok < 8 * T; tok += kMvWarps) {
+      for (int tok = warp; tok < n; tok += kMvWarps) {
         for (int q = lane; q < pieces; q += 32) *place(tok, q) = piece(tok, q);
         if (lane == 0) inv[tok] = 1.0f;
       }
@@ -364,136 +365,170 @@ __device__ bool stage_tokens(const MvParams& p, const MvPlan& pl, int rank, int 
   return wide;
 }
 
-template <int ACT, int WK, int T, bool WIDE>
-__device__ void run(const MvParams& p, const MvPlan& pl, int rank, int group, int n_groups, int n0, int n,
-                    const uint4* xs, float* part, float* parts, const float* inv, float* amax,
-                    Item (&it)[kDepth], int c_lo, int c_hi) {
+// one step's sums over this warp's chunks c_lo .. c_hi - 1 of the slab that
+// starts at chunk `lo`.  `it` holds the first items already, and gets the
+// first ones of the rows `next` (chunks n_lo .. n_hi - 1) on the way.
+template <bool GATED, int WK, int T, bool WIDE>
+__device__ __forceinline__ void step_sums(const MvParams& p, int tile, int next_tile, int lane, int n,
+                                          const uint4* xs, int lo, int c_lo, int c_hi, int n_lo, int n_hi,
+                                          const int (&at)[T], Item (&it)[kDepth], float (&acc)[2][T][4]) {
   using M = Mv<WK, T>;
-  constexpr bool GATED = ACT != kActNone;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rw = kMvWarps / pl.kw, wr = warp / pl.kw;
-  const int cols = rw * (GATED ? 16 : 32);  // outputs of a step
-  const float si = WK == kWNvfp4 ? __ldg(p.scale_inv) : 1.0f;
-  for (int step = group; step < pl.steps; step += n_groups) {
-    float acc[2][T][4];
+  Rows r;
+  if (c_lo >= c_hi) {  // nothing of this slab
+    M::template rows<GATED>(p, next_tile, lane, r);
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int d = 0; d < kDepth; ++d)
+      if (n_lo + d < n_hi) M::load(p, r, n_lo + d, lane, it[d]);
+    return;
+  }
+  M::template rows<GATED>(p, tile, lane, r);
+  for (int c = c_lo; c < c_hi; c += kDepth) {
+    // a slot's next item: of this step, or the first ones of the next
+    const bool last = c + kDepth >= c_hi;
+    if (last) M::template rows<GATED>(p, next_tile, lane, r);
+    const int from = last ? n_lo : c + kDepth, to = last ? n_hi : c_hi;
 #pragma unroll
-      for (int t = 0; t < T; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][t][i] = 0.0f;
-    Rows r;
-    M::template rows<GATED>(p, step * rw + wr, lane, r);
-    const int next = step + n_groups;
-    for (int c = c_lo; c < c_hi; c += kDepth) {
-      // a slot's next item: of this step, or the first ones of the next step
-      const bool last = c + kDepth >= c_hi;
-      if (last) M::template rows<GATED>(p, next * rw + wr, lane, r);
-      const int from = last ? c_lo : c + kDepth;
-      const int to = last && next >= pl.steps ? from : c_hi;
-#pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        if (c + d < c_hi)
-          M::template compute<WIDE>(it[d], xs + (size_t)(c + d - rank * pl.slab) * M::J * T * 32 + lane, acc);
-        if (from + d < to) M::load(p, r, from + d, lane, it[d]);
-      }
-    }
-    // this warp's sums: [T][8 tokens][32 rows]
-    float* mine = part + warp * T * 8 * kPartStride;
-    const int g = lane >> 2, t2 = (lane & 3) * 2;
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int t = 0; t < T; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mine[(t * 8 + t2 + (i & 1)) * kPartStride + m * 16 + g + (i >> 1) * 8] = acc[m][t][i];
-    __syncthreads();
-    // one row's sum over the CTA's warps, times what its token was scaled by
-    const auto cta_sum = [&](int tile, int tok, int row) {
-      const float* q = part + ((tile * pl.kw) * T * 8 + tok) * kPartStride + row;
-      float v = q[0];
-      for (int w = 1; w < pl.kw; ++w) v += q[w * T * 8 * kPartStride];
-      return v * inv[tok];
-    };
-    if (pl.split == 1) {
-      for (int i = threadIdx.x; i < cols * n; i += kMvThreads) {
-        const int tok = i / cols, col = i % cols;
-        if constexpr (GATED) {
-          const float a = cta_sum(col / 16, tok, col % 16) * si;
-          const float b = cta_sum(col / 16, tok, 16 + col % 16) * si;
-          finish<ACT>(p, n0 + tok, step * cols + col, a, b, amax);
-        } else {
-          finish<ACT>(p, n0 + tok, step * cols + col, cta_sum(col / 32, tok, col % 32) * si, 0.0f, amax);
-        }
-      }
-      __syncthreads();
-    } else {
-      // the steps' sums meet in the cluster's CTAs in turn
-      const int leader = ((step - group) / n_groups) % pl.split;
-      const int vals = rw * T * 8 * 32;
-      const uint32_t to = map_to_rank(smem_u32(parts + rank * vals), leader);
-      for (int i = threadIdx.x; i < rw * n * 32; i += kMvThreads) {
-        const int tile = i / (n * 32), tok = i / 32 % n, row = i & 31;
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + ((tile * T * 8 + tok) * 32 + row) * 4),
-                     "f"(cta_sum(tile, tok, row))
-                     : "memory");
-      }
-      cluster_sync();
-      if (rank == leader) {
-        const auto sum = [&](int tile, int tok, int row) {
-          const float* q = parts + (tile * T * 8 + tok) * 32 + row;
-          float v = q[0];
-          for (int s = 1; s < pl.split; ++s) v += q[s * vals];
-          return v * si;
-        };
-        for (int i = threadIdx.x; i < cols * n; i += kMvThreads) {
-          const int tok = i / cols, col = i % cols;
-          if constexpr (GATED)
-            finish<ACT>(p, n0 + tok, step * cols + col, sum(col / 16, tok, col % 16),
-                        sum(col / 16, tok, 16 + col % 16), amax);
-          else
-            finish<ACT>(p, n0 + tok, step * cols + col, sum(col / 32, tok, col % 32), 0.0f, amax);
-        }
-      }
+    for (int d = 0; d < kDepth; ++d) {
+      if (c + d < c_hi) M::template compute<WIDE>(it[d], xs + (c + d - lo) * (M::J * 4 * n), n, at, acc);
+      if (from + d < to) M::load(p, r, from + d, lane, it[d]);
     }
   }
 }
 
 template <int ACT, int WK, int T>
-__global__ void __launch_bounds__(kMvThreads, T == 1 ? 2 : 1)
-    rn_matvec_kernel(const MvParams p, const MvPlan pl) {
+__global__ void __launch_bounds__(kMvThreads, 2) rn_matvec_kernel(const MvParams p, const MvPlan pl) {
   using M = Mv<WK, T>;
+  constexpr bool GATED = ACT != kActNone;
   extern __shared__ uint4 smem[];
   __shared__ float inv[8 * T];
-  uint4* xs = smem;
-  float* part = reinterpret_cast<float*>(xs + (size_t)pl.slab * M::J * T * 32);
-  float* parts = part + kMvWarps * T * 8 * kPartStride;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = pl.split > 1 ? (int)cluster_rank() : 0;
   const int group = (int)blockIdx.x / pl.split, n_groups = (int)gridDim.x / pl.split;
   const int n0 = (int)blockIdx.y * 8 * T;
   const int n = min(8 * T, p.N - n0);
-  const int rw = kMvWarps / pl.kw;
-  // this warp's chunks, contiguous
-  const int lo = rank * pl.slab, hi = min(lo + pl.slab, pl.chunks);
-  const int wk = warp % pl.kw, len = max(0, hi - lo);
-  const int c_lo = lo + len * wk / pl.kw, c_hi = lo + len * (wk + 1) / pl.kw;
+  const int rw = kMvWarps / pl.kw, wr = warp / pl.kw, wk = warp % pl.kw;
+  const int cols = rw * (GATED ? 16 : 32);  // outputs of a step
+  // tokens; the warps' sums [8][T][8][kPartStride]; in a cluster its CTAs'
+  // sums [split][rw][n][32]; with several slabs the steps' sums [batch][rw][n][32]
+  const int n_max = min(8 * T, p.N);
+  uint4* xs = smem;
+  float* part = reinterpret_cast<float*>(xs + pl.slab * M::J * 4 * n_max);
+  float* parts = part + kMvWarps * T * 8 * kPartStride;
+  const int lo = rank * pl.part, hi = min(lo + pl.part, pl.chunks);
+  const int slabs = max(1, (hi - lo + pl.slab - 1) / pl.slab);
+  const int my_steps = (pl.steps - group + n_groups - 1) / n_groups;
+  // this warp's chunks of slab i: contiguous
+  const auto chunk_at = [&](int i, int w) {
+    const int a = min(lo + i * pl.slab, max(lo, hi)), b = min(a + pl.slab, max(lo, hi));
+    return a + (b - a) * w / pl.kw;
+  };
+  int at[T];
+  M::lane_at(n, lane, at);
+  const float si = WK == kWNvfp4 ? __ldg(p.scale_inv) : 1.0f;
+  float amax = 0.0f;
 
   Item it[kDepth];
   {
+    const int c_lo = chunk_at(0, wk), c_hi = chunk_at(0, wk + 1);
     Rows r;
-    M::template rows<ACT != kActNone>(p, group * rw + warp / pl.kw, lane, r);
+    M::template rows<GATED>(p, group * rw + wr, lane, r);
 #pragma unroll
     for (int d = 0; d < kDepth; ++d)
       if (c_lo + d < c_hi) M::load(p, r, c_lo + d, lane, it[d]);
   }
-  const bool wide = stage_tokens<WK, T>(p, pl, rank, n0, n, xs, inv);
-  float amax = 0.0f;
-  if (WK == kWNvfp4 && wide)
-    run<ACT, WK, T, true>(p, pl, rank, group, n_groups, n0, n, xs, part, parts, inv, &amax, it, c_lo, c_hi);
-  else
-    run<ACT, WK, T, false>(p, pl, rank, group, n_groups, n0, n, xs, part, parts, inv, &amax, it, c_lo, c_hi);
+  bool wide = false;
+  for (int b0 = 0; b0 < my_steps; b0 += pl.batch) {
+    const int b1 = min(b0 + pl.batch, my_steps);
+    for (int sl = 0; sl < slabs; ++sl) {
+      if (slabs > 1 || b0 == 0) {
+        const int s_lo = lo + sl * pl.slab;
+        wide = stage_tokens<WK, T>(p, s_lo, max(s_lo, min(s_lo + pl.slab, hi)), n0, n, xs, inv);
+      }
+      const int c_lo = chunk_at(sl, wk), c_hi = chunk_at(sl, wk + 1);
+      for (int j = b0; j < b1; ++j) {
+        const int step = group + j * n_groups;
+        // what follows: the batch's next step, its first with the next slab, the next batch's first
+        const bool wrap = j + 1 == b1;
+        const int sl2 = wrap ? (sl + 1) % slabs : sl;
+        const int j2 = wrap ? (sl + 1 < slabs ? b0 : b1) : j + 1;
+        const int n_lo = chunk_at(sl2, wk), n_hi = j2 < my_steps ? chunk_at(sl2, wk + 1) : n_lo;
+        const int next = group + min(j2, my_steps - 1) * n_groups;
+        float acc[2][T][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][t][i] = 0.0f;
+        if (WK == kWNvfp4 && wide)
+          step_sums<GATED, WK, T, true>(p, step * rw + wr, next * rw + wr, lane, n, xs, lo + sl * pl.slab,
+                                        c_lo, c_hi, n_lo, n_hi, at, it, acc);
+        else
+          step_sums<GATED, WK, T, false>(p, step * rw + wr, next * rw + wr, lane, n, xs, lo + sl * pl.slab,
+                                         c_lo, c_hi, n_lo, n_hi, at, it, acc);
+        // this warp's sums: [T][8 tokens][32 rows]
+        float* mine = part + warp * T * 8 * kPartStride;
+        const int g = lane >> 2, t2 = (lane & 3) * 2;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mine[(t * 8 + t2 + (i & 1)) * kPartStride + m * 16 + g + (i >> 1) * 8] = acc[m][t][i];
+        __syncthreads();
+        // one row's sum over the CTA's warps, times what its token was scaled by
+        const auto cta_sum = [&](int tile, int tok, int row) {
+          const float* q = part + ((tile * pl.kw) * T * 8 + tok) * kPartStride + row;
+          float v = q[0];
+          for (int w = 1; w < pl.kw; ++w) v += q[w * T * 8 * kPartStride];
+          return v * inv[tok];
+        };
+        // the outputs of the step, from what `sum` gives for a row
+        const auto outputs = [&](auto sum) {
+          for (int i = threadIdx.x; i < cols * n; i += kMvThreads) {
+            const int tok = i / cols, col = i % cols;
+            if constexpr (GATED)
+              finish<ACT>(p, n0 + tok, step * cols + col, sum(col / 16, tok, col % 16) * si,
+                          sum(col / 16, tok, 16 + col % 16) * si, &amax);
+            else
+              finish<ACT>(p, n0 + tok, step * cols + col, sum(col / 32, tok, col % 32) * si, 0.0f, &amax);
+          }
+        };
+        const int vals = rw * n * 32;
+        if (pl.split > 1) {
+          // the steps' sums meet in the cluster's CTAs in turn
+          const int leader = j % pl.split;
+          const uint32_t to = map_to_rank(smem_u32(parts + rank * vals), leader);
+          for (int i = threadIdx.x; i < vals; i += kMvThreads)
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * 4),
+                         "f"(cta_sum(i / (n * 32), i / 32 % n, i & 31))
+                         : "memory");
+          cluster_sync();
+          if (rank == leader)
+            outputs([&](int tile, int tok, int row) {
+              const float* q = parts + (tile * n + tok) * 32 + row;
+              float v = q[0];
+              for (int s = 1; s < pl.split; ++s) v += q[s * vals];
+              return v;
+            });
+        } else if (slabs > 1) {
+          // slab after slab, each thread its own sums
+          float* sums = parts + (j - b0) * vals;
+          for (int i = threadIdx.x; i < vals; i += kMvThreads) {
+            const float v = cta_sum(i / (n * 32), i / 32 % n, i & 31);
+            sums[i] = sl == 0 ? v : sums[i] + v;
+          }
+          __syncthreads();
+          if (sl + 1 == slabs)
+            outputs([&](int tile, int tok, int row) { return sums[(tile * n + tok) * 32 + row]; });
+        } else {
+          outputs(cta_sum);
+          __syncthreads();
+        }
+      }
+    }
+  }
   if (p.mode == kFfnFp8) {
     const float m = warp_max_nan(amax);
     if (lane == 0) {
@@ -504,15 +539,7 @@ __global__ void __launch_bounds__(kMvThreads, T == 1 ? 2 : 1)
   if (pl.split > 1) cluster_sync();  // no CTA leaves while another writes to it
 }
 
-constexpr size_t kMvSmemMax = 220 * 1024;
-
-template <int WK, int T>
-size_t smem_bytes(const MvPlan& pl) {
-  using M = Mv<WK, T>;
-  size_t b = (size_t)pl.slab * M::J * T * 32 * 16 + (size_t)kMvWarps * T * 8 * kPartStride * 4;
-  if (pl.split > 1) b += (size_t)pl.split * (kMvWarps / pl.kw) * T * 8 * 32 * 4;
-  return b;
-}
+constexpr size_t kMvSmemHalf = 112 * 1024;  // two CTAs an SM
 
 template <int ACT, int WK, int T>
 rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
@@ -521,36 +548,60 @@ rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
   constexpr int RO = ACT == kActNone ? 32 : 16;  // outputs of a row tile
   MvPlan pl{};
   pl.chunks = (p.K + M::CK - 1) / M::CK;
+  const int n = p.N < 8 * T ? p.N : 8 * T;
+  const int64_t ny = ((int64_t)p.N + 8 * T - 1) / (8 * T);
   const int tiles = (p.H + RO - 1) / RO;
-  const int kw_max = p.mode == kFfnMx ? kMvWarps / 2 : kMvWarps;  // an MXFP8 block: two row tiles a step
-  bool fits = false;
-  for (pl.split = 1; pl.split <= 8; pl.split *= 2) {
-    pl.slab = (pl.chunks + pl.split - 1) / pl.split;
-    pl.kw = kw_max;
-    if (smem_bytes<WK, T>(pl) > kMvSmemMax) continue;
-    fits = true;
-    if ((int64_t)tiles * pl.split >= sms || pl.slab < 2 * kMvWarps) break;
-  }
-  if (pl.split > 8) pl.split = 8;
-  pl.slab = (pl.chunks + pl.split - 1) / pl.split;
-  if (!fits) return RN_ERR_UNSUPPORTED;
-  pl.kw = kw_max;
-  while (pl.kw > 1 && pl.slab < 4 * pl.kw && (int64_t)tiles * pl.split * pl.kw >= 2ll * sms * kMvWarps) pl.kw /= 2;
+  const size_t chunk_bytes = (size_t)M::J * 4 * n * 16;
+  const size_t warp_bytes = (size_t)kMvWarps * T * 8 * kPartStride * 4;
+  // few row tiles: the reduction over a cluster, while its CTAs' warps keep
+  // two chunks each
+  pl.split = 1;
+  while (pl.split < 8 && tiles * ny * pl.split < sms && pl.chunks >= 4 * kMvWarps * pl.split) pl.split *= 2;
+  pl.part = (pl.chunks + pl.split - 1) / pl.split;
+  // warps along the reduction: fewer where it is short and the rows are many
+  // (an MXFP8 block needs two row tiles a step)
+  pl.kw = p.mode == kFfnMx ? kMvWarps / 2 : kMvWarps;
+  while (pl.kw > 1 && pl.part < kDepth * pl.kw &&
+         (int64_t)tiles * ny * pl.split * pl.kw >= 2ll * sms * kMvWarps)
+    pl.kw /= 2;
   const int rw = kMvWarps / pl.kw;
   pl.steps = (tiles + rw - 1) / rw;
-  const size_t smem = smem_bytes<WK, T>(pl);
-  if (smem > kMvSmemMax) return RN_ERR_UNSUPPORTED;
+  const size_t step_bytes = (size_t)rw * n * 32 * 4;
+  int per = (2 * sms) / pl.split;  // clusters or CTAs of one token group
+  if (per > pl.steps) per = pl.steps;
+  if (per < 1) per = 1;
+  const int my_steps = (pl.steps + per - 1) / per;
+  size_t room = kMvSmemHalf - warp_bytes - (pl.split > 1 ? pl.split * step_bytes : 0);
+  pl.slab = pl.part;
+  pl.batch = my_steps;
+  if (pl.slab * chunk_bytes > room) {
+    if (pl.split > 1) {  // then the rows are few: no cluster, several slabs
+      pl.split = 1;
+      pl.part = pl.chunks;
+      room = kMvSmemHalf - warp_bytes;
+      per = 2 * sms < pl.steps ? 2 * sms : pl.steps;
+    }
+    pl.batch = (pl.steps + per - 1) / per;
+    if (pl.slab * chunk_bytes > room || pl.part != pl.slab) {
+      // a third of the room at most for the steps' sums
+      const int fit = (int)(room / 3 / step_bytes);
+      if (pl.batch > fit) pl.batch = fit;
+      if (pl.batch < 1) return RN_ERR_UNSUPPORTED;
+      pl.slab = (int)((room - pl.batch * step_bytes) / chunk_bytes);
+      if (pl.slab < 1) return RN_ERR_UNSUPPORTED;
+      const int slabs = (pl.part + pl.slab - 1) / pl.slab;
+      pl.slab = (pl.part + slabs - 1) / slabs;
+    }
+  }
+  size_t smem = pl.slab * chunk_bytes + warp_bytes;
+  if (pl.split > 1)
+    smem += pl.split * step_bytes;
+  else if (pl.slab < pl.part)
+    smem += pl.batch * step_bytes;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return RN_ERR_CUDA;
-  int occ = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k, kMvThreads, smem) != cudaSuccess)
-    return RN_ERR_CUDA;
-  if (occ < 1) return RN_ERR_UNSUPPORTED;
-  int groups = sms * occ / pl.split;
-  if (groups < 1) groups = 1;
-  if (groups > pl.steps) groups = pl.steps;
-  const int64_t ny = ((int64_t)p.N + 8 * T - 1) / (8 * T);
   if (ny > 65535) return RN_ERR_UNSUPPORTED;
+  const int groups = per;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(groups * pl.split), (unsigned)ny);
   cfg.blockDim = dim3(kMvThreads);
@@ -576,15 +627,12 @@ rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? RN_OK : RN_ERR_CUDA;
 }
 
-// groups of 8, 16 or 32 tokens; long reductions, whose tokens would not fit,
-// take smaller groups
+// groups of 8, 16 or 32 tokens
 template <int ACT, int WK>
 rn_status launch_n(const MvParams& p, int sms, cudaStream_t s) {
-  rn_status st = RN_ERR_UNSUPPORTED;
-  if (p.N > 16) st = launch_t<ACT, WK, 4>(p, sms, s);
-  if (p.N > 8 && st == RN_ERR_UNSUPPORTED) st = launch_t<ACT, WK, 2>(p, sms, s);
-  if (st == RN_ERR_UNSUPPORTED) st = launch_t<ACT, WK, 1>(p, sms, s);
-  return st;
+  if (p.N <= 8) return launch_t<ACT, WK, 1>(p, sms, s);
+  if (p.N <= 16) return launch_t<ACT, WK, 2>(p, sms, s);
+  return launch_t<ACT, WK, 4>(p, sms, s);
 }
 
 }  // namespace

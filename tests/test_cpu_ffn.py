@@ -124,8 +124,8 @@ def _mv(lib, **kw):
 
 WEIGHTS = [(dict(codes=None), INVALID), (dict(blocks=None), INVALID), (dict(si=None), INVALID),
            (dict(codes=0x2008), UNSUPPORTED), (dict(blocks=0x3008), UNSUPPORTED),
-           (dict(si=0x4002), UNSUPPORTED), (dict(K=72), UNSUPPORTED), (dict(K=65552), UNSUPPORTED),
-           (dict(N=262145), UNSUPPORTED)]
+           (dict(si=0x4002), UNSUPPORTED), (dict(K=72), UNSUPPORTED), (dict(K=2 ** 26 + 16), UNSUPPORTED),
+           (dict(N=2 ** 20 + 1), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("kw,want", SHARED + WEIGHTS, ids=str)
