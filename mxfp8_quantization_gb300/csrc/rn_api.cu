@@ -1151,7 +1151,9 @@ rn_status rn_device_error(unsigned int* code) {
   if ((st = read_clear_error_bwd(&c)) != RN_OK) return st;
   unsigned d = 0;
   if ((st = read_clear_error_ffn(&d)) != RN_OK) return st;
-  *code = a ? a : (b ? b : (c ? c : d));
+  unsigned e = 0;
+  if ((st = read_clear_error_mv(&e)) != RN_OK) return st;
+  *code = a ? a : (b ? b : (c ? c : (d ? d : e)));
   return RN_OK;
 }
 

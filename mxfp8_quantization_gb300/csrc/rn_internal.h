@@ -265,5 +265,6 @@ rn_status read_clear_error_fwd_res(unsigned* code);
 rn_status read_clear_error_mx(unsigned* code);
 rn_status read_clear_error_bwd(unsigned* code);
 rn_status read_clear_error_ffn(unsigned* code);
+rn_status read_clear_error_mv(unsigned* code);
 
 }  // namespace rn

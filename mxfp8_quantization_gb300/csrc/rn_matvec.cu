@@ -17,10 +17,10 @@
 // (16-byte conflict-free reads).  NVFP4 weights become f16 with one
 // conversion and one product a pair: E2M1 value x E4M3 scale has at most 6
 // significant bits and lies in [2^-10, 2688], so it is exact in f16.  The
-// tokens, bf16, become f16 too, each times a power of two that puts its
-// largest magnitude at 2^14: exact unless a token's magnitudes span more than
-// 2^31; a CTA that finds an element that is not exact keeps its tokens in
-// bf16 and expands the weights to bf16 (exact as well), which is slower.  Sums
+// tokens, bf16, become f16 too, times the power of two that puts their
+// largest magnitude at 2^14: exact unless the magnitudes span more than 2^31;
+// a CTA that finds an element that is not exact keeps its tokens in bf16 and
+// expands the weights to bf16 (exact as well), which is slower.  Sums
 // are fp32.
 //
 // Warps split the reduction KW ways and the rows 8 / KW ways, clusters of S
@@ -37,10 +37,12 @@
 namespace rn {
 namespace {
 
-constexpr int kMvThreads = 256;
-constexpr int kMvWarps = kMvThreads / 32;
-constexpr int kDepth = 2;      // items in flight per warp
-constexpr int kPartStride = 36;  // floats per token of a warp's partial sums (32 rows, no bank conflicts)
+__device__ unsigned g_err_mv;
+
+constexpr int kWBytes = 128;     // of a row's weights in a chunk
+constexpr int kSBytes = 16;      // of its scales (NVFP4)
+constexpr int kDepth = 1;        // items in flight per warp
+constexpr int kPartStride = 36;  // floats per token of a warp's sums (32 rows, no bank conflicts)
 
 enum WeightKind : int { kWBf16 = 0, kWNvfp4 = 1 };
 
@@ -54,6 +56,13 @@ struct MvPlan {
   int batch;    // steps whose sums are kept while the slabs change (slab < part)
 };
 
+// weights: read once, so not kept in L1
+__device__ __forceinline__ void ldg_w32(const void* p, uint4 (&v)[2]) {
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y),
+                 "=r"(v[1].z), "=r"(v[1].w)
+               : "l"(p));
+}
 __device__ __forceinline__ uint4 ldg_w16(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -66,6 +75,15 @@ __device__ __forceinline__ uint2 ldg_w8(const void* p) {
   asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0, %1}, [%2];"
                : "=r"(v.x), "=r"(v.y)
                : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -123,139 +141,173 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// one item of a lane: 16 bytes of rows g and g + 8 of two 16-row tiles, and
-// for NVFP4 the two scale codes of each
+// an item of a lane: 32 bytes of rows g and g + 8 of two 16-row tiles, and
+// for NVFP4 the four scale codes of each
 struct Item {
-  uint4 w[2][2];
+  uint4 w[2][2][2];
   uint32_t s[2][2];
 };
 
-// the rows a lane reads: row g of both tiles, and how far on row g + 8 is
+__device__ __forceinline__ void sts16(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+// what a lane reads next: its bytes of rows g and g + 8 of two 16-row tiles
 struct Rows {
-  const uint8_t* w[2];
-  const uint8_t* s[2];
-  int dw[2], ds[2];
+  const uint8_t* w[2][2];
+  const uint8_t* s[2][2];
 };
 
 template <int WK, int T>
 struct Mv {
-  static constexpr int CK = WK == kWNvfp4 ? 128 : 32;  // reduction elements of a chunk
+  static constexpr int CK = WK == kWNvfp4 ? 256 : 64;  // reduction elements of a chunk
   static constexpr int J = CK / 32;                    // 16-byte pieces of a token a lane reads per chunk
 
-  // rows of row tile `rt`: a plain product's 32, or 16 gate and 16 linear
-  // ones; rows past the end read the last row (their sums are dropped)
+  // chunk `chunk` of row tile `rt`: a plain product's 32 rows, or 16 gate and
+  // 16 linear ones; rows past the end read the last row (their sums are
+  // dropped)
   template <bool GATED>
-  __device__ __forceinline__ static void rows(const MvParams& p, int rt, int lane, Rows& r) {
-    const int g = lane >> 2;
+  __device__ __forceinline__ static void rows(const MvParams& p, int rt, int chunk, int lane, Rows& r) {
+    const int g = lane >> 2, t = lane & 3;
     const int64_t pitch = WK == kWNvfp4 ? p.K / 2 : p.K * 2ll;
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int at = GATED ? rt * 16 : rt * 32 + m * 16;
-      const int r0 = min(at + g, p.H - 1), r1 = min(at + g + 8, p.H - 1);
-      const int64_t row = r0 + (GATED ? (int64_t)m * p.H : 0);
-      r.w[m] = static_cast<const uint8_t*>(p.w) + row * pitch;
-      r.dw[m] = (r1 - r0) * (int)pitch;  // 8 rows: K < 2^26 keeps it in 32 bits
-      if constexpr (WK == kWNvfp4) {
-        r.s[m] = p.blocks + row * (p.K / 16);
-        r.ds[m] = (r1 - r0) * (p.K / 16);
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = min((GATED ? rt * 16 : rt * 32 + m * 16) + g + 8 * h, p.H - 1);
+        const int64_t row = at + (GATED ? (int64_t)m * p.H : 0);
+        r.w[m][h] = static_cast<const uint8_t*>(p.w) + row * pitch + (int64_t)chunk * kWBytes + t * 32;
+        if constexpr (WK == kWNvfp4) r.s[m][h] = p.blocks + row * (p.K / 16) + chunk * kSBytes + t * 4;
       }
-    }
   }
 
-  __device__ __forceinline__ static void load(const MvParams& p, const Rows& r, int chunk, int lane,
+  // the item `d` chunks after r, which stands at chunk `chunk`
+  __device__ __forceinline__ static void load(const MvParams& p, const Rows& r, int chunk, int d, int lane,
                                               Item& it) {
-    const int t = lane & 3;
-    if constexpr (WK == kWBf16) {
-      const int k = chunk * 32 + t * 8;
+    const int left = p.K - (chunk + d) * CK - (lane & 3) * (CK / 4);  // of the row, from this lane's piece on
+    if ((p.K & (CK - 1)) == 0) {  // rows of whole chunks
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ldg_w32(r.w[m][h] + d * kWBytes, it.w[m][h]);
+          if constexpr (WK == kWNvfp4)
+            it.s[m][h] = __ldg(reinterpret_cast<const unsigned*>(r.s[m][h] + d * kSBytes));
+        }
+    } else if constexpr (WK == kWBf16) {
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          it.w[m][h] = k < p.K ? ldg_w16(r.w[m] + (h ? r.dw[m] : 0) + k * 2) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+            it.w[m][h][f] =
+                left > f * 8 ? ldg_w16(r.w[m][h] + d * kWBytes + f * 16) : make_uint4(0, 0, 0, 0);
     } else {
-      // past the row's end the last blocks are read again: the tokens are 0 there
-      const int k = chunk * 128 + t * 32;
-      if ((p.K & 31) == 0) {  // rows of whole 16-byte pieces
-        const int at = min(k, p.K - 32);
+      // past the row's end its last blocks are read again: the tokens are 0 there
+      const bool whole = (p.K & 31) == 0;  // rows of whole 16-byte pieces
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            it.w[m][h] = ldg_w16(r.w[m] + (h ? r.dw[m] : 0) + at / 2);
-            it.s[m][h] =
-                __ldg(reinterpret_cast<const unsigned short*>(r.s[m] + (h ? r.ds[m] : 0) + at / 16));
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* w = r.w[m][h] + d * kWBytes;
+          const uint8_t* sc = r.s[m][h] + d * kSBytes;
+          it.s[m][h] = 0;
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const int o0 = min(f * 32, left - 16), o1 = min(f * 32 + 16, left - 16);  // of two blocks
+            if (whole) {
+              it.w[m][h][f] = ldg_w16(w + min(f * 32, left - 32) / 2);
+            } else {
+              const uint2 lo = ldg_w8(w + o0 / 2), hi = ldg_w8(w + o1 / 2);
+              it.w[m][h][f] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
+            it.s[m][h] |= (__ldg(sc + o0 / 16) | (uint32_t)__ldg(sc + o1 / 16) << 8) << (16 * f);
           }
-      } else {  // an odd number of blocks: rows on 8 bytes
-        const int at0 = min(k, p.K - 16), at1 = min(k + 16, p.K - 16);
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint8_t* w = r.w[m] + (h ? r.dw[m] : 0);
-            const uint8_t* sc = r.s[m] + (h ? r.ds[m] : 0);
-            const uint2 lo = ldg_w8(w + at0 / 2), hi = ldg_w8(w + at1 / 2);
-            it.w[m][h] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-            it.s[m][h] = __ldg(sc + at0 / 16) | (uint32_t)__ldg(sc + at1 / 16) << 8;
-          }
-      }
+        }
     }
   }
+  __device__ __forceinline__ static void advance(Rows& r) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        r.w[m][h] += kDepth * kWBytes;
+        if constexpr (WK == kWNvfp4) r.s[m][h] += kDepth * kSBytes;
+      }
+  }
 
-  // where this lane's fragments of each group of 8 tokens start in a chunk (in 16 bytes); columns
+  // where this lane's fragments of each group of 8 tokens start in a chunk (in bytes); columns
   // without a token read the last token's: their sums are dropped
   __device__ __forceinline__ static void lane_at(int n, int lane, int (&at)[T]) {
 #pragma unroll
-    for (int t = 0; t < T; ++t) at[t] = min(t * 8 + (lane >> 2), n - 1) * 4 + (lane & 3);
+    for (int t = 0; t < T; ++t) at[t] = (min(t * 8 + (lane >> 2), n - 1) * 4 + (lane & 3)) * 16;
   }
 
-  // acc += item x tokens; xs: the chunk's fragments
+  // acc += item x tokens; xs: the chunk's fragments (a shared-memory address:
+  // through a pointer the compiler had lost the address space, 72 against 62
+  // us at 1 x 8192 x 65536), at: this lane's offsets in them
   template <bool WIDE>
-  __device__ __forceinline__ static void compute(const Item& it, const uint4* xs, int n,
+  __device__ __forceinline__ static void compute(const Item& it, uint32_t xs, int n,
                                                  const int (&at)[T], float (&acc)[2][T][4]) {
     if constexpr (WK == kWBf16) {
-      uint4 b[T];
 #pragma unroll
-      for (int t = 0; t < T; ++t) b[t] = xs[at[t]];
+      for (int f = 0; f < 2; ++f) {
+        uint4 b[T];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const uint32_t a0[4] = {it.w[m][0].x, it.w[m][1].x, it.w[m][0].y, it.w[m][1].y};
-        const uint32_t a1[4] = {it.w[m][0].z, it.w[m][1].z, it.w[m][0].w, it.w[m][1].w};
+        for (int t = 0; t < T; ++t) b[t] = lds16(xs + f * 64 * n + at[t]);
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
-          mma16816<false>(acc[m][t], a0, b[t].x, b[t].y);
-          mma16816<false>(acc[m][t], a1, b[t].z, b[t].w);
+        for (int m = 0; m < 2; ++m) {
+          const uint4 &u = it.w[m][0][f], &v = it.w[m][1][f];
+          const uint32_t a0[4] = {u.x, v.x, u.y, v.y};
+          const uint32_t a1[4] = {u.z, v.z, u.w, v.w};
+#pragma unroll
+          for (int t = 0; t < T; ++t) {
+            mma16816<false>(acc[m][t], a0, b[t].x, b[t].y);
+            mma16816<false>(acc[m][t], a1, b[t].z, b[t].w);
+          }
         }
       }
     } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {  // 8 codes of each row
-        uint4 b[T];
+      for (int f = 0; f < 2; ++f) {
+        uint32_t s2[2][2];  // the scales of two blocks
 #pragma unroll
-        for (int t = 0; t < T; ++t) b[t] = xs[q * 4 * n + at[t]];
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint32_t v[2][4];
+          for (int h = 0; h < 2; ++h) s2[m][h] = e4m3x2_f16(f == 0 ? it.s[m][h] : it.s[m][h] >> 16);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t w = q == 0 ? it.w[m][h].x : q == 1 ? it.w[m][h].y : q == 2 ? it.w[m][h].z : it.w[m][h].w;
-            const uint32_t s2 = e4m3x2_f16(it.s[m][h]);
-            const uint32_t s = __byte_perm(s2, 0u, q < 2 ? 0x1010 : 0x3232);
-            e2m1x8_f16(w, v[h]);
+        for (int q = 0; q < 4; ++q) {  // 8 codes of each row
+          uint4 b[T];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[h][i] = mul_f16x2(v[h][i], s);
-              if constexpr (WIDE) {
-                const float2 f = f16x2_f32(v[h][i]);
-                v[h][i] = pack_bf16x2(f.x, f.y);
+          for (int t = 0; t < T; ++t) b[t] = lds16(xs + (f * 4 + q) * 64 * n + at[t]);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            uint32_t v[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4& wq = it.w[m][h][f];
+              const uint32_t w = q == 0 ? wq.x : q == 1 ? wq.y : q == 2 ? wq.z : wq.w;
+              const uint32_t s = __byte_perm(s2[m][h], 0u, q < 2 ? 0x1010 : 0x3232);
+              e2m1x8_f16(w, v[h]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                v[h][i] = mul_f16x2(v[h][i], s);
+                if constexpr (WIDE) {
+                  const float2 g = f16x2_f32(v[h][i]);
+                  v[h][i] = pack_bf16x2(g.x, g.y);
+                }
               }
             }
-          }
-          const uint32_t a0[4] = {v[0][0], v[1][0], v[0][1], v[1][1]};
-          const uint32_t a1[4] = {v[0][2], v[1][2], v[0][3], v[1][3]};
+            const uint32_t a0[4] = {v[0][0], v[1][0], v[0][1], v[1][1]};
+            const uint32_t a1[4] = {v[0][2], v[1][2], v[0][3], v[1][3]};
 #pragma unroll
-          for (int t = 0; t < T; ++t) {
-            mma16816<!WIDE>(acc[m][t], a0, b[t].x, b[t].y);
-            mma16816<!WIDE>(acc[m][t], a1, b[t].z, b[t].w);
+            for (int t = 0; t < T; ++t) {
+              mma16816<!WIDE>(acc[m][t], a0, b[t].x, b[t].y);
+              mma16816<!WIDE>(acc[m][t], a1, b[t].z, b[t].w);
+            }
           }
         }
       }
@@ -298,161 +350,265 @@ __device__ __forceinline__ void finish(const MvParams& p, int n, int col, float 
 }
 
 // the tokens' elements of chunks lo .. hi - 1, in fragment order (zeros past
-// the row's end); returns whether they had to stay bf16 (NVFP4).  inv: what each token's sums are
-// multiplied with.
-template <int WK, int T>
-__device__ bool stage_tokens(const MvParams& p, int lo, int hi, int n0, int n, uint4* xs, float* inv) {
+// the row's end); returns what the sums are to be multiplied with.  *wide:
+// whether they had to stay bf16 (NVFP4).  A thread copies 16-byte pieces, four
+// loads at a time; the largest magnitude and the conversion then take them as
+// they lie in shared memory.
+template <int WK, int T, int W>
+__device__ __forceinline__ void copy_tokens(const MvParams& p, int lo, int hi, int n0, int n, uint32_t xs) {
   using M = Mv<WK, T>;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int k_lo = lo * M::CK;
-  const int pieces = (hi - lo) * M::CK / 8;  // per token, 8 elements each
-  const auto piece = [&](int tok, int q) {
-    const int k = k_lo + q * 8;
-    return k < p.K
-               ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) +
-                                                      (int64_t)(n0 + tok) * p.K + k))
-               : make_uint4(0, 0, 0, 0);
-  };
-  const auto place = [&](int tok, int q) {
-    const int chunk = q / (M::CK / 8), in = q % (M::CK / 8);
-    const int t = in / M::J, j = in % M::J;
-    return xs + ((chunk * M::J + j) * n + tok) * 4 + t;
-  };
-  bool wide = false;
-  for (int tok = warp; tok < n; tok += kMvWarps) {
-    if constexpr (WK == kWBf16) {
-      for (int q = lane; q < pieces; q += 32) *place(tok, q) = piece(tok, q);
-      if (lane == 0) inv[tok] = 1.0f;
-    } else {
-      uint32_t m = 0;  // largest magnitude, as bf16 bits
-      for (int q = lane; q < pieces; q += 32) {
-        const uint4 v = piece(tok, q);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  constexpr int CP = M::CK / 8;  // pieces of a token in a chunk
+  constexpr int kBatch = 4;
+  const int pieces = (hi - lo) * CP;  // per token, 8 elements each
+  const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)n0 * p.K + (int64_t)lo * M::CK;
+  const int left = p.K - lo * M::CK;
+  if (pieces > 0) {
+    const int dt = 32 * W / pieces, dq = 32 * W - dt * pieces;
+    int tok = (int)threadIdx.x / pieces, q = (int)threadIdx.x - tok * pieces;
+#pragma unroll 1
+    while (tok < n) {
+      uint4 v[kBatch];
+      uint32_t to[kBatch];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-      }
-      m = warp_umax(m);
-      // 2^c puts it into [2^14, 2^15); c within what fp32 holds
-      const int c = m == 0u ? 0 : min(126, max(-126, 14 - ((int)(m >> 7) - 127)));
-      const float up = __uint_as_float((uint32_t)(c + 127) << 23);
-      const float down = __uint_as_float((uint32_t)(127 - c) << 23);
-      for (int q = lane; q < pieces; q += 32) {
-        const uint4 v = piece(tok, q);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = bf16x2_f32(w[i]);
-          h[i] = pack_f16x2(f.x * up, f.y * up);
-          const float2 b = f16x2_f32(h[i]);
-          wide |= !(b.x * down == f.x && b.y * down == f.y);
+      for (int u = 0; u < kBatch; ++u) {
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (tok < n && q * 8 < left)
+          v[u] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)tok * p.K + q * 8));
+        to[u] = tok < n ? xs + (((q / CP * M::J + q % M::J) * n + tok) * 4 + q % CP / M::J) * 16 : 0u;
+        q += dq;
+        tok += dt;
+        if (q >= pieces) {
+          q -= pieces;
+          ++tok;
         }
-        *place(tok, q) = make_uint4(h[0], h[1], h[2], h[3]);
       }
-      if (lane == 0) inv[tok] = down;
-    }
-  }
-  if constexpr (WK == kWNvfp4) {
-    wide = __syncthreads_or(wide);
-    if (wide) {
-      for (int tok = warp; tok < n; tok += kMvWarps) {
-        for (int q = lane; q < pieces; q += 32) *place(tok, q) = piece(tok, q);
-        if (lane == 0) inv[tok] = 1.0f;
-      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (to[u] != 0) sts16(to[u], v[u]);
     }
   }
   __syncthreads();
-  return wide;
+}
+
+template <int WK, int T, int W>
+__device__ __forceinline__ float stage_tokens(const MvParams& p, int lo, int hi, int n0, int n, uint32_t xs,
+                                              bool* wide) {
+  copy_tokens<WK, T, W>(p, lo, hi, n0, n, xs);
+  if constexpr (WK == kWBf16) {
+    return 1.0f;
+  } else {
+    __shared__ uint32_t warp_max[W];
+    const int count = (hi - lo) * (Mv<WK, T>::CK / 8) * n;  // 16-byte pieces
+    uint32_t m = 0;                                         // largest magnitude, as bf16 bits
+#pragma unroll 1
+    for (int i = threadIdx.x; i < count; i += 32 * W) {
+      const uint4 v = lds16(xs + i * 16);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) m = max(m, warp_max[w]);
+    // 2^c puts it into [2^14, 2^15); c within what fp32 holds
+    const int c = m == 0u ? 0 : min(126, max(-126, 14 - ((int)(m >> 7) - 127)));
+    const float up = __uint_as_float((uint32_t)(c + 127) << 23);
+    const float down = __uint_as_float((uint32_t)(127 - c) << 23);
+    bool inexact = false;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < count; i += 32 * W) {
+      const uint4 v = lds16(xs + i * 16);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = bf16x2_f32(w[j]);
+        h[j] = pack_f16x2(f.x * up, f.y * up);
+        const float2 r = f16x2_f32(h[j]);
+        inexact |= !(r.x * down == f.x && r.y * down == f.y);
+      }
+      sts16(xs + i * 16, make_uint4(h[0], h[1], h[2], h[3]));
+    }
+    *wide = __syncthreads_or(inexact);
+    if (!*wide) return down;
+    copy_tokens<WK, T, W>(p, lo, hi, n0, n, xs);
+    return 1.0f;
+  }
 }
 
 // one step's sums over this warp's chunks c_lo .. c_hi - 1 of the slab that
-// starts at chunk `lo`.  `it` holds the first items already, and gets the
-// first ones of the rows `next` (chunks n_lo .. n_hi - 1) on the way.
+// starts at chunk `lo`; x: the tokens of chunk c_lo.  The first items are
+// under way (r stands at c_lo), and the first ones of tile next_tile (chunks
+// n_lo .. n_hi - 1) are sent on theirs.
 template <bool GATED, int WK, int T, bool WIDE>
-__device__ __forceinline__ void step_sums(const MvParams& p, int tile, int next_tile, int lane, int n,
-                                          const uint4* xs, int lo, int c_lo, int c_hi, int n_lo, int n_hi,
-                                          const int (&at)[T], Item (&it)[kDepth], float (&acc)[2][T][4]) {
+__device__ __forceinline__ void step_sums(const MvParams& p, int next_tile, int lane, int n, uint32_t x,
+                                          int c_lo, int c_hi, int n_lo, int n_hi,
+                                          const int (&at)[T], Rows& r, Item (&it)[kDepth],
+                                          float (&acc)[2][T][4]) {
   using M = Mv<WK, T>;
-  Rows r;
-  if (c_lo >= c_hi) {  // nothing of this slab
-    M::template rows<GATED>(p, next_tile, lane, r);
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d)
-      if (n_lo + d < n_hi) M::load(p, r, n_lo + d, lane, it[d]);
-    return;
-  }
-  M::template rows<GATED>(p, tile, lane, r);
-  for (int c = c_lo; c < c_hi; c += kDepth) {
+  const int stride = M::J * 64 * n;
+  int c = c_lo;
+  do {
     // a slot's next item: of this step, or the first ones of the next
     const bool last = c + kDepth >= c_hi;
-    if (last) M::template rows<GATED>(p, next_tile, lane, r);
+    if (last)
+      M::template rows<GATED>(p, next_tile, n_lo, lane, r);
+    else
+      M::advance(r);
     const int from = last ? n_lo : c + kDepth, to = last ? n_hi : c_hi;
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-      if (c + d < c_hi) M::template compute<WIDE>(it[d], xs + (c + d - lo) * (M::J * 4 * n), n, at, acc);
-      if (from + d < to) M::load(p, r, from + d, lane, it[d]);
+      if (c + d < c_hi) M::template compute<WIDE>(it[d], x + d * stride, n, at, acc);
+      if (from + d < to) M::load(p, r, from, d, lane, it[d]);
     }
-  }
+    c += kDepth;
+    x += kDepth * stride;
+  } while (c < c_hi);
 }
 
-template <int ACT, int WK, int T>
-__global__ void __launch_bounds__(kMvThreads, 2) rn_matvec_kernel(const MvParams p, const MvPlan pl) {
+// W warps a CTA; 8 warps and few tokens: two CTAs an SM
+template <int ACT, int WK, int T, int W>
+__global__ void __launch_bounds__(32 * W, (T == 1 && W == 8) ? 2 : 1) rn_matvec_kernel(const MvParams p, const MvPlan pl) {
   using M = Mv<WK, T>;
   constexpr bool GATED = ACT != kActNone;
   extern __shared__ uint4 smem[];
-  __shared__ float inv[8 * T];
+  __shared__ __align__(8) uint64_t ready_b[2], free_b[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = pl.split > 1 ? (int)cluster_rank() : 0;
   const int group = (int)blockIdx.x / pl.split, n_groups = (int)gridDim.x / pl.split;
   const int n0 = (int)blockIdx.y * 8 * T;
   const int n = min(8 * T, p.N - n0);
-  const int rw = kMvWarps / pl.kw, wr = warp / pl.kw, wk = warp % pl.kw;
+  const int rw = W / pl.kw, wr = warp / pl.kw, wk = warp % pl.kw;
   const int cols = rw * (GATED ? 16 : 32);  // outputs of a step
-  // tokens; the warps' sums [8][T][8][kPartStride]; in a cluster its CTAs'
-  // sums [split][rw][n][32]; with several slabs the steps' sums [batch][rw][n][32]
-  const int n_max = min(8 * T, p.N);
+  // the tokens; the warps' sums of two steps
+  // [2][warps][n][kPartStride]; in a cluster its CTAs' sums [split][rw][n][32]; with several slabs the steps'
+  // sums [batch][rw][n][32]
+  const int kPart = W * n * kPartStride;  // floats of the warps' sums of a step
   uint4* xs = smem;
-  float* part = reinterpret_cast<float*>(xs + pl.slab * M::J * 4 * n_max);
-  float* parts = part + kMvWarps * T * 8 * kPartStride;
-  const int lo = rank * pl.part, hi = min(lo + pl.part, pl.chunks);
+  float* part = reinterpret_cast<float*>(xs + pl.slab * M::J * 4 * n);
+  float* parts = part + 2 * kPart;
+  const int lo = rank * pl.part, hi = max(lo, min(lo + pl.part, pl.chunks));
   const int slabs = max(1, (hi - lo + pl.slab - 1) / pl.slab);
   const int my_steps = (pl.steps - group + n_groups - 1) / n_groups;
+  const int vals = rw * n * 32;
   // this warp's chunks of slab i: contiguous
   const auto chunk_at = [&](int i, int w) {
-    const int a = min(lo + i * pl.slab, max(lo, hi)), b = min(a + pl.slab, max(lo, hi));
+    const int a = min(lo + i * pl.slab, hi), b = min(a + pl.slab, hi);
     return a + (b - a) * w / pl.kw;
   };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ready_b[i]), W);
+      mbar_init(smem_u32(&free_b[i]), W);
+    }
+    fence_barrier_init();
+  }
   int at[T];
   M::lane_at(n, lane, at);
   const float si = WK == kWNvfp4 ? __ldg(p.scale_inv) : 1.0f;
-  float amax = 0.0f;
+  float amax = 0.0f, inv = 1.0f;
+
+  // The warps' sums of a step are added one step later, while the next
+  // step's weights are on their way: the warps of a CTA meet on two
+  // barriers a buffer (written, read) and may be a step apart.
+  uint32_t used = 0;              // steps whose sums were written
+  int held = -1, held_slab = 0;   // the one that waits to be added
+  const auto add_up = [&]() {
+    const uint32_t u = used - 1, buf = u & 1;
+    mbar_wait(smem_u32(&ready_b[buf]), (u >> 1) & 1, &g_err_mv, kErrReadyWait);
+    const float* from = part + buf * kPart;
+    // one row's sum over the CTA's warps, times what the tokens were scaled by
+    const auto cta_sum = [&](int tile, int tok, int row) {
+      const float* q = from + (tile * pl.kw * n + tok) * kPartStride + row;
+      float v = q[0];
+      for (int w = 1; w < pl.kw; ++w) v += q[w * n * kPartStride];
+      return v * inv;
+    };
+    const int step = group + held * n_groups;
+    if (pl.split == 1) {
+      // with several slabs each thread keeps its outputs' sums
+      float* sums = parts + (size_t)(held % pl.batch) * vals;
+      for (int i = threadIdx.x; i < cols * n; i += 32 * W) {
+        const int tok = i / cols, col = i % cols;
+        float a, b = 0.0f;
+        if constexpr (GATED) {
+          a = cta_sum(col / 16, tok, col % 16);
+          b = cta_sum(col / 16, tok, 16 + col % 16);
+        } else {
+          a = cta_sum(col / 32, tok, col % 32);
+        }
+        if (slabs > 1) {
+          if (held_slab > 0) {
+            a += sums[i];
+            if constexpr (GATED) b += sums[vals / 2 + i];
+          }
+          sums[i] = a;
+          if constexpr (GATED) sums[vals / 2 + i] = b;
+        }
+        if (held_slab + 1 == slabs) finish<ACT>(p, n0 + tok, step * cols + col, a * si, b * si, &amax);
+      }
+    } else {
+      // the steps' sums meet in the cluster's CTAs in turn
+      const int leader = held % pl.split;
+      const uint32_t to = map_to_rank(smem_u32(parts + rank * vals), leader);
+      for (int i = threadIdx.x; i < vals; i += 32 * W)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * 4),
+                     "f"(cta_sum(i / (n * 32), i / 32 % n, i & 31))
+                     : "memory");
+      __syncwarp();
+      cluster_sync();
+      if (rank == leader) {
+        const auto sum = [&](int tile, int tok, int row) {
+          const float* q = parts + (tile * n + tok) * 32 + row;
+          float v = q[0];
+          for (int s = 1; s < pl.split; ++s) v += q[s * vals];
+          return v * si;
+        };
+        for (int i = threadIdx.x; i < cols * n; i += 32 * W) {
+          const int tok = i / cols, col = i % cols;
+          if constexpr (GATED)
+            finish<ACT>(p, n0 + tok, step * cols + col, sum(col / 16, tok, col % 16),
+                        sum(col / 16, tok, 16 + col % 16), &amax);
+          else
+            finish<ACT>(p, n0 + tok, step * cols + col, sum(col / 32, tok, col % 32), 0.0f, &amax);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&free_b[buf]));
+    held = -1;
+  };
 
   Item it[kDepth];
+  Rows r;
   {
     const int c_lo = chunk_at(0, wk), c_hi = chunk_at(0, wk + 1);
-    Rows r;
-    M::template rows<GATED>(p, group * rw + wr, lane, r);
+    M::template rows<GATED>(p, group * rw + wr, c_lo, lane, r);
 #pragma unroll
     for (int d = 0; d < kDepth; ++d)
-      if (c_lo + d < c_hi) M::load(p, r, c_lo + d, lane, it[d]);
+      if (c_lo + d < c_hi) M::load(p, r, c_lo, d, lane, it[d]);
   }
   bool wide = false;
   for (int b0 = 0; b0 < my_steps; b0 += pl.batch) {
     const int b1 = min(b0 + pl.batch, my_steps);
     for (int sl = 0; sl < slabs; ++sl) {
       if (slabs > 1 || b0 == 0) {
+        if (held >= 0) add_up();  // it needs the scales of the slab before
+        __syncthreads();
         const int s_lo = lo + sl * pl.slab;
-        wide = stage_tokens<WK, T>(p, s_lo, max(s_lo, min(s_lo + pl.slab, hi)), n0, n, xs, inv);
+        inv = stage_tokens<WK, T, W>(p, s_lo, max(s_lo, min(s_lo + pl.slab, hi)), n0, n, smem_u32(xs), &wide);
       }
       const int c_lo = chunk_at(sl, wk), c_hi = chunk_at(sl, wk + 1);
+      const uint32_t x = smem_u32(xs) + (c_lo - lo - sl * pl.slab) * (M::J * 64 * n);
       for (int j = b0; j < b1; ++j) {
-        const int step = group + j * n_groups;
         // what follows: the batch's next step, its first with the next slab, the next batch's first
         const bool wrap = j + 1 == b1;
         const int sl2 = wrap ? (sl + 1) % slabs : sl;
         const int j2 = wrap ? (sl + 1 < slabs ? b0 : b1) : j + 1;
         const int n_lo = chunk_at(sl2, wk), n_hi = j2 < my_steps ? chunk_at(sl2, wk + 1) : n_lo;
-        const int next = group + min(j2, my_steps - 1) * n_groups;
+        const int next = (group + min(j2, my_steps - 1) * n_groups) * rw + wr;
         float acc[2][T][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -460,75 +616,40 @@ __global__ void __launch_bounds__(kMvThreads, 2) rn_matvec_kernel(const MvParams
           for (int t = 0; t < T; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[m][t][i] = 0.0f;
-        if (WK == kWNvfp4 && wide)
-          step_sums<GATED, WK, T, true>(p, step * rw + wr, next * rw + wr, lane, n, xs, lo + sl * pl.slab,
-                                        c_lo, c_hi, n_lo, n_hi, at, it, acc);
-        else
-          step_sums<GATED, WK, T, false>(p, step * rw + wr, next * rw + wr, lane, n, xs, lo + sl * pl.slab,
-                                         c_lo, c_hi, n_lo, n_hi, at, it, acc);
-        // this warp's sums: [T][8 tokens][32 rows]
-        float* mine = part + warp * T * 8 * kPartStride;
+        if (c_lo >= c_hi) {  // nothing of this slab for this warp
+          M::template rows<GATED>(p, next, n_lo, lane, r);
+#pragma unroll
+          for (int d = 0; d < kDepth; ++d)
+            if (n_lo + d < n_hi) M::load(p, r, n_lo, d, lane, it[d]);
+        } else if (WK == kWNvfp4 && wide) {
+          step_sums<GATED, WK, T, true>(p, next, lane, n, x, c_lo, c_hi, n_lo, n_hi, at, r, it, acc);
+        } else {
+          step_sums<GATED, WK, T, false>(p, next, lane, n, x, c_lo, c_hi, n_lo, n_hi, at, r, it, acc);
+        }
+        // this warp's sums: [n][32 rows]
+        const uint32_t buf = used & 1;
+        mbar_wait(smem_u32(&free_b[buf]), ((used >> 1) & 1) ^ 1, &g_err_mv, kErrEmptyWait);
+        float* mine = part + buf * kPart + warp * n * kPartStride;
         const int g = lane >> 2, t2 = (lane & 3) * 2;
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mine[(t * 8 + t2 + (i & 1)) * kPartStride + m * 16 + g + (i >> 1) * 8] = acc[m][t][i];
-        __syncthreads();
-        // one row's sum over the CTA's warps, times what its token was scaled by
-        const auto cta_sum = [&](int tile, int tok, int row) {
-          const float* q = part + ((tile * pl.kw) * T * 8 + tok) * kPartStride + row;
-          float v = q[0];
-          for (int w = 1; w < pl.kw; ++w) v += q[w * T * 8 * kPartStride];
-          return v * inv[tok];
-        };
-        // the outputs of the step, from what `sum` gives for a row
-        const auto outputs = [&](auto sum) {
-          for (int i = threadIdx.x; i < cols * n; i += kMvThreads) {
-            const int tok = i / cols, col = i % cols;
-            if constexpr (GATED)
-              finish<ACT>(p, n0 + tok, step * cols + col, sum(col / 16, tok, col % 16) * si,
-                          sum(col / 16, tok, 16 + col % 16) * si, &amax);
-            else
-              finish<ACT>(p, n0 + tok, step * cols + col, sum(col / 32, tok, col % 32) * si, 0.0f, &amax);
-          }
-        };
-        const int vals = rw * n * 32;
-        if (pl.split > 1) {
-          // the steps' sums meet in the cluster's CTAs in turn
-          const int leader = j % pl.split;
-          const uint32_t to = map_to_rank(smem_u32(parts + rank * vals), leader);
-          for (int i = threadIdx.x; i < vals; i += kMvThreads)
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * 4),
-                         "f"(cta_sum(i / (n * 32), i / 32 % n, i & 31))
-                         : "memory");
-          cluster_sync();
-          if (rank == leader)
-            outputs([&](int tile, int tok, int row) {
-              const float* q = parts + (tile * n + tok) * 32 + row;
-              float v = q[0];
-              for (int s = 1; s < pl.split; ++s) v += q[s * vals];
-              return v;
-            });
-        } else if (slabs > 1) {
-          // slab after slab, each thread its own sums
-          float* sums = parts + (j - b0) * vals;
-          for (int i = threadIdx.x; i < vals; i += kMvThreads) {
-            const float v = cta_sum(i / (n * 32), i / 32 % n, i & 31);
-            sums[i] = sl == 0 ? v : sums[i] + v;
-          }
-          __syncthreads();
-          if (sl + 1 == slabs)
-            outputs([&](int tile, int tok, int row) { return sums[(tile * n + tok) * 32 + row]; });
-        } else {
-          outputs(cta_sum);
-          __syncthreads();
-        }
+            for (int i = 0; i < 4; ++i) {
+              const int tok = t * 8 + t2 + (i & 1);
+              if (tok < n) mine[tok * kPartStride + m * 16 + g + (i >> 1) * 8] = acc[m][t][i];
+            }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ready_b[buf]));
+        if (held >= 0) add_up();
+        ++used;
+        held = j;
+        held_slab = sl;
       }
     }
   }
+  if (held >= 0) add_up();
   if (p.mode == kFfnFp8) {
     const float m = warp_max_nan(amax);
     if (lane == 0) {
@@ -539,12 +660,12 @@ __global__ void __launch_bounds__(kMvThreads, 2) rn_matvec_kernel(const MvParams
   if (pl.split > 1) cluster_sync();  // no CTA leaves while another writes to it
 }
 
-constexpr size_t kMvSmemHalf = 112 * 1024;  // two CTAs an SM
+constexpr size_t kMvSmem = 224 * 1024;  // shared memory of a CTA
 
-template <int ACT, int WK, int T>
+template <int ACT, int WK, int T, int W>
 rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
   using M = Mv<WK, T>;
-  auto k = rn_matvec_kernel<ACT, WK, T>;
+  auto k = rn_matvec_kernel<ACT, WK, T, W>;
   constexpr int RO = ACT == kActNone ? 32 : 16;  // outputs of a row tile
   MvPlan pl{};
   pl.chunks = (p.K + M::CK - 1) / M::CK;
@@ -552,48 +673,46 @@ rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
   const int64_t ny = ((int64_t)p.N + 8 * T - 1) / (8 * T);
   const int tiles = (p.H + RO - 1) / RO;
   const size_t chunk_bytes = (size_t)M::J * 4 * n * 16;
-  const size_t warp_bytes = (size_t)kMvWarps * T * 8 * kPartStride * 4;
+  constexpr int PER_SM = T == 1 && W == 8 ? 2 : 1;
+  const size_t fixed_bytes = 2 * (size_t)W * n * kPartStride * 4;
   // few row tiles: the reduction over a cluster, while its CTAs' warps keep
   // two chunks each
   pl.split = 1;
-  while (pl.split < 8 && tiles * ny * pl.split < sms && pl.chunks >= 4 * kMvWarps * pl.split) pl.split *= 2;
+  while (pl.split < 8 && tiles * ny * pl.split < sms && pl.chunks >= 2 * W * pl.split) pl.split *= 2;
   pl.part = (pl.chunks + pl.split - 1) / pl.split;
   // warps along the reduction: fewer where it is short and the rows are many
   // (an MXFP8 block needs two row tiles a step)
-  pl.kw = p.mode == kFfnMx ? kMvWarps / 2 : kMvWarps;
+  pl.kw = p.mode == kFfnMx ? W / 2 : W;
   while (pl.kw > 1 && pl.part < kDepth * pl.kw &&
-         (int64_t)tiles * ny * pl.split * pl.kw >= 2ll * sms * kMvWarps)
+         (int64_t)tiles * ny * pl.split * pl.kw >= (int64_t)sms * W)
     pl.kw /= 2;
-  const int rw = kMvWarps / pl.kw;
+  const int rw = W / pl.kw;
   pl.steps = (tiles + rw - 1) / rw;
   const size_t step_bytes = (size_t)rw * n * 32 * 4;
-  int per = (2 * sms) / pl.split;  // clusters or CTAs of one token group
+  // the tokens whole where there is room; else in slabs (and no cluster)
+  pl.slab = pl.part;
+  size_t cluster_bytes = pl.split > 1 ? pl.split * step_bytes : 0;
+  if (pl.slab * chunk_bytes + fixed_bytes + cluster_bytes > kMvSmem / PER_SM) {
+    pl.split = 1;
+    pl.part = pl.slab = pl.chunks;
+    cluster_bytes = 0;
+  }
+  int per = PER_SM * sms / pl.split;  // clusters or CTAs of one token group
   if (per > pl.steps) per = pl.steps;
   if (per < 1) per = 1;
-  const int my_steps = (pl.steps + per - 1) / per;
-  size_t room = kMvSmemHalf - warp_bytes - (pl.split > 1 ? pl.split * step_bytes : 0);
-  pl.slab = pl.part;
-  pl.batch = my_steps;
+  pl.batch = (pl.steps + per - 1) / per;
+  const size_t room = kMvSmem / PER_SM - fixed_bytes - cluster_bytes;
   if (pl.slab * chunk_bytes > room) {
-    if (pl.split > 1) {  // then the rows are few: no cluster, several slabs
-      pl.split = 1;
-      pl.part = pl.chunks;
-      room = kMvSmemHalf - warp_bytes;
-      per = 2 * sms < pl.steps ? 2 * sms : pl.steps;
-    }
-    pl.batch = (pl.steps + per - 1) / per;
-    if (pl.slab * chunk_bytes > room || pl.part != pl.slab) {
-      // a third of the room at most for the steps' sums
-      const int fit = (int)(room / 3 / step_bytes);
-      if (pl.batch > fit) pl.batch = fit;
-      if (pl.batch < 1) return RN_ERR_UNSUPPORTED;
-      pl.slab = (int)((room - pl.batch * step_bytes) / chunk_bytes);
-      if (pl.slab < 1) return RN_ERR_UNSUPPORTED;
-      const int slabs = (pl.part + pl.slab - 1) / pl.slab;
-      pl.slab = (pl.part + slabs - 1) / slabs;
-    }
+    // a third of the room at most for the steps' sums
+    const int fit = (int)(room / 3 / step_bytes);
+    if (pl.batch > fit) pl.batch = fit;
+    if (pl.batch < 1) return RN_ERR_UNSUPPORTED;
+    pl.slab = (int)((room - pl.batch * step_bytes) / chunk_bytes);
+    if (pl.slab < 1) return RN_ERR_UNSUPPORTED;
+    const int slabs = (pl.part + pl.slab - 1) / pl.slab;
+    pl.slab = (pl.part + slabs - 1) / slabs;
   }
-  size_t smem = pl.slab * chunk_bytes + warp_bytes;
+  size_t smem = pl.slab * chunk_bytes + fixed_bytes;
   if (pl.split > 1)
     smem += pl.split * step_bytes;
   else if (pl.slab < pl.part)
@@ -604,7 +723,7 @@ rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
   const int groups = per;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(groups * pl.split), (unsigned)ny);
-  cfg.blockDim = dim3(kMvThreads);
+  cfg.blockDim = dim3(32 * W);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -630,9 +749,12 @@ rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
 // groups of 8, 16 or 32 tokens
 template <int ACT, int WK>
 rn_status launch_n(const MvParams& p, int sms, cudaStream_t s) {
-  if (p.N <= 8) return launch_t<ACT, WK, 1>(p, sms, s);
-  if (p.N <= 16) return launch_t<ACT, WK, 2>(p, sms, s);
-  return launch_t<ACT, WK, 4>(p, sms, s);
+  // up to 8 tokens: two CTAs an SM of 8 warps while their tokens are small
+  // (each CTA stages its own), else one of 16
+  if (p.N <= 8 && (int64_t)p.N * p.K <= 40960) return launch_t<ACT, WK, 1, 8>(p, sms, s);
+  if (p.N <= 8) return launch_t<ACT, WK, 1, 16>(p, sms, s);
+  if (p.N <= 16) return launch_t<ACT, WK, 2, 16>(p, sms, s);
+  return launch_t<ACT, WK, 4, 8>(p, sms, s);
 }
 
 }  // namespace
@@ -648,6 +770,14 @@ rn_status launch_nvfp4_mv(int act, const MvParams& p, int sms, cudaStream_t s) {
 rn_status launch_bf16_mv(int act, const MvParams& p, int sms, cudaStream_t s) {
   return act == kActSwiglu ? launch_n<kActSwiglu, kWBf16>(p, sms, s)
                            : launch_n<kActClampedSwiglu, kWBf16>(p, sms, s);
+}
+
+rn_status read_clear_error_mv(unsigned* code) {
+  unsigned v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_mv, sizeof(v)) != cudaSuccess) return RN_ERR_CUDA;
+  if (cudaMemcpyToSymbol(g_err_mv, &zero, sizeof(zero)) != cudaSuccess) return RN_ERR_CUDA;
+  *code = v;
+  return RN_OK;
 }
 
 }  // namespace rn
