@@ -981,7 +981,7 @@ rn_status rn_gated_ffn_fwd(rn_act act, const void* x, const void* w, rn_dtype dt
   if (kind == kFfnFp8 && (st = launch_fwd_init(out->amax, out->scale, out->scale_inv, s)) != RN_OK)
     return st;
   if (N == 0) return RN_OK;
-  if (N <= kFewTokens && K <= kMvMaxK) {
+  if (few_tokens(N, H) && K <= kMvMaxK) {
     MvParams m{};
     m.x = x;
     m.w = w;

@@ -41,8 +41,12 @@ __device__ unsigned g_err_mv;
 
 constexpr int kWBytes = 128;     // of a row's weights in a chunk
 constexpr int kSBytes = 16;      // of its scales (NVFP4)
-constexpr int kDepth = 1;        // items in flight per warp
 constexpr int kPartStride = 36;  // floats per token of a warp's sums (32 rows, no bank conflicts)
+
+// items in flight per warp: two only with 32 tokens, where a CTA is 8 warps of
+// up to 255 registers
+template <int T>
+constexpr int kDepth = T == 4 ? 2 : 1;
 
 enum WeightKind : int { kWBf16 = 0, kWNvfp4 = 1 };
 
@@ -234,8 +238,8 @@ struct Mv {
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        r.w[m][h] += kDepth * kWBytes;
-        if constexpr (WK == kWNvfp4) r.s[m][h] += kDepth * kSBytes;
+        r.w[m][h] += kDepth<T> * kWBytes;
+        if constexpr (WK == kWNvfp4) r.s[m][h] += kDepth<T> * kSBytes;
       }
   }
 
@@ -445,26 +449,26 @@ __device__ __forceinline__ float stage_tokens(const MvParams& p, int lo, int hi,
 template <bool GATED, int WK, int T, bool WIDE>
 __device__ __forceinline__ void step_sums(const MvParams& p, int next_tile, int lane, int n, uint32_t x,
                                           int c_lo, int c_hi, int n_lo, int n_hi,
-                                          const int (&at)[T], Rows& r, Item (&it)[kDepth],
+                                          const int (&at)[T], Rows& r, Item (&it)[kDepth<T>],
                                           float (&acc)[2][T][4]) {
   using M = Mv<WK, T>;
   const int stride = M::J * 64 * n;
   int c = c_lo;
   do {
     // a slot's next item: of this step, or the first ones of the next
-    const bool last = c + kDepth >= c_hi;
+    const bool last = c + kDepth<T> >= c_hi;
     if (last)
       M::template rows<GATED>(p, next_tile, n_lo, lane, r);
     else
       M::advance(r);
-    const int from = last ? n_lo : c + kDepth, to = last ? n_hi : c_hi;
+    const int from = last ? n_lo : c + kDepth<T>, to = last ? n_hi : c_hi;
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
+    for (int d = 0; d < kDepth<T>; ++d) {
       if (c + d < c_hi) M::template compute<WIDE>(it[d], x + d * stride, n, at, acc);
       if (from + d < to) M::load(p, r, from, d, lane, it[d]);
     }
-    c += kDepth;
-    x += kDepth * stride;
+    c += kDepth<T>;
+    x += kDepth<T> * stride;
   } while (c < c_hi);
 }
 
@@ -581,13 +585,13 @@ __global__ void __launch_bounds__(32 * W, (T == 1 && W == 8) ? 2 : 1) rn_matvec_
     held = -1;
   };
 
-  Item it[kDepth];
+  Item it[kDepth<T>];
   Rows r;
   {
     const int c_lo = chunk_at(0, wk), c_hi = chunk_at(0, wk + 1);
     M::template rows<GATED>(p, group * rw + wr, c_lo, lane, r);
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d)
+    for (int d = 0; d < kDepth<T>; ++d)
       if (c_lo + d < c_hi) M::load(p, r, c_lo, d, lane, it[d]);
   }
   bool wide = false;
@@ -619,7 +623,7 @@ __global__ void __launch_bounds__(32 * W, (T == 1 && W == 8) ? 2 : 1) rn_matvec_
         if (c_lo >= c_hi) {  // nothing of this slab for this warp
           M::template rows<GATED>(p, next, n_lo, lane, r);
 #pragma unroll
-          for (int d = 0; d < kDepth; ++d)
+          for (int d = 0; d < kDepth<T>; ++d)
             if (n_lo + d < n_hi) M::load(p, r, n_lo, d, lane, it[d]);
         } else if (WK == kWNvfp4 && wide) {
           step_sums<GATED, WK, T, true>(p, next, lane, n, x, c_lo, c_hi, n_lo, n_hi, at, r, it, acc);
@@ -681,28 +685,30 @@ rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
   while (pl.split < 8 && tiles * ny * pl.split < sms && pl.chunks >= 2 * W * pl.split) pl.split *= 2;
   pl.part = (pl.chunks + pl.split - 1) / pl.split;
   // warps along the reduction: fewer where it is short and the rows are many
-  // (an MXFP8 block needs two row tiles a step)
+  // (an MXFP8 block needs two row tiles a step), or where its slabs are short
   pl.kw = p.mode == kFfnMx ? W / 2 : W;
-  while (pl.kw > 1 && pl.part < kDepth * pl.kw &&
-         (int64_t)tiles * ny * pl.split * pl.kw >= (int64_t)sms * W)
+  while (pl.kw > 1 && pl.part < kDepth<T> * pl.kw && (int64_t)tiles * ny * pl.split * pl.kw >= (int64_t)sms * W)
     pl.kw /= 2;
-  const int rw = W / pl.kw;
-  pl.steps = (tiles + rw - 1) / rw;
-  const size_t step_bytes = (size_t)rw * n * 32 * 4;
-  // the tokens whole where there is room; else in slabs (and no cluster)
-  pl.slab = pl.part;
-  size_t cluster_bytes = pl.split > 1 ? pl.split * step_bytes : 0;
-  if (pl.slab * chunk_bytes + fixed_bytes + cluster_bytes > kMvSmem / PER_SM) {
-    pl.split = 1;
-    pl.part = pl.slab = pl.chunks;
-    cluster_bytes = 0;
-  }
-  int per = PER_SM * sms / pl.split;  // clusters or CTAs of one token group
-  if (per > pl.steps) per = pl.steps;
-  if (per < 1) per = 1;
-  pl.batch = (pl.steps + per - 1) / per;
-  const size_t room = kMvSmem / PER_SM - fixed_bytes - cluster_bytes;
-  if (pl.slab * chunk_bytes > room) {
+  size_t step_bytes = 0;
+  int per = 1;
+  for (;; pl.kw /= 2) {
+    const int rw = W / pl.kw;
+    pl.steps = (tiles + rw - 1) / rw;
+    step_bytes = (size_t)rw * n * 32 * 4;
+    // the tokens whole where there is room; else in slabs (and no cluster)
+    pl.slab = pl.part;
+    size_t cluster_bytes = pl.split > 1 ? pl.split * step_bytes : 0;
+    if (pl.slab * chunk_bytes + fixed_bytes + cluster_bytes > kMvSmem / PER_SM) {
+      pl.split = 1;
+      pl.part = pl.slab = pl.chunks;
+      cluster_bytes = 0;
+    }
+    per = PER_SM * sms / pl.split;  // clusters or CTAs of one token group
+    if (per > pl.steps) per = pl.steps;
+    if (per < 1) per = 1;
+    pl.batch = (pl.steps + per - 1) / per;
+    const size_t room = kMvSmem / PER_SM - fixed_bytes - cluster_bytes;
+    if (pl.slab * chunk_bytes <= room) break;
     // a third of the room at most for the steps' sums
     const int fit = (int)(room / 3 / step_bytes);
     if (pl.batch > fit) pl.batch = fit;
@@ -711,6 +717,7 @@ rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
     if (pl.slab < 1) return RN_ERR_UNSUPPORTED;
     const int slabs = (pl.part + pl.slab - 1) / pl.slab;
     pl.slab = (pl.part + slabs - 1) / slabs;
+    if (pl.slab >= kDepth<T> * pl.kw || pl.kw == 1) break;
   }
   size_t smem = pl.slab * chunk_bytes + fixed_bytes;
   if (pl.split > 1)
@@ -753,7 +760,7 @@ rn_status launch_n(const MvParams& p, int sms, cudaStream_t s) {
   // (each CTA stages its own), else one of 16
   if (p.N <= 8 && (int64_t)p.N * p.K <= 40960) return launch_t<ACT, WK, 1, 8>(p, sms, s);
   if (p.N <= 8) return launch_t<ACT, WK, 1, 16>(p, sms, s);
-  if (p.N <= 16) return launch_t<ACT, WK, 2, 16>(p, sms, s);
+  if (p.N <= 16) return launch_t<ACT, WK, 2, 8>(p, sms, s);
   return launch_t<ACT, WK, 4, 8>(p, sms, s);
 }
 
