@@ -157,7 +157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t full_b[kStages], empty_b[kStages], done_b[2], free_b[2];
   __shared__ uint32_t tmem_at;
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int cluster = (int)(blockIdx.x >> 1), n_clusters = (int)(gridDim.x >> 1);
   int total = 0;
@@ -183,7 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   bool ok = true;
   if (warp == 0) {
-    if (lane == 0) {
+    {
       RingPos r{0, 0};
       for (int t = cluster; t < total && ok; t += n_clusters) {
         const Tile tl = tile_at(p, t);
@@ -194,12 +194,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int n0 = ACT == kActNone ? tl.n * 256 + (int)rank * 128
                                        : tl.n * 128 + (int)rank * p.f.H;
         for (int k = 0; k < j.slices; ++k) {
-          if (!mbar_wait(smem_u32(&empty_b[r.slot]), r.phase ^ 1u, &g_err_ffn, kErrEmptyWait)) {
+          if (!mbar_wait_warp(smem_u32(&empty_b[r.slot]), r.phase ^ 1u, &g_err_ffn, kErrEmptyWait)) {
             ok = false;
             break;
           }
           const uint32_t bar = map_to_rank(smem_u32(&full_b[r.slot]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_b[r.slot]), 2 * kStageBytes);
+          if (rank == 0) mbar_expect_elected(smem_u32(&full_b[r.slot]), 2 * kStageBytes);
           const uint32_t sa = ring + r.slot * kStageBytes, sb = sa + kOperandBytes;
           if (j.a_mn) {
             tma_load_2d(sa, ma, m0, k * 64, bar);
@@ -218,7 +218,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       RingPos r{0, 0};
       int it = 0;
       for (int t = cluster; t < total && ok; t += n_clusters, ++it) {
@@ -227,13 +227,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t idesc =
             kIdesc256 | (j.a_mn ? kIdescAMN : 0u) | (j.b_mn ? kIdescBMN : 0u);
         const uint64_t da = smem_desc_step(j.a_mn), db = smem_desc_step(j.b_mn);
-        if (!mbar_wait(smem_u32(&free_b[acc]), ((it >> 1) & 1) ^ 1u, &g_err_ffn, kErrReadyWait)) {
+        if (!mbar_wait_warp(smem_u32(&free_b[acc]), ((it >> 1) & 1) ^ 1u, &g_err_ffn, kErrReadyWait)) {
           ok = false;
           break;
         }
         tc_fence_after();
         for (int k = 0; k < j.slices; ++k) {
-          if (!mbar_wait(smem_u32(&full_b[r.slot]), r.phase, &g_err_ffn, kErrFullWait)) {
+          if (!mbar_wait_warp(smem_u32(&full_b[r.slot]), r.phase, &g_err_ffn, kErrFullWait)) {
             ok = false;
             break;
           }
@@ -262,9 +262,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Tile tl = tile_at(p, t);
       const Job& j = p.job[tl.job];
       const uint32_t acc = it & 1;
-      if (!mbar_wait(smem_u32(&done_b[acc]), (it >> 1) & 1, &g_err_ffn, kErrStatsWait)) ok = false;
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
+      if (!mbar_wait_warp(smem_u32(&done_b[acc]), (it >> 1) & 1, &g_err_ffn, kErrStatsWait)) {
+        ok = false;
+        break;
+      }
       tc_fence_after();
       const int64_t row = (int64_t)tl.m * 256 + rank * 128 + lb + lane;
       const uint32_t ta = tmem + acc * 256 + ((uint32_t)lb << 16);
