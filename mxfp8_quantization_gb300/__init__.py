@@ -134,6 +134,18 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+# the current stream's handle without the Stream object around it (3 us of a
+# small call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _ok(t, dev, dtype, shape):
+    """Whether ``_need`` would take the tensor; the calls below ask it first, as it is the cheaper."""
+    return (t is not None and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+            and t.device.index == dev)
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return _BF16
@@ -384,11 +396,20 @@ def _gated(act):
     return ACTS[act]
 
 
-def _matrix(t, name, dtype=torch.bfloat16):
-    _need(t, name, dtype)
-    if t.dim() != 2:
+def _matrix(t, name, dev, dtype=torch.bfloat16):
+    if t is None or len(t.shape) != 2 or not _ok(t, dev, dtype, t.shape):
+        _need(t, name, dtype)
         raise RNError(f"{name} must have 2 dimensions, got {t.dim()}")
     return t.shape
+
+
+def _take(t, name, dev, dtype, shape):
+    if not _ok(t, dev, dtype, shape):
+        _need(t, name, dtype, shape)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 @dataclass
@@ -406,26 +427,33 @@ def _make_rows_output(x, N, H, quant, out_dtype, scale):
     return _make_output(_Like((N, H), x.dtype, x.device), quant, out_dtype, scale, True, False)
 
 
+def _ffn_weights(w, K, dev):
+    R = _matrix(w, "w", dev)[0]
+    if R % 2 or w.shape[1] != K:
+        raise RNError(f"w must have shape (2 H, {K}), got {tuple(w.shape)}")
+    return R
+
+
 def gated_ffn_fwd(x, w, act="swiglu", scales=None, quant="none", limit=7.0, alpha=1.702, scale=None,
                   out_dtype=None, save_pre=False):
     """y = scales[:, None] * act(x @ w[:H].T, x @ w[H:].T): x bf16 [N, K], w bf16 [2H, K] (gate rows,
     then linear rows), act "swiglu" or "clamped_swiglu" -> (output, pre); output per ``quant``
     ("none", "fp8_delayed", "mxfp8" rowwise), pre the projections bf16 [N, 2H] for
     ``gated_ffn_bwd``, or None without ``save_pre``."""
-    lib = _load()
+    lib = _lib or _load()
     code = _gated(act)
-    N, K = _matrix(x, "x")
-    R, _ = _matrix(w, "w")
-    if R % 2 or tuple(w.shape) != (R, K):
-        raise RNError(f"w must have shape (2 H, {K}), got {tuple(w.shape)}")
+    dev = torch.cuda.current_device()
+    N, K = _matrix(x, "x", dev)
+    R = _ffn_weights(w, K, dev)
     H = R // 2
     if scales is not None:
-        _need(scales, "scales", torch.float32, (N,))
+        _take(scales, "scales", dev, torch.float32, (N,))
     o, res = _make_rows_output(x, N, H, quant, out_dtype, scale)
     pre = torch.empty((N, R), dtype=x.dtype, device=x.device) if save_pre else None
-    st = lib.rn_gated_ffn_fwd(code, _ptr(x), _ptr(w), _BF16, _ptr(scales), N, K, H, float(limit),
-                              float(alpha), QUANT_MODES[quant], ctypes.byref(o), _ptr(pre), _stream())
-    _check(st, "rn_gated_ffn_fwd")
+    st = lib.rn_gated_ffn_fwd(code, x.data_ptr(), w.data_ptr(), _BF16, _addr(scales), N, K, H, limit,
+                              alpha, QUANT_MODES[quant], ctypes.byref(o), _addr(pre), _raw_stream(dev))
+    if st:
+        _check(st, "rn_gated_ffn_fwd")
     return res, pre
 
 
@@ -442,54 +470,57 @@ def gated_ffn_bwd(dy, x, w, pre, act="swiglu", scales=None, limit=7.0, alpha=1.7
                   workspace=None, need_dx=True, need_dw=True):
     """Backward of ``gated_ffn_fwd`` at its ``pre``: dy bf16 [N, H] -> (dx bf16 [N, K] or None, dw
     bf16 [2H, K] or None, dscales fp32 [N] or None); ``need_dx`` / ``need_dw`` / ``dscales`` select."""
-    lib = _load()
+    lib = _lib or _load()
     code = _gated(act)
-    N, K = _matrix(x, "x")
-    R, _ = _matrix(w, "w")
-    if R % 2 or tuple(w.shape) != (R, K):
-        raise RNError(f"w must have shape (2 H, {K}), got {tuple(w.shape)}")
+    dev = torch.cuda.current_device()
+    N, K = _matrix(x, "x", dev)
+    R = _ffn_weights(w, K, dev)
     H = R // 2
-    _need(dy, "dy", torch.bfloat16, (N, H))
-    _need(pre, "pre", torch.bfloat16, (N, R))
+    _take(dy, "dy", dev, torch.bfloat16, (N, H))
+    _take(pre, "pre", dev, torch.bfloat16, (N, R))
     if scales is not None:
-        _need(scales, "scales", torch.float32, (N,))
-    need = gated_ffn_bwd_workspace_bytes(N, K, H)
+        _take(scales, "scales", dev, torch.float32, (N,))
+    if not (need_dx or need_dw or dscales):
+        raise RNError("nothing to compute: dx, dw and dscales are all skipped")
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        workspace = torch.empty(max(gated_ffn_bwd_workspace_bytes(N, K, H), 16), dtype=torch.uint8,
+                                device=x.device)
     else:
         _need(workspace, "workspace")
     n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
-    dx = torch.empty_like(x) if need_dx else None
-    dw = torch.empty_like(w) if need_dw else None
+    dx = torch.empty((N, K), dtype=x.dtype, device=x.device) if need_dx else None
+    dw = torch.empty((R, K), dtype=x.dtype, device=x.device) if need_dw else None
     ds = torch.empty(N, dtype=torch.float32, device=x.device) if dscales else None
-    if dx is None and dw is None and ds is None:
-        raise RNError("nothing to compute: dx, dw and dscales are all skipped")
-    st = lib.rn_gated_ffn_bwd(code, _ptr(dy), _ptr(x), _ptr(w), _ptr(pre), _BF16, _ptr(scales), N, K, H,
-                              float(limit), float(alpha), _ptr(dx), _ptr(dw), _ptr(ds),
-                              _ptr(workspace), ctypes.byref(n), _stream())
-    _check(st, "rn_gated_ffn_bwd")
+    st = lib.rn_gated_ffn_bwd(code, dy.data_ptr(), x.data_ptr(), w.data_ptr(), pre.data_ptr(), _BF16,
+                              _addr(scales), N, K, H, limit, alpha, _addr(dx), _addr(dw), _addr(ds),
+                              workspace.data_ptr(), ctypes.byref(n), _raw_stream(dev))
+    if st:
+        _check(st, "rn_gated_ffn_bwd")
     return dx, dw, ds
 
 
-def _nvfp4_weights(x, w):
-    N, K = _matrix(x, "x")
-    R, half = _matrix(w.data, "w.data", torch.uint8)
+def _nvfp4_weights(x, w, dev):
+    N, K = _matrix(x, "x", dev)
+    R, half = _matrix(w.data, "w.data", dev, torch.uint8)
     if K % 16 or half * 2 != K:
         raise RNError(f"w must hold rows of {K} elements (a multiple of 16), got {2 * half}")
-    _need(w.row_scales, "w.row_scales", torch.uint8, (R, K // 16))
-    _need(w.scale_inv, "w.scale_inv", torch.float32, (1,))
+    _take(w.row_scales, "w.row_scales", dev, torch.uint8, (R, K // 16))
+    _take(w.scale_inv, "w.scale_inv", dev, torch.float32, (1,))
     return N, K, R
 
 
 def nvfp4_matvec(x, w, out_dtype=None):
     """y = x @ W.T for one or a few tokens: x bf16 [N, K], w the ``NVFP4Output`` of a weight matrix
     [R, K] -> y [N, R] in ``out_dtype`` (x's by default, or float32)."""
-    lib = _load()
-    N, K, R = _nvfp4_weights(x, w)
+    lib = _lib or _load()
+    dev = torch.cuda.current_device()
+    N, K, R = _nvfp4_weights(x, w, dev)
     y = torch.empty((N, R), dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
-    st = lib.rn_nvfp4_matvec(_ptr(x), _BF16, _ptr(w.data), _ptr(w.row_scales), _ptr(w.scale_inv), N, K,
-                             R, _dtype_code(y), _ptr(y), _stream())
-    _check(st, "rn_nvfp4_matvec")
+    st = lib.rn_nvfp4_matvec(x.data_ptr(), _BF16, w.data.data_ptr(), w.row_scales.data_ptr(),
+                             w.scale_inv.data_ptr(), N, K, R, _dtype_code(y), y.data_ptr(),
+                             _raw_stream(dev))
+    if st:
+        _check(st, "rn_nvfp4_matvec")
     return y
 
 
@@ -497,18 +528,21 @@ def nvfp4_gated_ffn(x, w, act="swiglu", scales=None, quant="none", limit=7.0, al
                     out_dtype=None):
     """``gated_ffn_fwd`` for one or a few tokens with NVFP4 weights: w the ``NVFP4Output`` of a
     weight matrix [2H, K] (gate rows, then linear rows) -> output per ``quant``."""
-    lib = _load()
+    lib = _lib or _load()
     code = _gated(act)
-    N, K, R = _nvfp4_weights(x, w)
+    dev = torch.cuda.current_device()
+    N, K, R = _nvfp4_weights(x, w, dev)
     if R % 2:
         raise RNError(f"w must have an even number of rows, got {R}")
     if scales is not None:
-        _need(scales, "scales", torch.float32, (N,))
+        _take(scales, "scales", dev, torch.float32, (N,))
     o, res = _make_rows_output(x, N, R // 2, quant, out_dtype, scale)
-    st = lib.rn_nvfp4_gated_ffn(code, _ptr(x), _BF16, _ptr(w.data), _ptr(w.row_scales),
-                                _ptr(w.scale_inv), _ptr(scales), N, K, R // 2, float(limit),
-                                float(alpha), QUANT_MODES[quant], ctypes.byref(o), _stream())
-    _check(st, "rn_nvfp4_gated_ffn")
+    st = lib.rn_nvfp4_gated_ffn(code, x.data_ptr(), _BF16, w.data.data_ptr(),
+                                w.row_scales.data_ptr(), w.scale_inv.data_ptr(), _addr(scales), N, K,
+                                R // 2, limit, alpha, QUANT_MODES[quant], ctypes.byref(o),
+                                _raw_stream(dev))
+    if st:
+        _check(st, "rn_nvfp4_gated_ffn")
     return res
 
 

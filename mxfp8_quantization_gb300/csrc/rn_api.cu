@@ -10,7 +10,6 @@
 namespace rn {
 namespace {
 
-constexpr int kMaxDevices = 64;
 std::atomic<int> g_sms[kMaxDevices];
 std::atomic<int> g_smem[kMaxDevices];
 std::atomic<int> g_smem_sm[kMaxDevices];

@@ -361,9 +361,6 @@ int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 template <int ACT, int MODE>
 rn_status launch(const GemmParams& p, const Maps& maps, int sms, bool pdl, cudaStream_t s) {
   auto k = rn_ffn_kernel<ACT, MODE>;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
-      cudaSuccess)
-    return RN_ERR_CUDA;
   int64_t total = 0;
   for (int j = 0; j < p.n_jobs; ++j) total += (int64_t)p.job[j].tiles_m * p.job[j].tiles_n;
   if (total > INT32_MAX / 2) return RN_ERR_UNSUPPORTED;
@@ -372,10 +369,16 @@ rn_status launch(const GemmParams& p, const Maps& maps, int sms, bool pdl, cudaS
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
-  cfg.gridDim = dim3((unsigned)sms / 2 * 2);
-  int resident = 0;
-  if (cudaOccupancyMaxActiveClusters(&resident, k, &cfg) != cudaSuccess) return RN_ERR_CUDA;
-  if (resident < 1) return RN_ERR_UNSUPPORTED;
+  // clusters that run at the same time; the shared-memory limit is raised first
+  static std::atomic<int> kept[kMaxDevices];
+  const int resident = once_per_device(kept, [&] {
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess)
+      return -1;
+    cfg.gridDim = dim3((unsigned)sms / 2 * 2);
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, k, &cfg) == cudaSuccess && n > 0 ? n : -1;
+  });
+  if (resident < 1) return RN_ERR_CUDA;
   cfg.gridDim = dim3(2u * (unsigned)(total < resident ? total : resident));
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -2,6 +2,7 @@
 // parameter blocks, launch plans and the per-unit launch functions.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -187,6 +188,21 @@ struct DeviceInfo {
   int smem_per_sm;      // per SM
 };
 rn_status device_info(DeviceInfo* out);
+
+// A value found out once per device and kept (0: not yet); `find` gives a
+// positive value, or a negative one on failure, which is not kept.
+constexpr int kMaxDevices = 64;
+template <class Find>
+int once_per_device(std::atomic<int> (&kept)[kMaxDevices], Find find) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
+  int v = kept[dev].load(std::memory_order_acquire);
+  if (v <= 0) {
+    v = find();
+    if (v > 0) kept[dev].store(v, std::memory_order_release);
+  }
+  return v;
+}
 
 // Grid of a persistent kernel: min(work, sms * CTAs per SM), where CTAs per
 // SM is the planned count capped by what the kernel's resources allow.

@@ -724,7 +724,12 @@ rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
     smem += pl.split * step_bytes;
   else if (pl.slab < pl.part)
     smem += pl.batch * step_bytes;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  static std::atomic<int> kept[kMaxDevices];
+  if (once_per_device(kept, [&] {
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMvSmem) == cudaSuccess
+                   ? 1
+                   : -1;
+      }) < 1)
     return RN_ERR_CUDA;
   if (ny > 65535) return RN_ERR_UNSUPPORTED;
   const int groups = per;
