@@ -40,7 +40,8 @@ __device__ unsigned g_err_ffn;
 constexpr int kStages = 6;
 constexpr int kOperandBytes = 16384;              // 128 x 64 bf16
 constexpr int kStageBytes = 2 * kOperandBytes;    // A and B of one CTA
-constexpr int kThreads = 192;                     // copies, products, 4 epilogue warps
+constexpr int kEpiWarps = 8;                      // two for each 32 lanes of tensor memory
+constexpr int kThreads = 64 + 32 * kEpiWarps;     // and one warp each for copies and products
 constexpr size_t kSmemBytes = (size_t)kStages * kStageBytes + 1024;
 
 // one product of the launch: tiles of 256 x 256 (forward: 256 x 128 outputs)
@@ -86,33 +87,52 @@ __device__ __forceinline__ Tile tile_at(const GemmParams& p, int t) {
   return r;
 }
 
+// 16 columns of one row in one 32-byte store; `o` is 32-byte aligned
+__device__ __forceinline__ void store16_bf16(void* o, const float* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o),
+               "r"(pack_bf16x2(v[0], v[1])), "r"(pack_bf16x2(v[2], v[3])), "r"(pack_bf16x2(v[4], v[5])),
+               "r"(pack_bf16x2(v[6], v[7])), "r"(pack_bf16x2(v[8], v[9])),
+               "r"(pack_bf16x2(v[10], v[11])), "r"(pack_bf16x2(v[12], v[13])),
+               "r"(pack_bf16x2(v[14], v[15]))
+               : "memory");
+}
+
 // 8 columns of one row; `o` is 16-byte aligned
 __device__ __forceinline__ void store8_bf16(void* o, const float* v) {
   *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
+// 32 columns of one row, of which `left` exist (a multiple of 8); wide: rows
+// of whole 32 bytes, on 32 bytes
+__device__ __forceinline__ void store32_bf16(uint16_t* o, const float* v, int left, bool wide) {
+  if (wide) {
+#pragma unroll
+    for (int q = 0; q < 32; q += 16)
+      if (q < left) store16_bf16(o + q, v + q);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 32; q += 8)
+      if (q < left) store8_bf16(o + q, v + q);
+  }
+}
+
 // 32 outputs (columns c .. c + 31, of which those below p.H exist) of a row
 template <int ACT, int MODE>
 __device__ __forceinline__ void epilogue32(const FfnParams& p, int64_t row, int c, const float* a,
-                                           const float* b, float s, float fp8_scale, float& amax) {
+                                           const float* b, float s, float fp8_scale, bool wide,
+                                           float& amax) {
   if (p.pre != nullptr) {
     uint16_t* pre = static_cast<uint16_t*>(p.pre) + row * 2 * p.H + c;
-#pragma unroll
-    for (int q = 0; q < 32; q += 8)
-      if (c + q < p.H) {
-        store8_bf16(pre + q, a + q);
-        store8_bf16(pre + p.H + q, b + q);
-      }
+    store32_bf16(pre, a, p.H - c, wide);
+    store32_bf16(pre + p.H, b, p.H - c, wide);
   }
   float y[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) y[i] = act_value<ACT>(a[i], b[i], p.limit, p.alpha) * s;
   const int64_t o = row * p.H + c;
   if constexpr (MODE == kFfnBf16) {
-#pragma unroll
-    for (int q = 0; q < 32; q += 8)
-      if (c + q < p.H) store8_bf16(static_cast<uint16_t*>(p.out) + o + q, y + q);
+    store32_bf16(static_cast<uint16_t*>(p.out) + o, y, p.H - c, wide);
   } else if constexpr (MODE == kFfnF32) {
 #pragma unroll
     for (int q = 0; q < 32; q += 4)
@@ -170,7 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&done_b[i]), 1);    // the products of a tile
-      mbar_init(smem_u32(&free_b[i]), 8);    // the epilogue warps of both CTAs
+      mbar_init(smem_u32(&free_b[i]), 2 * kEpiWarps);    // the epilogue warps of both CTAs
     }
     fence_barrier_init();
   }
@@ -253,10 +273,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // epilogue warp: lanes 32 (warp % 4) .. + 31 of tensor memory
-    const int lb = (warp & 3) * 32;
+    // epilogue warp: lanes 32 (warp % 4) .. + 31 of tensor memory, one half of the tile's columns
+    const int lb = (warp & 3) * 32, side = (warp - 2) / 4;
     float amax = 0.0f, fp8_scale = 1.0f;
     if constexpr (MODE == kFfnFp8) fp8_scale = *p.f.scale;
+    // 32-byte stores (whole sectors) where every row starts on 32 bytes
+    bool wide = false;
+    if constexpr (ACT != kActNone)
+      wide = (p.f.H & 15) == 0 &&
+             ((reinterpret_cast<uintptr_t>(p.f.out) | reinterpret_cast<uintptr_t>(p.f.pre)) & 31) == 0;
     int it = 0;
     for (int t = cluster; t < total && ok; t += n_clusters, ++it) {
       const Tile tl = tile_at(p, t);
@@ -271,28 +296,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t ta = tmem + acc * 256 + ((uint32_t)lb << 16);
       if constexpr (ACT == kActNone) {
         const int c0 = tl.n * 256;
-        for (int c = 0; c < 256; c += 32) {
+        const bool wide_out = (j.cols & 15) == 0 && (reinterpret_cast<uintptr_t>(j.out) & 31) == 0;
+        for (int c = side * 128; c < side * 128 + 128; c += 32) {
           if (c0 + c >= j.cols) break;
           float v[32];
           tmem_load32(ta + c, v);
           tmem_load_wait();
-          if (row < j.rows) {
-            uint16_t* o = static_cast<uint16_t*>(j.out) + row * j.cols + c0 + c;
-#pragma unroll
-            for (int q = 0; q < 32; q += 8)
-              if (c0 + c + q < j.cols) store8_bf16(o + q, v + q);
-          }
+          if (row < j.rows)
+            store32_bf16(static_cast<uint16_t*>(j.out) + row * j.cols + c0 + c, v, j.cols - c0 - c, wide_out);
         }
       } else {
         const int c0 = tl.n * 128;
         const float s = (p.f.scales != nullptr && row < p.f.N) ? __ldg(p.f.scales + row) : 1.0f;
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = side * 64; c < side * 64 + 64; c += 32) {
           if (c0 + c >= p.f.H) break;
           float a[32], b[32];
           tmem_load32(ta + c, a);
           tmem_load32(ta + 128 + c, b);
           tmem_load_wait();
-          if (row < p.f.N) epilogue32<ACT, MODE>(p.f, row, c0 + c, a, b, s, fp8_scale, amax);
+          if (row < p.f.N) epilogue32<ACT, MODE>(p.f, row, c0 + c, a, b, s, fp8_scale, wide, amax);
         }
       }
       tc_fence_before();
