@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(kActThreads, 2) rn_act_bwd_kernel(const ActPar
   const int lane = threadIdx.x & 31;
   const int gw = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
   const int nw = (int)((gridDim.x * blockDim.x) >> 5);
+  pdl_launch_dependents();  // a dependent waits for this kernel's end before it reads
   const int H = p.H;
   const int nco = H / VEC;
   const size_t in_w = GLU ? 2 * (size_t)H : (size_t)H;

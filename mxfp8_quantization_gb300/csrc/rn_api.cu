@@ -1023,7 +1023,7 @@ rn_status rn_gated_ffn_bwd(rn_act act, const void* dy, const void* x, const void
   rn_status st = ffn_checks(act, dtype, N, K, H, limit, alpha, scales);
   if (st != RN_OK) return st;
   if (K % 8 != 0 || H % 8 != 0) return RN_ERR_UNSUPPORTED;
-  const size_t need = (size_t)N * (size_t)H * 4;
+  const size_t need = ffn_bwd_plan(N, K, H).bytes;
   if (workspace == nullptr && (dx == nullptr && dw == nullptr && dscales == nullptr)) {
     if (workspace_bytes == nullptr) return RN_ERR_INVALID;
     *workspace_bytes = need;
@@ -1055,7 +1055,7 @@ rn_status rn_gated_ffn_bwd(rn_act act, const void* dy, const void* x, const void
   a.alpha = alpha;
   if ((st = launch_act_bwd(act, true, a, di.sms, s)) != RN_OK) return st;
   FfnBwdParams p{};
-  p.dp = workspace;
+  p.ws = workspace;
   p.x = x;
   p.w = w;
   p.dx = dx;

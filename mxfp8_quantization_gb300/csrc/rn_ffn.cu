@@ -48,6 +48,8 @@ constexpr size_t kSmemBytes = (size_t)kStages * kStageBytes + 1024;
 struct Job {
   int tiles_m, tiles_n;
   int slices;            // of 64 along the reduction
+  int splits, per;       // the reduction in parts of `per` slices
+  float* part;           // splits > 1: the parts' sums, fp32 [splits, rows, cols]
   bool a_mn, b_mn;
   void* out;             // dx / dW: bf16 [rows, cols]
   int rows, cols;
@@ -64,8 +66,10 @@ struct Maps {
 };
 
 struct Tile {
-  int job, m, n;
+  int job, m, n, split;
 };
+
+__host__ __device__ inline int64_t units(const Job& j) { return (int64_t)j.tiles_m * j.tiles_n * j.splits; }
 
 // Tiles in order of their index: jobs one after another, within a job bands
 // of 8 tiles of rows walked along the columns, so that the clusters that run
@@ -73,12 +77,15 @@ struct Tile {
 __device__ __forceinline__ Tile tile_at(const GemmParams& p, int t) {
   Tile r;
   r.job = 0;
-  const int n0 = p.job[0].tiles_m * p.job[0].tiles_n;
+  const int n0 = (int)units(p.job[0]);
   if (t >= n0) {
     r.job = 1;
     t -= n0;
   }
   const Job& j = p.job[r.job];
+  const int tiles = j.tiles_m * j.tiles_n;
+  r.split = t / tiles;
+  t -= r.split * tiles;
   const int band = t / (8 * j.tiles_n);
   const int rest = t - band * 8 * j.tiles_n;
   const int h = min(8, j.tiles_m - band * 8);
@@ -181,7 +188,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_rank();
   const int cluster = (int)(blockIdx.x >> 1), n_clusters = (int)(gridDim.x >> 1);
   int total = 0;
-  for (int j = 0; j < p.n_jobs; ++j) total += p.job[j].tiles_m * p.job[j].tiles_n;
+  for (int j = 0; j < p.n_jobs; ++j) total += (int)units(p.job[j]);
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -200,6 +207,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_at;
+  // everything above overlaps the end of the kernel before; nothing of the
+  // caller's memory is touched until it has completed
+  pdl_launch_dependents();
+  pdl_wait();
 
   bool ok = true;
   if (warp == 0) {
@@ -213,7 +224,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int m0 = tl.m * 256 + (int)rank * 128;
         const int n0 = ACT == kActNone ? tl.n * 256 + (int)rank * 128
                                        : tl.n * 128 + (int)rank * p.f.H;
-        for (int k = 0; k < j.slices; ++k) {
+        const int k0 = tl.split * j.per, k1 = min(k0 + j.per, j.slices);
+        for (int k = k0; k < k1; ++k) {
           if (!mbar_wait_warp(smem_u32(&empty_b[r.slot]), r.phase ^ 1u, &g_err_ffn, kErrEmptyWait)) {
             ok = false;
             break;
@@ -242,7 +254,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       RingPos r{0, 0};
       int it = 0;
       for (int t = cluster; t < total && ok; t += n_clusters, ++it) {
-        const Job& j = p.job[tile_at(p, t).job];
+        const Tile tl = tile_at(p, t);
+        const Job& j = p.job[tl.job];
+        const int k0 = tl.split * j.per, k1 = min(k0 + j.per, j.slices);
         const uint32_t acc = it & 1;
         const uint32_t idesc =
             kIdesc256 | (j.a_mn ? kIdescAMN : 0u) | (j.b_mn ? kIdescBMN : 0u);
@@ -252,7 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        for (int k = 0; k < j.slices; ++k) {
+        for (int k = k0; k < k1; ++k) {
           if (!mbar_wait_warp(smem_u32(&full_b[r.slot]), r.phase, &g_err_ffn, kErrFullWait)) {
             ok = false;
             break;
@@ -262,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint64_t a = smem_desc(sa, j.a_mn), b = smem_desc(sa + kOperandBytes, j.b_mn);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            mma_bf16_pair(tmem + acc * 256, a, b, idesc, k > 0 || q > 0);
+            mma_bf16_pair(tmem + acc * 256, a, b, idesc, k > k0 || q > 0);
             a += da;
             b += db;
           }
@@ -302,7 +316,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           float v[32];
           tmem_load32(ta + c, v);
           tmem_load_wait();
-          if (row < j.rows)
+          if (row < j.rows && j.splits > 1) {
+            float* o = j.part + ((int64_t)tl.split * j.rows + row) * j.cols + c0 + c;
+#pragma unroll
+            for (int q = 0; q < 32; q += 4)
+              if (c0 + c + q < j.cols)
+                *reinterpret_cast<float4*>(o + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+          } else if (row < j.rows)
             store32_bf16(static_cast<uint16_t*>(j.out) + row * j.cols + c0 + c, v, j.cols - c0 - c, wide_out);
         }
       } else {
@@ -323,10 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if constexpr (MODE == kFfnFp8) {
       const float m = warp_max_nan(amax);
-      if (lane == 0) {
-        pdl_wait();  // amax was zeroed by the kernel this one depends on
-        atomicMax(reinterpret_cast<unsigned*>(p.f.amax), abs_bits(m));
-      }
+      if (lane == 0) atomicMax(reinterpret_cast<unsigned*>(p.f.amax), abs_bits(m));
     }
   }
   // A wait that ran out leaves copies and products in flight: give them a
@@ -381,10 +398,10 @@ rn_status make_map(CUtensorMap* tm, const void* base, int64_t rows, int64_t cols
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 template <int ACT, int MODE>
-rn_status launch(const GemmParams& p, const Maps& maps, int sms, bool pdl, cudaStream_t s) {
+rn_status launch(const GemmParams& p, const Maps& maps, int sms, cudaStream_t s) {
   auto k = rn_ffn_kernel<ACT, MODE>;
   int64_t total = 0;
-  for (int j = 0; j < p.n_jobs; ++j) total += (int64_t)p.job[j].tiles_m * p.job[j].tiles_n;
+  for (int j = 0; j < p.n_jobs; ++j) total += units(p.job[j]);
   if (total > INT32_MAX / 2) return RN_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -405,7 +422,7 @@ rn_status launch(const GemmParams& p, const Maps& maps, int sms, bool pdl, cudaS
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
+  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, k, p, maps) != cudaSuccess) return RN_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? RN_OK : RN_ERR_CUDA;
 }
@@ -413,10 +430,10 @@ rn_status launch(const GemmParams& p, const Maps& maps, int sms, bool pdl, cudaS
 template <int ACT>
 rn_status launch_mode(const GemmParams& p, const Maps& maps, int sms, cudaStream_t s) {
   switch (p.f.mode) {
-    case kFfnBf16: return launch<ACT, kFfnBf16>(p, maps, sms, false, s);
-    case kFfnF32: return launch<ACT, kFfnF32>(p, maps, sms, false, s);
-    case kFfnFp8: return launch<ACT, kFfnFp8>(p, maps, sms, true, s);
-    case kFfnMx: return launch<ACT, kFfnMx>(p, maps, sms, false, s);
+    case kFfnBf16: return launch<ACT, kFfnBf16>(p, maps, sms, s);
+    case kFfnF32: return launch<ACT, kFfnF32>(p, maps, sms, s);
+    case kFfnFp8: return launch<ACT, kFfnFp8>(p, maps, sms, s);
+    case kFfnMx: return launch<ACT, kFfnMx>(p, maps, sms, s);
     default: return RN_ERR_INVALID;
   }
 }
@@ -427,7 +444,8 @@ rn_status launch_ffn_fwd(int act, const FfnParams& f, int sms, cudaStream_t s) {
   GemmParams p{};
   p.n_jobs = 1;
   p.f = f;
-  p.job[0] = Job{cdiv(f.N, 256), cdiv(f.H, 128), cdiv(f.K, 64), false, false, nullptr, 0, 0};
+  const int slices = cdiv(f.K, 64);
+  p.job[0] = Job{cdiv(f.N, 256), cdiv(f.H, 128), slices, 1, slices, nullptr, false, false, nullptr, 0, 0};
   Maps m{};
   rn_status st;
   if ((st = make_map(&m.a[0], f.x, f.N, f.K, 128)) != RN_OK) return st;
@@ -436,25 +454,125 @@ rn_status launch_ffn_fwd(int act, const FfnParams& f, int sms, cudaStream_t s) {
                            : launch_mode<kActClampedSwiglu>(p, m, sms, s);
 }
 
+namespace {
+
+// Adds the parts' sums of up to two products in their order and rounds once.
+struct JoinParams {
+  const float* part[2];
+  void* out[2];
+  int splits[2];
+  int64_t size[2];  // elements of the product; 0: none
+};
+
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) rn_ffn_join_kernel(const JoinParams p) {
+  pdl_wait();
+  for (int j = 0; j < 2; ++j) {
+    const int64_t n8 = p.size[j] / 8;
+    for (int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; i < n8;
+         i += (int64_t)gridDim.x * kJoinThreads) {
+      float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      const float4* q = reinterpret_cast<const float4*>(p.part[j]) + i * 2;
+#pragma unroll 4
+      for (int s = 0; s < p.splits[j]; ++s) {
+        const float4 a = q[s * (p.size[j] / 4)], b = q[s * (p.size[j] / 4) + 1];
+        v[0] += a.x;
+        v[1] += a.y;
+        v[2] += a.z;
+        v[3] += a.w;
+        v[4] += b.x;
+        v[5] += b.y;
+        v[6] += b.z;
+        v[7] += b.w;
+      }
+      store8_bf16(static_cast<uint16_t*>(p.out[j]) + i * 8, v);
+    }
+  }
+}
+
+// pairs of SMs on a GB300: what the plan spreads the work over (a constant,
+// so that the workspace's size depends on the problem only)
+constexpr int64_t kPairs = 76;
+
+// A product's reduction is split where one of its tiles would take longer
+// than an even share of the launch's work: into parts of that share, of 8
+// slices at least (a part's sums cost about as much as 4 slices), and no more
+// than two parts a pair.  203 x 1000 x 2056: dx 30.3 us unsplit.
+FfnSplit split_for(int64_t tiles, int64_t slices, int64_t share) {
+  int64_t n = 1;
+  if (slices > share + share / 4) {
+    n = (slices + share - 1) / share;
+    if (n > slices / 8) n = slices / 8;
+    if (n > 2 * kPairs / tiles) n = 2 * kPairs / tiles;
+    if (n < 1) n = 1;
+  }
+  FfnSplit r;
+  r.per = (int)((slices + n - 1) / n);
+  r.splits = (int)((slices + r.per - 1) / r.per);
+  return r;
+}
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+}  // namespace
+
+FfnBwdPlan ffn_bwd_plan(int64_t N, int64_t K, int64_t H) {
+  FfnBwdPlan p{};
+  const int64_t R = 2 * H, kc = (K + 255) / 256;
+  const int64_t dx_tiles = (N + 255) / 256 * kc, dx_slices = (R + 63) / 64;
+  const int64_t dw_tiles = (R + 255) / 256 * kc, dw_slices = (N + 63) / 64;
+  if (N > 0) {
+    const int64_t share = (dx_tiles * dx_slices + dw_tiles * dw_slices) / kPairs + 1;
+    p.dx = split_for(dx_tiles, dx_slices, share);
+    p.dw = split_for(dw_tiles, dw_slices, share);
+  }
+  p.dx_part = up256((size_t)N * R * 2);
+  p.dw_part = p.dx_part + (p.dx.splits > 1 ? up256((size_t)p.dx.splits * N * K * 4) : 0);
+  p.bytes = p.dw_part + (p.dw.splits > 1 ? up256((size_t)p.dw.splits * R * K * 4) : 0);
+  return p;
+}
+
 rn_status launch_ffn_bwd(const FfnBwdParams& b, int sms, cudaStream_t s) {
   GemmParams p{};
   Maps m{};
+  JoinParams jp{};
   const int64_t R = 2 * (int64_t)b.H;
+  const FfnBwdPlan plan = ffn_bwd_plan(b.N, b.K, b.H);
+  char* ws = static_cast<char*>(b.ws);
+  int64_t join = 0;
   rn_status st;
-  if (b.dx != nullptr) {
+  const auto add = [&](int64_t rows, int64_t red, bool a_mn, const void* bm, int64_t b_rows, void* out,
+                       const FfnSplit& sp, size_t part) -> rn_status {
     const int i = p.n_jobs++;
-    p.job[i] = Job{cdiv(b.N, 256), cdiv(b.K, 256), cdiv(R, 64), false, true, b.dx, b.N, b.K};
-    if ((st = make_map(&m.a[i], b.dp, b.N, R, 128)) != RN_OK) return st;
-    if ((st = make_map(&m.b[i], b.w, R, b.K, 64)) != RN_OK) return st;
-  }
-  if (b.dw != nullptr) {
-    const int i = p.n_jobs++;
-    p.job[i] = Job{cdiv(R, 256), cdiv(b.K, 256), cdiv(b.N, 64), true, true, b.dw, (int)R, b.K};
-    if ((st = make_map(&m.a[i], b.dp, b.N, R, 64)) != RN_OK) return st;
-    if ((st = make_map(&m.b[i], b.x, b.N, b.K, 64)) != RN_OK) return st;
-  }
+    p.job[i] = Job{cdiv(rows, 256), cdiv(b.K, 256), cdiv(red, 64), sp.splits, sp.per,
+                   reinterpret_cast<float*>(ws + part), a_mn, true, out, (int)rows, b.K};
+    if (sp.splits > 1) {
+      jp.part[i] = p.job[i].part;
+      jp.out[i] = out;
+      jp.splits[i] = sp.splits;
+      jp.size[i] = rows * b.K;
+      join += jp.size[i];
+    }
+    if ((st = make_map(&m.a[i], ws, b.N, R, a_mn ? 64 : 128)) != RN_OK) return st;
+    return make_map(&m.b[i], bm, b_rows, b.K, 64);
+  };
+  if (b.dx != nullptr && (st = add(b.N, R, false, b.w, R, b.dx, plan.dx, plan.dx_part)) != RN_OK) return st;
+  if (b.dw != nullptr && (st = add(R, b.N, true, b.x, b.N, b.dw, plan.dw, plan.dw_part)) != RN_OK) return st;
   if (p.n_jobs == 0) return RN_OK;
-  return launch<kActNone, kFfnBf16>(p, m, sms, false, s);
+  if ((st = launch<kActNone, kFfnBf16>(p, m, sms, s)) != RN_OK || join == 0) return st;
+  const int64_t blocks = (join / 8 + kJoinThreads - 1) / kJoinThreads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(blocks < 8 * sms ? blocks : 8 * sms));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, rn_ffn_join_kernel, jp) != cudaSuccess) return RN_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? RN_OK : RN_ERR_CUDA;
 }
 
 rn_status read_clear_error_ffn(unsigned* code) {

@@ -147,8 +147,21 @@ struct FfnParams {
   int mode;               // FfnOut
 };
 
+// how the backward's two products split their reductions: `splits` parts of
+// `per` slices of 64 each; with more than one part their fp32 sums go to the
+// workspace and a second kernel adds them
+struct FfnSplit {
+  int splits, per;
+};
+struct FfnBwdPlan {
+  FfnSplit dx, dw;
+  size_t dx_part, dw_part;  // byte offsets of the sums in the workspace (after dp)
+  size_t bytes;             // of the workspace
+};
+FfnBwdPlan ffn_bwd_plan(int64_t N, int64_t K, int64_t H);
+
 struct FfnBwdParams {
-  const void* dp;         // bf16 [N, 2H], workspace
+  void* ws;               // workspace: dp bf16 [N, 2H], then the parts' sums
   const void* x;          // bf16 [N, K]
   const void* w;          // bf16 [2H, K]
   void* dx;               // bf16 [N, K] or NULL

@@ -509,6 +509,9 @@ __global__ void __launch_bounds__(32 * W, (T == 1 && W == 8) ? 2 : 1) rn_matvec_
     }
     fence_barrier_init();
   }
+  // nothing of the caller's memory is touched until the kernel before has completed
+  pdl_launch_dependents();
+  pdl_wait();
   int at[T];
   M::lane_at(n, lane, at);
   const float si = WK == kWNvfp4 ? __ldg(p.scale_inv) : 1.0f;
@@ -656,10 +659,7 @@ __global__ void __launch_bounds__(32 * W, (T == 1 && W == 8) ? 2 : 1) rn_matvec_
   if (held >= 0) add_up();
   if (p.mode == kFfnFp8) {
     const float m = warp_max_nan(amax);
-    if (lane == 0) {
-      pdl_wait();  // amax was zeroed by the kernel this one depends on
-      atomicMax(reinterpret_cast<unsigned*>(p.amax), abs_bits(m));
-    }
+    if (lane == 0) atomicMax(reinterpret_cast<unsigned*>(p.amax), abs_bits(m));
   }
   if (pl.split > 1) cluster_sync();  // no CTA leaves while another writes to it
 }
@@ -747,11 +747,9 @@ rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
     attr[na].val.clusterDim.z = 1;
     ++na;
   }
-  if (p.mode == kFfnFp8) {
-    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[na].val.programmaticStreamSerializationAllowed = 1;
-    ++na;
-  }
+  attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[na].val.programmaticStreamSerializationAllowed = 1;
+  ++na;
   cfg.attrs = attr;
   cfg.numAttrs = na;
   if (cudaLaunchKernelEx(&cfg, k, p, pl) != cudaSuccess) return RN_ERR_CUDA;

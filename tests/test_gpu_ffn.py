@@ -100,6 +100,23 @@ def test_backward(i, size):
     _check_bwd(x, w, dy, s, pre, act, dx, dw, ds)
 
 
+# reductions split over the workspace: dx (many hidden rows), dW (many tokens), both
+@pytest.mark.parametrize("N,K,H", [(40, 64, 3000), (3000, 72, 40), (2100, 264, 2104), (70, 520, 1544)])
+def test_backward_split_reductions(N, K, H):
+    x, w, dy, s = block(N, K, H, True, seed=N)
+    pre = (x.float() @ w.float().T).bfloat16()
+    need = rn.gated_ffn_bwd_workspace_bytes(N, K, H)
+    assert need > 4 * N * H + 256                       # room for the parts' sums
+    full = rn.gated_ffn_bwd(dy, x, w, pre, "swiglu", s)
+    _check_bwd(x, w, dy, s, pre, "swiglu", *full)
+    # a workspace on 16 bytes, and one product at a time
+    ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")[16:]
+    part = (*rn.gated_ffn_bwd(dy, x, w, pre, "swiglu", s, workspace=ws, need_dw=False)[:1],
+            *rn.gated_ffn_bwd(dy, x, w, pre, "swiglu", s, workspace=ws, need_dx=False)[1:])
+    for a, b in zip(full, part):
+        assert torch.equal(a, b)
+
+
 def _check_bwd(x, w, dy, s, pre, act, dx, dw, ds):
     x64, w64, dy64, pre64 = f64(x), f64(w), f64(dy), f64(pre)
     N, K = x64.shape
