@@ -58,6 +58,7 @@ struct Job {
 struct GemmParams {
   Job job[2];
   int n_jobs;
+  int pairs;             // of a cluster; more than one: each sums a part of the one tile's reduction
   FfnParams f;           // forward
 };
 
@@ -176,9 +177,85 @@ __device__ __forceinline__ void epilogue32(const FfnParams& p, int64_t row, int 
   }
 }
 
+// The end of a tile whose reduction the cluster's pairs shared: pair q keeps
+// the outputs [q w, q w + w) of the tile, w = 128 / pairs, and gets the other
+// pairs' sums for them into the shared memory of its operands (which all
+// products have left by then), [pair - 1 of them][gate, linear][w][128 rows].
+// The sums are added in the order of the pairs.  Called by every thread of the
+// cluster, each of which works on one tile.
+template <int ACT, int MODE>
+__device__ __forceinline__ void split_epilogue(const GemmParams& p, int cluster, uint32_t tmem, uint32_t ring,
+                                               uint32_t done, int warp, int lane, int half, int pair, bool& ok) {
+  const int w = 128 / p.pairs;
+  const bool works = warp >= 2;
+  const int lb = (warp & 3) * 32, side = (warp - 2) / 4;
+  const uint32_t ta = tmem + ((uint32_t)lb << 16);
+  if (works) ok = mbar_wait_warp(done, 0, &g_err_ffn, kErrStatsWait) && ok;
+  tc_fence_after();
+  __syncwarp();
+  cluster_sync();  // no pair's operands are needed any more
+  if (works) {
+    for (int q = 0; q < p.pairs; ++q) {
+      if (q == pair) continue;
+      const int slot = pair < q ? pair : pair - 1;
+      const uint32_t to = map_to_rank(ring, 2 * q + half) + (uint32_t)(slot * 2 + side) * w * 512 + (lb + lane) * 4;
+      for (int c = 0; c < w; c += 32) {
+        float v[32];
+        tmem_load32(ta + side * 128 + q * w + c, v);
+        tmem_load_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + (c + i) * 512), "f"(v[i]) : "memory");
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync();
+  if (works && side * 32 < w) {
+    const Tile tl = tile_at(p, cluster);
+    const int64_t row = (int64_t)tl.m * 256 + half * 128 + lb + lane;
+    const int c = side * 32, col = tl.n * 128 + pair * w + c;
+    float amax = 0.0f, fp8_scale = 1.0f;
+    if constexpr (MODE == kFfnFp8) fp8_scale = *p.f.scale;
+    if (col < p.f.H) {
+      const bool wide = (p.f.H & 15) == 0 &&
+                        ((reinterpret_cast<uintptr_t>(p.f.out) | reinterpret_cast<uintptr_t>(p.f.pre)) & 31) == 0;
+      const float s = (p.f.scales != nullptr && row < p.f.N) ? __ldg(p.f.scales + row) : 1.0f;
+      float v[2][32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float own[32];
+        tmem_load32(ta + h * 128 + pair * w + c, own);
+        tmem_load_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[h][i] = 0.0f;
+        for (int q = 0; q < p.pairs; ++q) {
+          if (q == pair) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[h][i] += own[i];
+          } else {
+            const uint32_t from = ring + (uint32_t)((q < pair ? q : q - 1) * 2 + h) * w * 512 + (lb + lane) * 4;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float u;
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(u) : "r"(from + (c + i) * 512) : "memory");
+              v[h][i] += u;
+            }
+          }
+        }
+      }
+      if (row < p.f.N) epilogue32<ACT, MODE>(p.f, row, col, v[0], v[1], s, fp8_scale, wide, amax);
+    }
+    if constexpr (MODE == kFfnFp8) {
+      const float m = warp_max_nan(amax);
+      if (lane == 0) atomicMax(reinterpret_cast<unsigned*>(p.f.amax), abs_bits(m));
+    }
+  }
+}
+
 // ACT kActNone: the products of the backward, stored as they are
 template <int ACT, int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     rn_ffn_kernel(const GemmParams p, const __grid_constant__ Maps maps) {
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t full_b[kStages], empty_b[kStages], done_b[2], free_b[2];
@@ -186,7 +263,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const int cluster = (int)(blockIdx.x >> 1), n_clusters = (int)(gridDim.x >> 1);
+  // of a cluster of `pairs` pairs: the CTA's half of its pair's tile, and its pair
+  const int half = (int)rank & 1, pair = (int)rank >> 1;
+  const uint32_t leader = rank & ~1u;
+  const int cluster = (int)blockIdx.x / (2 * p.pairs), n_clusters = (int)gridDim.x / (2 * p.pairs);
   int total = 0;
   for (int j = 0; j < p.n_jobs; ++j) total += (int)units(p.job[j]);
 
@@ -221,17 +301,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Job& j = p.job[tl.job];
         const CUtensorMap* ma = &maps.a[tl.job];
         const CUtensorMap* mb = &maps.b[tl.job];
-        const int m0 = tl.m * 256 + (int)rank * 128;
-        const int n0 = ACT == kActNone ? tl.n * 256 + (int)rank * 128
-                                       : tl.n * 128 + (int)rank * p.f.H;
-        const int k0 = tl.split * j.per, k1 = min(k0 + j.per, j.slices);
+        const int m0 = tl.m * 256 + half * 128;
+        const int n0 = ACT == kActNone ? tl.n * 256 + half * 128 : tl.n * 128 + half * p.f.H;
+        const int k0 = (tl.split + pair) * j.per, k1 = min(k0 + j.per, j.slices);
         for (int k = k0; k < k1; ++k) {
           if (!mbar_wait_warp(smem_u32(&empty_b[r.slot]), r.phase ^ 1u, &g_err_ffn, kErrEmptyWait)) {
             ok = false;
             break;
           }
-          const uint32_t bar = map_to_rank(smem_u32(&full_b[r.slot]), 0);
-          if (rank == 0) mbar_expect_elected(smem_u32(&full_b[r.slot]), 2 * kStageBytes);
+          const uint32_t bar = map_to_rank(smem_u32(&full_b[r.slot]), leader);
+          if (half == 0) mbar_expect_elected(smem_u32(&full_b[r.slot]), 2 * kStageBytes);
           const uint32_t sa = ring + r.slot * kStageBytes, sb = sa + kOperandBytes;
           if (j.a_mn) {
             tma_load_2d(sa, ma, m0, k * 64, bar);
@@ -250,13 +329,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (rank == 0) {
+    if (half == 0) {
       RingPos r{0, 0};
       int it = 0;
       for (int t = cluster; t < total && ok; t += n_clusters, ++it) {
         const Tile tl = tile_at(p, t);
         const Job& j = p.job[tl.job];
-        const int k0 = tl.split * j.per, k1 = min(k0 + j.per, j.slices);
+        const int k0 = (tl.split + pair) * j.per, k1 = min(k0 + j.per, j.slices);
         const uint32_t acc = it & 1;
         const uint32_t idesc =
             kIdesc256 | (j.a_mn ? kIdescAMN : 0u) | (j.b_mn ? kIdescBMN : 0u);
@@ -280,13 +359,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             a += da;
             b += db;
           }
-          mma_commit_pair(smem_u32(&empty_b[r.slot]));
+          mma_commit(smem_u32(&empty_b[r.slot]), 3u << leader);
           r.advance(1, kStages);
         }
-        if (ok) mma_commit_pair(smem_u32(&done_b[acc]));
+        if (ok) mma_commit(smem_u32(&done_b[acc]), 3u << leader);
       }
     }
-  } else {
+  } else if (ACT == kActNone || p.pairs == 1) {
     // epilogue warp: lanes 32 (warp % 4) .. + 31 of tensor memory, one half of the tile's columns
     const int lb = (warp & 3) * 32, side = (warp - 2) / 4;
     float amax = 0.0f, fp8_scale = 1.0f;
@@ -306,7 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      const int64_t row = (int64_t)tl.m * 256 + rank * 128 + lb + lane;
+      const int64_t row = (int64_t)tl.m * 256 + half * 128 + lb + lane;
       const uint32_t ta = tmem + acc * 256 + ((uint32_t)lb << 16);
       if constexpr (ACT == kActNone) {
         const int c0 = tl.n * 256;
@@ -339,12 +418,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&free_b[acc]), 0));
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&free_b[acc]), leader));
     }
     if constexpr (MODE == kFfnFp8) {
       const float m = warp_max_nan(amax);
       if (lane == 0) atomicMax(reinterpret_cast<unsigned*>(p.f.amax), abs_bits(m));
     }
+  }
+  if constexpr (ACT != kActNone) {
+    if (p.pairs > 1) split_epilogue<ACT, MODE>(p, cluster, tmem, ring, smem_u32(&done_b[0]), warp, lane, half, pair, ok);
   }
   // A wait that ran out leaves copies and products in flight: give them a
   // millisecond to land before the memory they write is given back.
@@ -404,25 +486,34 @@ rn_status launch(const GemmParams& p, const Maps& maps, int sms, cudaStream_t s)
   for (int j = 0; j < p.n_jobs; ++j) total += units(p.job[j]);
   if (total > INT32_MAX / 2) return RN_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2u * (unsigned)p.pairs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
-  // clusters that run at the same time; the shared-memory limit is raised first
+  // pairs that run at the same time; the shared-memory limit is raised first
   static std::atomic<int> kept[kMaxDevices];
   const int resident = once_per_device(kept, [&] {
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess)
       return -1;
+    attr[0].val.clusterDim.x = 2;
+    cfg.numAttrs = 1;
     cfg.gridDim = dim3((unsigned)sms / 2 * 2);
     int n = 0;
     return cudaOccupancyMaxActiveClusters(&n, k, &cfg) == cudaSuccess && n > 0 ? n : -1;
   });
   if (resident < 1) return RN_ERR_CUDA;
-  cfg.gridDim = dim3(2u * (unsigned)(total < resident ? total : resident));
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  attr[0].val.clusterDim.x = 2u * (unsigned)p.pairs;
+  cfg.numAttrs = 2;
+  // one tile a cluster where its pairs share the tile, else as many pairs as run at the same time
+  cfg.gridDim = dim3(p.pairs > 1 ? 2u * (unsigned)p.pairs * (unsigned)total
+                                 : 2u * (unsigned)(total < resident ? total : resident));
   if (cudaLaunchKernelEx(&cfg, k, p, maps) != cudaSuccess) return RN_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? RN_OK : RN_ERR_CUDA;
 }
@@ -440,12 +531,27 @@ rn_status launch_mode(const GemmParams& p, const Maps& maps, int sms, cudaStream
 
 }  // namespace
 
+// Pairs that share a tile of the forward: 4 or 2 where the tiles are so few
+// that every SM still gets at most one CTA (15 clusters of 8 CTAs, 36 of 4 run
+// at the same time on a GB300) and the reduction is long (us, shared against
+// not: 64 x 8192 x 512 17.0 / 37.5, 256 x 8192 x 2048 24.0 / 38.3, 512 x 4096 x
+// 1024 15.4 / 21.2, 32 x 2048 x 2048 10.6 / 12.8; with 16 slices 64 x 1024 x 256
+// 9.0 / 8.0, 203 x 1000 x 2056 9.9 / 10.4).
+static int share_pairs(int64_t tiles, int slices) {
+  if (tiles <= 15 && slices >= 40) return 4;
+  if (tiles <= 36 && slices >= 20) return 2;
+  return 1;
+}
+
 rn_status launch_ffn_fwd(int act, const FfnParams& f, int sms, cudaStream_t s) {
   GemmParams p{};
   p.n_jobs = 1;
   p.f = f;
   const int slices = cdiv(f.K, 64);
-  p.job[0] = Job{cdiv(f.N, 256), cdiv(f.H, 128), slices, 1, slices, nullptr, false, false, nullptr, 0, 0};
+  const int64_t tiles = (int64_t)cdiv(f.N, 256) * cdiv(f.H, 128);
+  p.pairs = share_pairs(tiles, slices);
+  const int per = cdiv(slices, p.pairs);
+  p.job[0] = Job{cdiv(f.N, 256), cdiv(f.H, 128), slices, 1, per, nullptr, false, false, nullptr, 0, 0};
   Maps m{};
   rn_status st;
   if ((st = make_map(&m.a[0], f.x, f.N, f.K, 128)) != RN_OK) return st;
@@ -535,6 +641,7 @@ FfnBwdPlan ffn_bwd_plan(int64_t N, int64_t K, int64_t H) {
 
 rn_status launch_ffn_bwd(const FfnBwdParams& b, int sms, cudaStream_t s) {
   GemmParams p{};
+  p.pairs = 1;
   Maps m{};
   JoinParams jp{};
   const int64_t R = 2 * (int64_t)b.H;

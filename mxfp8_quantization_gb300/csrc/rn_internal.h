@@ -123,11 +123,12 @@ struct ActParams {
 // gated feed-forward block and the NVFP4 products
 constexpr int kActNone = -1;  // rn_nvfp4_matvec: no activation
 
-// The bf16 block of few tokens: up to 8 the few-token kernel (4096 x 8192, 8
-// tokens: 28 against 30 us with the tensor-core tiles), up to 32 while the
-// tiles of 128 outputs would leave most SMs idle (2048 x 2048, 32 tokens: 16
-// against 17 us; 4096 x 8192: 57 against 30 us).
-inline bool few_tokens(int64_t N, int64_t H) { return N <= 8 || (N <= 32 && H <= 32 * 128); }
+// The bf16 block of few tokens: up to 8 the few-token kernel, up to 32 while
+// the outputs are few (us, few-token kernel against tensor-core tiles, K = H
+// unless given: 8 tokens 2048 8.1 / 10.6, 8 x 4096 x 8192 28 / 26; 16 tokens
+// 1024 x 512 4.8 / 9.4, 2048 9.0 / 10.7, 4096 x 8192 39 / 26; 32 tokens 2048
+// 12.7 / 10.6, 4096 26.5 / 15.8).
+inline bool few_tokens(int64_t N, int64_t H) { return N <= 8 || (N <= 32 && N * H <= 32768); }
 // few-token kernel: 8 rows apart stays within 32 bits; groups of 32 tokens in gridDim.y
 constexpr int64_t kMvMaxK = int64_t(1) << 26, kMvMaxN = int64_t(1) << 20;
 

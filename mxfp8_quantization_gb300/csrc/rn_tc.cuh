@@ -93,14 +93,14 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b
       : "memory");
 }
 
-// one arrival on the barrier at `bar` in both CTAs once every product this
-// thread issued so far has completed
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+// one arrival on the barrier at `bar` in each CTA of `mask` once every product
+// the elected thread issued so far has completed
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t mask) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;\n\t}" ::"r"(bar),
-      "h"((uint16_t)3)
+      "h"((uint16_t)mask)
       : "memory");
 }
 

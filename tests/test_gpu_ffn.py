@@ -90,6 +90,13 @@ def test_forward_modes(mode, act, N, K, H):
     _check_fwd(N, K, H, act, True, mode, True, seed=1)
 
 
+# few tiles and a long reduction: clusters of 4 and of 8 CTAs share a tile
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("N,K,H", [(40, 2568, 1056), (300, 2056, 160), (200, 1288, 2080), (130, 4104, 288)])
+def test_forward_shared_tiles(mode, N, K, H):
+    _check_fwd(N, K, H, "clamped_swiglu" if N == 40 else "swiglu", N != 130, mode, True, seed=2)
+
+
 @pytest.mark.parametrize("i,size", list(enumerate(SIZES)), ids=lambda v: str(v))
 def test_backward(i, size):
     N, K, H = size
