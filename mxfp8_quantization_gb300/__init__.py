@@ -221,7 +221,8 @@ def _make_output(x, quant, out_dtype, scale, rowwise=True, colwise=True):
             if scale is None:
                 raise RNError("fp8_delayed needs scale")
             s = scale if isinstance(scale, torch.Tensor) else torch.tensor([float(scale)], dtype=torch.float32)
-            s = s.to(device=dev, dtype=torch.float32).reshape(1).contiguous()
+            if not (s.dtype is torch.float32 and s.shape == (1,) and s.device == dev):
+                s = s.to(device=dev, dtype=torch.float32).reshape(1).contiguous()
             res.scale = s
             o.scale = s.data_ptr()
         else:
@@ -450,8 +451,8 @@ def gated_ffn_fwd(x, w, act="swiglu", scales=None, quant="none", limit=7.0, alph
         _take(scales, "scales", dev, torch.float32, (N,))
     o, res = _make_rows_output(x, N, H, quant, out_dtype, scale)
     pre = torch.empty((N, R), dtype=x.dtype, device=x.device) if save_pre else None
-    st = lib.rn_gated_ffn_fwd(code, x.data_ptr(), w.data_ptr(), _BF16, _addr(scales), N, K, H, limit,
-                              alpha, QUANT_MODES[quant], ctypes.byref(o), _addr(pre), _raw_stream(dev))
+    st = lib.rn_gated_ffn_fwd(code, x.data_ptr(), w.data_ptr(), _BF16, _addr(scales), N, K, H, float(limit),
+                              float(alpha), QUANT_MODES[quant], ctypes.byref(o), _addr(pre), _raw_stream(dev))
     if st:
         _check(st, "rn_gated_ffn_fwd")
     return res, pre
@@ -492,7 +493,7 @@ def gated_ffn_bwd(dy, x, w, pre, act="swiglu", scales=None, limit=7.0, alpha=1.7
     dw = torch.empty((R, K), dtype=x.dtype, device=x.device) if need_dw else None
     ds = torch.empty(N, dtype=torch.float32, device=x.device) if dscales else None
     st = lib.rn_gated_ffn_bwd(code, dy.data_ptr(), x.data_ptr(), w.data_ptr(), pre.data_ptr(), _BF16,
-                              _addr(scales), N, K, H, limit, alpha, _addr(dx), _addr(dw), _addr(ds),
+                              _addr(scales), N, K, H, float(limit), float(alpha), _addr(dx), _addr(dw), _addr(ds),
                               workspace.data_ptr(), ctypes.byref(n), _raw_stream(dev))
     if st:
         _check(st, "rn_gated_ffn_bwd")
@@ -539,7 +540,7 @@ def nvfp4_gated_ffn(x, w, act="swiglu", scales=None, quant="none", limit=7.0, al
     o, res = _make_rows_output(x, N, R // 2, quant, out_dtype, scale)
     st = lib.rn_nvfp4_gated_ffn(code, x.data_ptr(), _BF16, w.data.data_ptr(),
                                 w.row_scales.data_ptr(), w.scale_inv.data_ptr(), _addr(scales), N, K,
-                                R // 2, limit, alpha, QUANT_MODES[quant], ctypes.byref(o),
+                                R // 2, float(limit), float(alpha), QUANT_MODES[quant], ctypes.byref(o),
                                 _raw_stream(dev))
     if st:
         _check(st, "rn_nvfp4_gated_ffn")

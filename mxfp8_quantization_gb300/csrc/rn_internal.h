@@ -181,6 +181,7 @@ struct MvParams {
   const float* scale;     // kFfnFp8
   float* amax;            // kFfnFp8
   void* pre;              // bf16 weights: bf16 [N, 2H] or NULL
+  int rows;               // how the weights' rows can be read (set at the launch)
   int N, K, H;
   float limit, alpha;
   int mode;               // FfnOut

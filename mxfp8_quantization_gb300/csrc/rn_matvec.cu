@@ -50,6 +50,10 @@ constexpr int kDepth = T == 4 ? 2 : 1;
 
 enum WeightKind : int { kWBf16 = 0, kWNvfp4 = 1 };
 
+// how the weights' rows can be read: in whole chunks and on 32 bytes, in
+// whole 32-byte pieces of a lane, in whole 16-byte halves of one, or any
+enum RowKind : int { kRowsChunks = 0, kRowsPieces = 1, kRowsHalves = 2, kRowsAny = 3 };
+
 struct MvPlan {
   int kw;       // warps along the reduction
   int split;    // CTAs of a cluster along the reduction
@@ -191,7 +195,7 @@ struct Mv {
   __device__ __forceinline__ static void load(const MvParams& p, const Rows& r, int chunk, int d, int lane,
                                               Item& it) {
     const int left = p.K - (chunk + d) * CK - (lane & 3) * (CK / 4);  // of the row, from this lane's piece on
-    if ((p.K & (CK - 1)) == 0) {  // rows of whole chunks
+    if (p.rows == kRowsChunks) {
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -209,9 +213,19 @@ struct Mv {
           for (int f = 0; f < 2; ++f)
             it.w[m][h][f] =
                 left > f * 8 ? ldg_w16(r.w[m][h] + d * kWBytes + f * 16) : make_uint4(0, 0, 0, 0);
+    } else if (p.rows == kRowsPieces) {
+      // past the row's end its last pieces are read again: the tokens are 0 there
+      const int at = d * CK + min(0, left - 64);
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ldg_w32(r.w[m][h] + at / 2, it.w[m][h]);
+          it.s[m][h] = __ldg(reinterpret_cast<const unsigned*>(r.s[m][h] + at / 16));
+        }
     } else {
-      // past the row's end its last blocks are read again: the tokens are 0 there
-      const bool whole = (p.K & 31) == 0;  // rows of whole 16-byte pieces
+      // the same in blocks
+      const bool whole = p.rows == kRowsHalves;
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -769,7 +783,13 @@ rn_status launch_n(const MvParams& p, int sms, cudaStream_t s) {
 
 }  // namespace
 
-rn_status launch_nvfp4_mv(int act, const MvParams& p, int sms, cudaStream_t s) {
+rn_status launch_nvfp4_mv(int act, const MvParams& q, int sms, cudaStream_t s) {
+  MvParams p = q;
+  const bool on32 = reinterpret_cast<uintptr_t>(p.w) % 32 == 0;
+  p.rows = on32 && p.K % 256 == 0  ? kRowsChunks
+           : on32 && p.K % 64 == 0 ? kRowsPieces
+           : p.K % 32 == 0         ? kRowsHalves
+                                   : kRowsAny;
   switch (act) {
     case kActNone: return launch_n<kActNone, kWNvfp4>(p, sms, s);
     case kActSwiglu: return launch_n<kActSwiglu, kWNvfp4>(p, sms, s);
@@ -777,7 +797,9 @@ rn_status launch_nvfp4_mv(int act, const MvParams& p, int sms, cudaStream_t s) {
   }
 }
 
-rn_status launch_bf16_mv(int act, const MvParams& p, int sms, cudaStream_t s) {
+rn_status launch_bf16_mv(int act, const MvParams& q, int sms, cudaStream_t s) {
+  MvParams p = q;
+  p.rows = p.K % 64 == 0 && reinterpret_cast<uintptr_t>(p.w) % 32 == 0 ? kRowsChunks : kRowsAny;
   return act == kActSwiglu ? launch_n<kActSwiglu, kWBf16>(p, sms, s)
                            : launch_n<kActClampedSwiglu, kWBf16>(p, sms, s);
 }

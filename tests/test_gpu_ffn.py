@@ -42,7 +42,7 @@ def np_scales(s):
 # one token to several tiles in each direction, odd sizes, K below and across a staged slice
 SIZES = [(1, 8, 8), (1, 64, 64), (1, 2048, 264), (2, 72, 40), (5, 200, 1000), (8, 2048, 96), (9, 136, 104),
          (16, 520, 264), (17, 512, 136), (31, 1000, 72), (33, 96, 2056), (64, 4104, 128), (127, 64, 136),
-         (128, 256, 128), (129, 264, 136), (255, 328, 248), (257, 72, 264), (300, 1000, 1032),
+         (128, 256, 128), (129, 264, 136), (255, 328, 248), (257, 72, 264), (300, 1000, 1032), (17, 136, 2056),
          (513, 128, 520), (2600, 64, 1104)]
 MODES = ["bf16", "f32", "fp8_delayed", "mxfp8"]
 
@@ -145,6 +145,37 @@ def _check_bwd(x, w, dy, s, pre, act, dx, dw, ds):
             v = np.abs(dy64 * a * F._act.sigmoid(ALPHA * a)) * (np.abs(b) + 1)
         tol = (2.0 ** -18 + dy64.shape[1] * 2.0 ** -23) * v.sum(1)
         assert np.all(np.abs(f64(ds) - ref["dscales"]) <= tol + 1e-37)
+
+
+def shifted(t, by=16):
+    """A contiguous copy that starts `by` bytes past an allocation's start."""
+    buf = torch.empty(t.numel() * t.element_size() + by, dtype=torch.uint8, device="cuda")
+    return buf[by:].view(t.dtype).view(t.shape).copy_(t)
+
+
+@pytest.mark.parametrize("N,K,H", [(3, 256, 64), (3, 264, 72), (40, 128, 64), (300, 256, 320)])
+def test_operands_on_16_bytes(N, K, H):
+    """The documented alignment is 16 bytes: 32-byte loads and stores may only be taken where they fit."""
+    lib = rn._load()
+    x, w, dy, s = block(N, K, H, True)
+    y, pre = rn.gated_ffn_fwd(x, w, "swiglu", s, save_pre=True)
+    dx, dw, ds = rn.gated_ffn_bwd(dy, x, w, pre, "swiglu", s)
+    x2, w2, dy2, y2, pre2, dx2, dw2 = (shifted(t) for t in (x, w, dy, y, pre, dx, dw))
+    assert all(t.data_ptr() % 32 == 16 for t in (x2, w2, dy2, y2, pre2, dx2, dw2))
+    for t in (y2, pre2, dx2, dw2):
+        t.zero_()
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    o = rn._Output()
+    o.data, o.out_dtype = y2.data_ptr(), 0
+    st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert lib.rn_gated_ffn_fwd(1, p(x2), p(w2), 0, p(s), N, K, H, 7.0, 1.702, 0, ctypes.byref(o), p(pre2), st) == 0
+    need = rn.gated_ffn_bwd_workspace_bytes(N, K, H)
+    ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")[16:]
+    n = ctypes.c_size_t(need)
+    assert lib.rn_gated_ffn_bwd(1, p(dy2), p(x2), p(w2), p(pre2), 0, p(s), N, K, H, 7.0, 1.702, p(dx2), p(dw2),
+                                p(ds), p(ws), ctypes.byref(n), st) == 0
+    for a, b in ((y, y2), (pre, pre2), (dx, dx2), (dw, dw2)):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("skip", ["dx", "dw", "ds", "both"])

@@ -51,7 +51,7 @@ def proj(x, w):
 SIZES = [(1, 16, 1), (1, 32, 7), (1, 48, 33), (1, 4096, 64), (1, 2064, 250), (2, 4112, 65), (3, 16384, 17),
          (4, 128, 513), (7, 1040, 64), (8, 2048, 100), (9, 512, 96), (13, 5136, 40), (16, 256, 31),
          (17, 1024, 64), (24, 144, 130), (32, 8192, 24), (33, 96, 48), (40, 2080, 66), (100, 1024, 72),
-         (1, 1024, 20000), (3, 65536, 24), (12, 65536, 40), (20, 65520, 16)]
+         (1, 1024, 20000), (5, 4160, 70), (3, 65536, 24), (12, 65536, 40), (20, 65520, 16)]
 
 
 @pytest.mark.parametrize("i,size", list(enumerate(SIZES)), ids=lambda v: str(v))
@@ -99,6 +99,25 @@ def _check_gated(N, K, H, act, scaled, mode, seed):
         assert float(out.scale_inv) == np.float32(1) / np.float32(3.5)
     else:
         check_mx(out.data.cpu().numpy(), out.row_scales.cpu().numpy(), ref, err, "y")
+
+
+def shifted(t, by=16):
+    """A contiguous copy that starts `by` bytes past an allocation's start."""
+    buf = torch.empty(t.numel() * t.element_size() + by, dtype=torch.uint8, device="cuda")
+    out = buf[by:].view(t.dtype).view(t.shape)
+    return out.copy_(t)
+
+
+@pytest.mark.parametrize("N", [1, 13, 24])
+@pytest.mark.parametrize("K", [512, 320, 288, 272])
+def test_operands_on_16_bytes(N, K):
+    """The documented alignment is 16 bytes: 32-byte loads may only be taken where they fit."""
+    x, w = tokens(N, K), weights(96, K)
+    v = rn.NVFP4Output(shifted(w.data), shifted(w.row_scales), w.scale, w.scale_inv, w.amax)
+    assert v.data.data_ptr() % 32 == 16 and shifted(x).data_ptr() % 32 == 16
+    for a, b in ((x, shifted(x)), (shifted(x), x)):
+        assert torch.equal(rn.nvfp4_matvec(a, v), rn.nvfp4_matvec(b, w))
+        assert torch.equal(rn.nvfp4_gated_ffn(a, v), rn.nvfp4_gated_ffn(b, w))
 
 
 def test_every_code_and_scale():
