@@ -50,6 +50,11 @@ constexpr int kDepth = T == 4 ? 2 : 1;
 
 enum WeightKind : int { kWBf16 = 0, kWNvfp4 = 1 };
 
+// Bytes of one fragment of n tokens: 4 lanes x 16 bytes each, and 16 that keep
+// the staging of neighbouring fragments off the same banks (with 16 tokens its
+// stores had taken 32 turns each).
+__host__ __device__ constexpr int frag_row(int n) { return n * 64 + 16; }
+
 // how the weights' rows can be read: in whole chunks and on 32 bytes, in
 // whole 32-byte pieces of a lane, in whole 16-byte halves of one, or any
 enum RowKind : int { kRowsChunks = 0, kRowsPieces = 1, kRowsHalves = 2, kRowsAny = 3 };
@@ -275,7 +280,7 @@ struct Mv {
       for (int f = 0; f < 2; ++f) {
         uint4 b[T];
 #pragma unroll
-        for (int t = 0; t < T; ++t) b[t] = lds16(xs + f * 64 * n + at[t]);
+        for (int t = 0; t < T; ++t) b[t] = lds16(xs + f * frag_row(n) + at[t]);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           const uint4 &u = it.w[m][0][f], &v = it.w[m][1][f];
@@ -300,7 +305,7 @@ struct Mv {
         for (int q = 0; q < 4; ++q) {  // 8 codes of each row
           uint4 b[T];
 #pragma unroll
-          for (int t = 0; t < T; ++t) b[t] = lds16(xs + (f * 4 + q) * 64 * n + at[t]);
+          for (int t = 0; t < T; ++t) b[t] = lds16(xs + (f * 4 + q) * frag_row(n) + at[t]);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             uint32_t v[2][4];
@@ -378,6 +383,8 @@ __device__ __forceinline__ void copy_tokens(const MvParams& p, int lo, int hi, i
   constexpr int CP = M::CK / 8;  // pieces of a token in a chunk
   constexpr int kBatch = 4;
   const int pieces = (hi - lo) * CP;  // per token, 8 elements each
+  for (int i = threadIdx.x; i < (hi - lo) * M::J; i += 32 * W)  // the 16 bytes behind each fragment
+    sts16(xs + i * frag_row(n) + n * 64, make_uint4(0, 0, 0, 0));
   const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)n0 * p.K + (int64_t)lo * M::CK;
   const int left = p.K - lo * M::CK;
   if (pieces > 0) {
@@ -392,7 +399,7 @@ __device__ __forceinline__ void copy_tokens(const MvParams& p, int lo, int hi, i
         v[u] = make_uint4(0, 0, 0, 0);
         if (tok < n && q * 8 < left)
           v[u] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)tok * p.K + q * 8));
-        to[u] = tok < n ? xs + (((q / CP * M::J + q % M::J) * n + tok) * 4 + q % CP / M::J) * 16 : 0u;
+        to[u] = tok < n ? xs + (q / CP * M::J + q % M::J) * frag_row(n) + (tok * 4 + q % CP / M::J) * 16 : 0u;
         q += dq;
         tok += dt;
         if (q >= pieces) {
@@ -416,7 +423,7 @@ __device__ __forceinline__ float stage_tokens(const MvParams& p, int lo, int hi,
     return 1.0f;
   } else {
     __shared__ uint32_t warp_max[W];
-    const int count = (hi - lo) * (Mv<WK, T>::CK / 8) * n;  // 16-byte pieces
+    const int count = (hi - lo) * Mv<WK, T>::J * (frag_row(n) / 16);  // 16-byte pieces
     uint32_t m = 0;                                         // largest magnitude, as bf16 bits
 #pragma unroll 1
     for (int i = threadIdx.x; i < count; i += 32 * W) {
@@ -466,7 +473,7 @@ __device__ __forceinline__ void step_sums(const MvParams& p, int next_tile, int 
                                           const int (&at)[T], Rows& r, Item (&it)[kDepth<T>],
                                           float (&acc)[2][T][4]) {
   using M = Mv<WK, T>;
-  const int stride = M::J * 64 * n;
+  const int stride = M::J * frag_row(n);
   int c = c_lo;
   do {
     // a slot's next item: of this step, or the first ones of the next
@@ -505,7 +512,7 @@ __global__ void __launch_bounds__(32 * W, (T == 1 && W == 8) ? 2 : 1) rn_matvec_
   // sums [batch][rw][n][32]
   const int kPart = W * n * kPartStride;  // floats of the warps' sums of a step
   uint4* xs = smem;
-  float* part = reinterpret_cast<float*>(xs + pl.slab * M::J * 4 * n);
+  float* part = reinterpret_cast<float*>(xs + pl.slab * M::J * (frag_row(n) / 16));
   float* parts = part + 2 * kPart;
   const int lo = rank * pl.part, hi = max(lo, min(lo + pl.part, pl.chunks));
   const int slabs = max(1, (hi - lo + pl.slab - 1) / pl.slab);
@@ -622,7 +629,7 @@ __global__ void __launch_bounds__(32 * W, (T == 1 && W == 8) ? 2 : 1) rn_matvec_
         inv = stage_tokens<WK, T, W>(p, s_lo, max(s_lo, min(s_lo + pl.slab, hi)), n0, n, smem_u32(xs), &wide);
       }
       const int c_lo = chunk_at(sl, wk), c_hi = chunk_at(sl, wk + 1);
-      const uint32_t x = smem_u32(xs) + (c_lo - lo - sl * pl.slab) * (M::J * 64 * n);
+      const uint32_t x = smem_u32(xs) + (c_lo - lo - sl * pl.slab) * (M::J * frag_row(n));
       for (int j = b0; j < b1; ++j) {
         // what follows: the batch's next step, its first with the next slab, the next batch's first
         const bool wrap = j + 1 == b1;
@@ -690,7 +697,7 @@ rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
   const int n = p.N < 8 * T ? p.N : 8 * T;
   const int64_t ny = ((int64_t)p.N + 8 * T - 1) / (8 * T);
   const int tiles = (p.H + RO - 1) / RO;
-  const size_t chunk_bytes = (size_t)M::J * 4 * n * 16;
+  const size_t chunk_bytes = (size_t)M::J * frag_row(n);
   constexpr int PER_SM = T == 1 && W == 8 ? 2 : 1;
   const size_t fixed_bytes = 2 * (size_t)W * n * kPartStride * 4;
   // few row tiles: the reduction over a cluster, while its CTAs' warps keep
@@ -701,7 +708,8 @@ rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
   // warps along the reduction: fewer where it is short and the rows are many
   // (an MXFP8 block needs two row tiles a step), or where its slabs are short
   pl.kw = p.mode == kFfnMx ? W / 2 : W;
-  while (pl.kw > 1 && pl.part < kDepth<T> * pl.kw && (int64_t)tiles * ny * pl.split * pl.kw >= (int64_t)sms * W)
+  constexpr int kLong = T == 1 ? 1 : 4;  // chunks a warp should have of a step
+  while (pl.kw > 1 && pl.part < kLong * pl.kw && (int64_t)tiles * ny * pl.split * pl.kw >= (int64_t)sms * W)
     pl.kw /= 2;
   size_t step_bytes = 0;
   int per = 1;
@@ -731,7 +739,7 @@ rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
     if (pl.slab < 1) return RN_ERR_UNSUPPORTED;
     const int slabs = (pl.part + pl.slab - 1) / pl.slab;
     pl.slab = (pl.part + slabs - 1) / slabs;
-    if (pl.slab >= kDepth<T> * pl.kw || pl.kw == 1) break;
+    if (pl.slab >= kLong * pl.kw || pl.kw == 1 || pl.steps < 2 * per) break;
   }
   size_t smem = pl.slab * chunk_bytes + fixed_bytes;
   if (pl.split > 1)
