@@ -30,6 +30,7 @@ few tokens with the NVFP4 weights that ``quantize_only`` makes.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -458,6 +459,7 @@ def gated_ffn_fwd(x, w, act="swiglu", scales=None, quant="none", limit=7.0, alph
     return res, pre
 
 
+@functools.lru_cache(maxsize=256)
 def gated_ffn_bwd_workspace_bytes(N, K, H) -> int:
     """Workspace bytes ``gated_ffn_bwd`` needs (the query step of the protocol)."""
     n = ctypes.c_size_t(0)
