@@ -141,12 +141,6 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _ok(t, dev, dtype, shape):
-    """Whether ``_need`` would take the tensor; the calls below ask it first, as it is the cheaper."""
-    return (t is not None and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
-            and t.device.index == dev)
-
-
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return _BF16
@@ -398,16 +392,43 @@ def _gated(act):
     return ACTS[act]
 
 
-def _matrix(t, name, dev, dtype=torch.bfloat16):
-    if t is None or len(t.shape) != 2 or not _ok(t, dev, dtype, t.shape):
-        _need(t, name, dtype)
+# Small calls spend more time in these checks than on the device, so each entry
+# point asks for everything at once and goes through the refusals one by one
+# only when something is amiss.
+_BF, _U8, _FP32 = torch.bfloat16, torch.uint8, torch.float32
+
+
+def _matrix(t, name, dtype):
+    _need(t, name, dtype)
+    if t.dim() != 2:
         raise RNError(f"{name} must have 2 dimensions, got {t.dim()}")
     return t.shape
 
 
-def _take(t, name, dev, dtype, shape):
-    if not _ok(t, dev, dtype, shape):
-        _need(t, name, dtype, shape)
+def _refuse_block(x, w, **more):
+    """The refusal of a block's tensors; ``more``: name=(tensor, dtype, (rows, columns) from N, H) pairs."""
+    N, K = _matrix(x, "x", _BF)
+    R = _matrix(w, "w", _BF)[0]
+    if R % 2 or w.shape[1] != K:
+        raise RNError(f"w must have shape (2 H, {K}), got {tuple(w.shape)}")
+    for name, (t, dtype, shape) in more.items():
+        if t is not None:
+            _need(t, name, dtype, shape(N, R // 2))
+    raise RNError("unsupported tensors")
+
+
+def _refuse_nvfp4(x, w, scales, halves):
+    N, K = _matrix(x, "x", _BF)
+    R, half = _matrix(w.data, "w.data", _U8)
+    if K % 16 or half * 2 != K:
+        raise RNError(f"w must hold rows of {K} elements (a multiple of 16), got {2 * half}")
+    _need(w.row_scales, "w.row_scales", _U8, (R, K // 16))
+    _need(w.scale_inv, "w.scale_inv", _FP32, (1,))
+    if halves and R % 2:
+        raise RNError(f"w must have an even number of rows, got {R}")
+    if scales is not None:
+        _need(scales, "scales", _FP32, (N,))
+    raise RNError("unsupported tensors")
 
 
 def _addr(t):
@@ -424,16 +445,38 @@ class _Like:
 
 def _make_rows_output(x, N, H, quant, out_dtype, scale):
     """The output of a block with rows of H: ``x`` gives the device and the default dtype."""
-    if quant not in ("none", "fp8_delayed", "mxfp8"):
+    if quant == "none":
+        o = _Output()
+        data = torch.empty((N, H), dtype=out_dtype or x.dtype, device=x.device)
+        o.data = data.data_ptr()
+        o.out_dtype = _dtype_code(data)
+        return o, data
+    if quant not in ("fp8_delayed", "mxfp8"):
         raise RNError(f"a gated block gives 'none', 'fp8_delayed' or 'mxfp8' output, got {quant!r}")
     return _make_output(_Like((N, H), x.dtype, x.device), quant, out_dtype, scale, True, False)
 
 
-def _ffn_weights(w, K, dev):
-    R = _matrix(w, "w", dev)[0]
-    if R % 2 or w.shape[1] != K:
-        raise RNError(f"w must have shape (2 H, {K}), got {tuple(w.shape)}")
-    return R
+def _scales_ok(scales, N, dev):
+    return scales is None or (scales.dtype is _FP32 and scales.shape == (N,) and scales.is_contiguous()
+                              and scales.device.index == dev)
+
+
+def _block_ok(x, w, dev):
+    return (x.dtype is _BF and w.dtype is _BF and x.dim() == 2 and w.dim() == 2 and w.shape[1] == x.shape[1]
+            and w.shape[0] % 2 == 0 and x.is_contiguous() and w.is_contiguous() and x.device.index == dev
+            and w.device.index == dev and x.is_cuda and w.is_cuda)
+
+
+def _nvfp4_ok(x, w, dev):
+    d, b, si = w.data, w.row_scales, w.scale_inv
+    if not (x.dtype is _BF and d.dtype is _U8 and b.dtype is _U8 and si.dtype is _FP32 and x.dim() == 2
+            and d.dim() == 2):
+        return False
+    K, R = x.shape[1], d.shape[0]
+    return (K % 16 == 0 and d.shape[1] * 2 == K and b.shape == (R, K // 16) and si.shape == (1,)
+            and x.is_contiguous() and d.is_contiguous() and b.is_contiguous() and si.is_contiguous()
+            and x.device.index == dev and d.device.index == dev and b.device.index == dev
+            and si.device.index == dev and x.is_cuda)
 
 
 def gated_ffn_fwd(x, w, act="swiglu", scales=None, quant="none", limit=7.0, alpha=1.702, scale=None,
@@ -445,11 +488,11 @@ def gated_ffn_fwd(x, w, act="swiglu", scales=None, quant="none", limit=7.0, alph
     lib = _lib or _load()
     code = _gated(act)
     dev = torch.cuda.current_device()
-    N, K = _matrix(x, "x", dev)
-    R = _ffn_weights(w, K, dev)
+    if not (_block_ok(x, w, dev) and _scales_ok(scales, x.shape[0], dev)):
+        _refuse_block(x, w, scales=(scales, _FP32, lambda n, h: (n,)))
+    N, K = x.shape
+    R = w.shape[0]
     H = R // 2
-    if scales is not None:
-        _take(scales, "scales", dev, torch.float32, (N,))
     o, res = _make_rows_output(x, N, H, quant, out_dtype, scale)
     pre = torch.empty((N, R), dtype=x.dtype, device=x.device) if save_pre else None
     st = lib.rn_gated_ffn_fwd(code, x.data_ptr(), w.data_ptr(), _BF16, _addr(scales), N, K, H, float(limit),
@@ -476,13 +519,15 @@ def gated_ffn_bwd(dy, x, w, pre, act="swiglu", scales=None, limit=7.0, alpha=1.7
     lib = _lib or _load()
     code = _gated(act)
     dev = torch.cuda.current_device()
-    N, K = _matrix(x, "x", dev)
-    R = _ffn_weights(w, K, dev)
+    if not (_block_ok(x, w, dev) and _scales_ok(scales, x.shape[0], dev) and dy.dtype is _BF
+            and pre.dtype is _BF and dy.shape == (x.shape[0], w.shape[0] // 2)
+            and pre.shape == (x.shape[0], w.shape[0]) and dy.is_contiguous() and pre.is_contiguous()
+            and dy.device.index == dev and pre.device.index == dev):
+        _refuse_block(x, w, dy=(dy, _BF, lambda n, h: (n, h)), pre=(pre, _BF, lambda n, h: (n, 2 * h)),
+                      scales=(scales, _FP32, lambda n, h: (n,)))
+    N, K = x.shape
+    R = w.shape[0]
     H = R // 2
-    _take(dy, "dy", dev, torch.bfloat16, (N, H))
-    _take(pre, "pre", dev, torch.bfloat16, (N, R))
-    if scales is not None:
-        _take(scales, "scales", dev, torch.float32, (N,))
     if not (need_dx or need_dw or dscales):
         raise RNError("nothing to compute: dx, dw and dscales are all skipped")
     if workspace is None:
@@ -502,22 +547,15 @@ def gated_ffn_bwd(dy, x, w, pre, act="swiglu", scales=None, limit=7.0, alpha=1.7
     return dx, dw, ds
 
 
-def _nvfp4_weights(x, w, dev):
-    N, K = _matrix(x, "x", dev)
-    R, half = _matrix(w.data, "w.data", dev, torch.uint8)
-    if K % 16 or half * 2 != K:
-        raise RNError(f"w must hold rows of {K} elements (a multiple of 16), got {2 * half}")
-    _take(w.row_scales, "w.row_scales", dev, torch.uint8, (R, K // 16))
-    _take(w.scale_inv, "w.scale_inv", dev, torch.float32, (1,))
-    return N, K, R
-
-
 def nvfp4_matvec(x, w, out_dtype=None):
     """y = x @ W.T for one or a few tokens: x bf16 [N, K], w the ``NVFP4Output`` of a weight matrix
     [R, K] -> y [N, R] in ``out_dtype`` (x's by default, or float32)."""
     lib = _lib or _load()
     dev = torch.cuda.current_device()
-    N, K, R = _nvfp4_weights(x, w, dev)
+    if not _nvfp4_ok(x, w, dev):
+        _refuse_nvfp4(x, w, None, False)
+    N, K = x.shape
+    R = w.data.shape[0]
     y = torch.empty((N, R), dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
     st = lib.rn_nvfp4_matvec(x.data_ptr(), _BF16, w.data.data_ptr(), w.row_scales.data_ptr(),
                              w.scale_inv.data_ptr(), N, K, R, _dtype_code(y), y.data_ptr(),
@@ -534,11 +572,10 @@ def nvfp4_gated_ffn(x, w, act="swiglu", scales=None, quant="none", limit=7.0, al
     lib = _lib or _load()
     code = _gated(act)
     dev = torch.cuda.current_device()
-    N, K, R = _nvfp4_weights(x, w, dev)
-    if R % 2:
-        raise RNError(f"w must have an even number of rows, got {R}")
-    if scales is not None:
-        _take(scales, "scales", dev, torch.float32, (N,))
+    if not (_nvfp4_ok(x, w, dev) and w.data.shape[0] % 2 == 0 and _scales_ok(scales, x.shape[0], dev)):
+        _refuse_nvfp4(x, w, scales, True)
+    N, K = x.shape
+    R = w.data.shape[0]
     o, res = _make_rows_output(x, N, R // 2, quant, out_dtype, scale)
     st = lib.rn_nvfp4_gated_ffn(code, x.data_ptr(), _BF16, w.data.data_ptr(),
                                 w.row_scales.data_ptr(), w.scale_inv.data_ptr(), _addr(scales), N, K,
