@@ -262,6 +262,38 @@ def test_nothing_is_written_behind_the_outputs(N, K, H):
     assert torch.all(ws[need:] == 0x5A)
 
 
+def test_offsets_past_32_bits():
+    """Projections of more than 2**31 elements: the last tokens' rows, checked against the same tokens alone,
+    forward and backward (a token's row of y, pre and dx does not depend on how many there are)."""
+    N, K, H = 133_000, 64, 8200
+    assert N * 2 * H > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(N, K, generator=g, device="cuda").bfloat16()
+    w = (torch.randn(2 * H, K, generator=g, device="cuda") / 8).bfloat16()
+    dy = torch.randn(N, H, generator=g, device="cuda").bfloat16()
+    y, pre = rn.gated_ffn_fwd(x, w, save_pre=True)
+    dx, dw, ds = rn.gated_ffn_bwd(dy, x, w, pre)
+    for lo in (0, N // 2, N - 300):
+        t = slice(lo, lo + 300)
+        y2, pre2 = rn.gated_ffn_fwd(x[t].contiguous(), w, save_pre=True)
+        assert torch.equal(y[t], y2) and torch.equal(pre[t], pre2)
+        p2 = f64(pre2)
+        ref = F.gated_ffn_bwd(f64(dy[t]), f64(x[t]), f64(w), p2, None, "swiglu")
+        e = 2.0 ** -18 * dp_bound(p2, f64(dy[t]), None, "swiglu")
+        e = e + U * (np.abs(ref["dp"]) + e)
+        aw = np.abs(f64(w))
+        check_grad(f64(dx[t]), ref["dx"], e @ aw + 2 * H * 2.0 ** -23 * ((np.abs(ref["dp"]) + e) @ aw), "dx")
+    # dW over all tokens: a sum of dp^T x over slices of tokens in fp64, on the device
+    want = torch.zeros(2 * H, K, dtype=torch.float64, device="cuda")
+    for lo in range(0, N, 8192):
+        t = slice(lo, lo + 8192)
+        a, b, d = pre[t, :H].double(), pre[t, H:].double(), dy[t].double()
+        sg = torch.sigmoid(a)
+        dp = torch.cat([d * b * sg * (1 + a * (1 - sg)), d * a * sg], 1)
+        want += dp.T @ x[t].double()
+    assert float((dw.double() - want).norm() / want.norm()) <= 4e-3
+
+
 def _step(x, w, dy, s, ws=None):
     y, pre = rn.gated_ffn_fwd(x, w, "clamped_swiglu", s, save_pre=True)
     return (y, pre, *rn.gated_ffn_bwd(dy, x, w, pre, "clamped_swiglu", s, workspace=ws))

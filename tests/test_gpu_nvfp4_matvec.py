@@ -141,6 +141,24 @@ def test_every_code_and_scale():
             assert np.array_equal(f64(y), f64(x) @ F.nvfp4_values(packed.cpu().numpy(), bs, 0.125).T)
 
 
+def test_offsets_past_32_bits():
+    """Weights of more than 4 GiB: the last rows, against the same rows alone."""
+    R, K = 133_000, 65536
+    assert R * K // 2 > 2 ** 32
+    g = torch.Generator(device="cuda").manual_seed(1)
+    one = torch.ones(1, device="cuda")
+    w = rn.NVFP4Output(torch.randint(0, 256, (R, K // 2), generator=g, dtype=torch.uint8, device="cuda"),
+                       torch.randint(0x30, 0x41, (R, K // 16), generator=g, dtype=torch.uint8, device="cuda"),
+                       one, one, one)
+    for N in (1, 12):
+        x = tokens(N, K, N)
+        y = rn.nvfp4_matvec(x, w, out_dtype=torch.float32)
+        for lo in (0, R - 40):
+            part = rn.NVFP4Output(w.data[lo:lo + 40].clone(), w.row_scales[lo:lo + 40].clone(), one, one, one)
+            p, ep = proj(x, part)
+            check_value(f64(y[:, lo:lo + 40]), p, ep, False, "y")
+
+
 def test_wide_range_of_inputs():
     """Activations near bf16's ends keep their products: 2**100 and 2**-100 beside ones whose weight is 0."""
     K, R = 512, 40
