@@ -34,6 +34,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
+// brings a tensor map (a kernel argument) in before its first copy
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* tm) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(tm) : "memory");
+}
+
 // mbar_wait of a converged warp: every lane gets the same answer
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, unsigned* err, unsigned code) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, err, code));
