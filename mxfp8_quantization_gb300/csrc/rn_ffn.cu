@@ -400,19 +400,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (ACT == kActNone) {
         const int c0 = tl.n * 256;
         const bool wide_out = (j.cols & 15) == 0 && (reinterpret_cast<uintptr_t>(j.out) & 31) == 0;
-        for (int c = side * 128; c < side * 128 + 128; c += 32) {
-          if (c0 + c >= j.cols) break;
-          float v[32];
-          tmem_load32(ta + c, v);
-          tmem_load_wait();
+        // all 128 columns at once: one latency of tensor memory, and the
+        // accumulator is free before the stores
+        float v[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c0 + side * 128 + 32 * i < j.cols) tmem_load32(ta + side * 128 + 32 * i, v[i]);
+        tmem_load_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&free_b[acc]), leader));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = c0 + side * 128 + 32 * i;
           if (row < j.rows && j.splits > 1) {
-            float* o = j.part + ((int64_t)tl.split * j.rows + row) * j.cols + c0 + c;
+            float* o = j.part + ((int64_t)tl.split * j.rows + row) * j.cols + c;
 #pragma unroll
             for (int q = 0; q < 32; q += 4)
-              if (c0 + c + q < j.cols)
-                *reinterpret_cast<float4*>(o + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
-          } else if (row < j.rows)
-            store32_bf16(static_cast<uint16_t*>(j.out) + row * j.cols + c0 + c, v, j.cols - c0 - c, wide_out);
+              if (c + q < j.cols)
+                *reinterpret_cast<float4*>(o + q) =
+                    make_float4(v[i][q], v[i][q + 1], v[i][q + 2], v[i][q + 3]);
+          } else if (row < j.rows) {
+            store32_bf16(static_cast<uint16_t*>(j.out) + row * j.cols + c, v[i], j.cols - c, wide_out);
+          }
         }
       } else {
         const int c0 = tl.n * 128;
@@ -426,9 +436,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row < p.f.N) epilogue32<ACT, MODE>(p.f, row, c0 + c, a, b, s, fp8_scale, wide, amax);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&free_b[acc]), leader));
+      if constexpr (ACT != kActNone) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&free_b[acc]), leader));
+      }
     }
     if constexpr (MODE == kFfnFp8) {
       const float m = warp_max_nan(amax);
