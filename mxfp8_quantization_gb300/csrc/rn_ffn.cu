@@ -427,19 +427,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         const int c0 = tl.n * 128;
         const float s = (p.f.scales != nullptr && row < p.f.N) ? __ldg(p.f.scales + row) : 1.0f;
-        for (int c = side * 64; c < side * 64 + 64; c += 32) {
-          if (c0 + c >= p.f.H) break;
-          float a[32], b[32];
-          tmem_load32(ta + c, a);
-          tmem_load32(ta + 128 + c, b);
-          tmem_load_wait();
-          if (row < p.f.N) epilogue32<ACT, MODE>(p.f, row, c0 + c, a, b, s, fp8_scale, wide, amax);
-        }
-      }
-      if constexpr (ACT != kActNone) {
+        float a[2][32], b[2][32];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (c0 + side * 64 + 32 * i < p.f.H) {
+            tmem_load32(ta + side * 64 + 32 * i, a[i]);
+            tmem_load32(ta + 128 + side * 64 + 32 * i, b[i]);
+          }
+        tmem_load_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&free_b[acc]), leader));
+        if (row < p.f.N) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int c = c0 + side * 64 + 32 * i;
+            if (c < p.f.H) epilogue32<ACT, MODE>(p.f, row, c, a[i], b[i], s, fp8_scale, wide, amax);
+          }
+        }
       }
     }
     if constexpr (MODE == kFfnFp8) {
