@@ -35,7 +35,7 @@
 // computation alone 33 us) and 5.3 TB/s in bf16 (1 x 4096 x 8192 gated, 134 MB,
 // 25.1 us); for 8 to 32 tokens the expansion's instructions at 8 to 16 warps an
 // SM and the staging of the tokens in every CTA (8 x 8192 x 65536 71 us, 16
-// 117 us, 32 x 4096 x 32768 78 us).
+// 112 us, 32 x 4096 x 32768 78 us).
 #include <cuda_runtime.h>
 
 #include "rn_act_math.cuh"
@@ -794,7 +794,10 @@ rn_status launch_n(const MvParams& p, int sms, cudaStream_t s) {
   // (each CTA stages its own), else one of 16
   if (p.N <= 8 && (int64_t)p.N * p.K <= 40960) return launch_t<ACT, WK, 1, 8>(p, sms, s);
   if (p.N <= 8) return launch_t<ACT, WK, 1, 16>(p, sms, s);
-  if (p.N <= 16) return launch_t<ACT, WK, 2, 8>(p, sms, s);
+  // 9 to 16: 12 warps, what 65536 registers hold without spills (16 x 4096 x
+  // 8192 gated NVFP4 21.5 us, 24.2 with 8 warps, 24.4 with 8 of two items in
+  // flight; 13 x 5136 x 8200 27.5, 29.0, 29.2)
+  if (p.N <= 16) return launch_t<ACT, WK, 2, 12>(p, sms, s);
   return launch_t<ACT, WK, 4, 8>(p, sms, s);
 }
 
