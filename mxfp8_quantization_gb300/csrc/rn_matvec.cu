@@ -170,6 +170,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 struct Item {
   uint4 w[2][2][2];
   uint32_t s[2][2];
+  // 9 to 16 tokens, rows whose scales lie on any byte: the word behind, and by
+  // how many bits the four codes stand off (a byte for each row)
+  uint32_t s_next[2][2], off;
 };
 
 __device__ __forceinline__ void sts16(uint32_t addr, const uint4& v) {
@@ -239,9 +242,39 @@ struct Mv {
           ldg_w32(r.w[m][h] + at / 2, it.w[m][h]);
           it.s[m][h] = __ldg(reinterpret_cast<const unsigned*>(r.s[m][h] + at / 16));
         }
+    } else if (T == 2 && left >= 128) {
+      // The piece, and four blocks behind it, are in the row: its codes from
+      // fixed offsets, its scales as the two words around them, put together
+      // when they are used (13 x 5136 x 8200 20.5 us; put together here, where
+      // the warp has to wait for them, 22.8).  Not with other numbers of tokens,
+      // whose registers are all in use: 1 x 8192 x 65536 64.5 us instead of
+      // 61.1, 5 x 2080 x 5000 gated 13.7 instead of 12.4.
+      it.off = 0;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* w = r.w[m][h] + d * kWBytes;
+          if (p.rows == kRowsHalves) {
+            it.w[m][h][0] = ldg_w16(w);
+            it.w[m][h][1] = ldg_w16(w + 16);
+          } else {
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const uint2 a = ldg_w8(w + f * 16), b = ldg_w8(w + f * 16 + 8);
+              it.w[m][h][f] = make_uint4(a.x, a.y, b.x, b.y);
+            }
+          }
+          const uintptr_t sc = reinterpret_cast<uintptr_t>(r.s[m][h] + d * kSBytes);
+          const unsigned* at = reinterpret_cast<const unsigned*>(sc & ~(uintptr_t)3);
+          it.s[m][h] = __ldg(at);
+          it.s_next[m][h] = __ldg(at + 1);
+          it.off |= (uint32_t)(sc & 3) << (3 + 8 * (m * 2 + h));
+        }
     } else {
-      // the same in blocks
+      // at the row's end: block after block, past it the last one again
       const bool whole = p.rows == kRowsHalves;
+      it.off = 0;
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -249,6 +282,7 @@ struct Mv {
           const uint8_t* w = r.w[m][h] + d * kWBytes;
           const uint8_t* sc = r.s[m][h] + d * kSBytes;
           it.s[m][h] = 0;
+          it.s_next[m][h] = 0;
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
             const int o0 = min(f * 32, left - 16), o1 = min(f * 32 + 16, left - 16);  // of two blocks
@@ -280,11 +314,12 @@ struct Mv {
     for (int t = 0; t < T; ++t) at[t] = (min(t * 8 + (lane >> 2), n - 1) * 4 + (lane & 3)) * 16;
   }
 
-  // acc += item x tokens; xs: the chunk's fragments (a shared-memory address:
-  // through a pointer the compiler had lost the address space, 72 against 62
-  // us at 1 x 8192 x 65536), at: this lane's offsets in them
+  // acc += item x tokens; shifted: the item's scales are in two words; xs: the
+  // chunk's fragments (a shared-memory address: through a pointer the compiler
+  // had lost the address space, 72 against 62 us at 1 x 8192 x 65536), at: this
+  // lane's offsets in them
   template <bool WIDE>
-  __device__ __forceinline__ static void compute(const Item& it, uint32_t xs, int n,
+  __device__ __forceinline__ static void compute(const Item& it, bool shifted, uint32_t xs, int n,
                                                  const int (&at)[T], float (&acc)[2][T][4]) {
     if constexpr (WK == kWBf16) {
 #pragma unroll
@@ -311,7 +346,11 @@ struct Mv {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) s2[m][h] = e4m3x2_f16(f == 0 ? it.s[m][h] : it.s[m][h] >> 16);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t s4 = shifted ? __funnelshift_r(it.s[m][h], it.s_next[m][h], it.off >> (8 * (m * 2 + h)))
+                                        : it.s[m][h];
+            s2[m][h] = e4m3x2_f16(f == 0 ? s4 : s4 >> 16);
+          }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {  // 8 codes of each row
           uint4 b[T];
@@ -496,7 +535,8 @@ __device__ __forceinline__ void step_sums(const MvParams& p, int next_tile, int 
     const int from = last ? n_lo : c + kDepth<T>, to = last ? n_hi : c_hi;
 #pragma unroll
     for (int d = 0; d < kDepth<T>; ++d) {
-      if (c + d < c_hi) M::template compute<WIDE>(it[d], x + d * stride, n, at, acc);
+      if (c + d < c_hi)
+        M::template compute<WIDE>(it[d], T == 2 && p.rows >= kRowsHalves, x + d * stride, n, at, acc);
       if (from + d < to) M::load(p, r, from, d, lane, it[d]);
     }
     c += kDepth<T>;

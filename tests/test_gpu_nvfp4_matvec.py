@@ -185,6 +185,21 @@ def test_non_finite_rows_stay_in_their_rows():
     assert not torch.isfinite(y[9].float()).any()
 
 
+@pytest.mark.parametrize("N", [1, 9, 16, 17])
+@pytest.mark.parametrize("K", [16, 48, 96, 112, 128, 144, 240, 272, 304, 400, 528, 5136])
+def test_scales_of_neighbouring_rows_stay_apart(N, K):
+    # every second row's scales are NaN: the rows between end and begin beside them, on any byte
+    R = 37
+    x, w = tokens(N, K, K), weights(R, K, K)
+    want = rn.nvfp4_matvec(x, w, out_dtype=torch.float32)
+    p, ep = proj(x, w)
+    check_value(f64(want), p, ep, False, "y")
+    w.row_scales[1::2] = 0x7F
+    y = rn.nvfp4_matvec(x, w, out_dtype=torch.float32)
+    assert torch.equal(y[:, 0::2], want[:, 0::2])
+    assert torch.isnan(y[:, 1::2]).all()
+
+
 def test_empty_batch():
     w = weights(64, 32)
     x = torch.empty(0, 32, device="cuda", dtype=torch.bfloat16)
