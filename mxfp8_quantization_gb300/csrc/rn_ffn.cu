@@ -17,7 +17,7 @@
 // tile while the next is being summed.
 //
 // What bounds it is the tensor pipe: 93 % (forward) and 97 % (backward) of the
-// active cycles; 8192 x 4096 x 8192 (N x K x H) forward 543 us, 2027 TFLOP/s in a
+// active cycles; 8192 x 4096 x 8192 (N x K x H) forward 541 us, 2032 TFLOP/s in a
 // burst (1690 in a long loop, at the power cap), backward's products 1130 us,
 // 1945 TFLOP/s.  Eight epilogue warps with 32-byte stores: a forward that keeps
 // the projections, 8192 x 1024 x 4096, 120 us with four and 16-byte stores, 90 us

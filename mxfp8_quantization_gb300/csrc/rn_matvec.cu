@@ -30,7 +30,7 @@
 // them slab after slab and keeps its steps' sums.  The parts meet in shared
 // memory and are added in a fixed order.
 //
-// What bounds it: for one token the weights' read, 5.1 TB/s at 1 x 8192 x 65536
+// What bounds it: for one token the weights' read, 5.0 TB/s at 1 x 8192 x 65536
 // (59-61 us for 302 MB; the same loads with nothing computed took 49 us, the
 // computation alone 33 us) and 5.3 TB/s in bf16 (1 x 4096 x 8192 gated, 134 MB,
 // 25.1 us); for 8 to 32 tokens the expansion's instructions at 8 to 16 warps an

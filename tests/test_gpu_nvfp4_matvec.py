@@ -101,6 +101,17 @@ def _check_gated(N, K, H, act, scaled, mode, seed):
         check_mx(out.data.cpu().numpy(), out.row_scales.cpu().numpy(), ref, err, "y")
 
 
+@pytest.mark.parametrize("N", [3, 9, 16, 30])
+@pytest.mark.parametrize("K", [96, 1040, 2048])
+def test_many_rows(N, K):
+    # rows enough that a CTA's warps take several row tiles each, the reduction short or of middle length
+    x, w = tokens(N, K, N), weights(20000, K, K)
+    p, ep = proj(x, w)
+    check_value(f64(rn.nvfp4_matvec(x, w, out_dtype=torch.float32)), p, ep, False, "y")
+    _check_gated(N, K, 9984, "swiglu", True, "mxfp8", K)
+    _check_gated(N, K, 9999, "clamped_swiglu", False, "bf16", K)
+
+
 def shifted(t, by=16):
     """A contiguous copy that starts `by` bytes past an allocation's start."""
     buf = torch.empty(t.numel() * t.element_size() + by, dtype=torch.uint8, device="cuda")
