@@ -581,6 +581,10 @@ __global__ void __launch_bounds__(32 * W, (T == 1 && W == 8) ? 2 : 1) rn_matvec_
     }
     fence_barrier_init();
   }
+  // every CTA of the cluster has to have started before the first sums go to
+  // another one's shared memory; waited for behind the staging
+  __syncwarp();
+  if (pl.split > 1) cluster_arrive();
   // nothing of the caller's memory is touched until the kernel before has completed
   pdl_launch_dependents();
   pdl_wait();
@@ -678,6 +682,10 @@ __global__ void __launch_bounds__(32 * W, (T == 1 && W == 8) ? 2 : 1) rn_matvec_
         __syncthreads();
         const int s_lo = lo + sl * pl.slab;
         inv = stage_tokens<WK, T, W>(p, s_lo, max(s_lo, min(s_lo + pl.slab, hi)), n0, n, smem_u32(xs), &wide);
+        if (pl.split > 1 && b0 == 0 && sl == 0) {
+          __syncwarp();
+          cluster_wait();
+        }
       }
       const int c_lo = chunk_at(sl, wk), c_hi = chunk_at(sl, wk + 1);
       const uint32_t x = smem_u32(xs) + (c_lo - lo - sl * pl.slab) * (M::J * frag_row(n));

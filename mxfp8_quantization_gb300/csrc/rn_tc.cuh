@@ -17,9 +17,18 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// The cluster's barrier, and its two halves: what a thread does between them is
+// ordered neither way.  Another CTA's shared memory may be touched only after
+// a barrier of the whole cluster: until then that CTA need not have started.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 
 // the same shared-memory address in CTA `rank` of the cluster

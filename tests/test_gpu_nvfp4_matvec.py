@@ -254,6 +254,25 @@ def test_repeats_and_replays(N, K, H):
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
 
 
+@pytest.mark.parametrize("N,K,R", [(1, 4096, 64), (1, 4096, 4096), (3, 16384, 40), (12, 4096, 96), (20, 4096, 64)])
+def test_clusters_that_start_apart(N, K, R):
+    """Few rows and a long reduction go to clusters of CTAs; launches on two streams crowd each other, so that
+    a cluster's CTAs find their places at different times."""
+    x, w = tokens(N, K, N), weights(R, K, R)
+    want = rn.nvfp4_matvec(x, w, out_dtype=torch.float32)
+    p, ep = proj(x, w)
+    check_value(f64(want), p, ep, False, "y")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(100):
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append(rn.nvfp4_matvec(x, w, out_dtype=torch.float32))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+
+
 def test_generation_step_together():
     """RMSNorm -> gated block -> down projection on NVFP4 weights, as one token is generated; the block
     with bf16 weights of the same values gives the same result within both bounds."""
