@@ -200,7 +200,6 @@ __device__ __forceinline__ void split_epilogue(const GemmParams& p, int cluster,
   const uint32_t ta = tmem + ((uint32_t)lb << 16);
   if (works) ok = mbar_wait_warp(done, 0, &g_err_ffn, kErrStatsWait) && ok;
   tc_fence_after();
-  __syncwarp();
   cluster_sync();  // no pair's operands are needed any more
   if (works) {
     for (int q = 0; q < p.pairs; ++q) {
@@ -217,7 +216,6 @@ __device__ __forceinline__ void split_epilogue(const GemmParams& p, int cluster,
       }
     }
   }
-  __syncwarp();
   cluster_sync();
   if (works && side * 32 < w) {
     const Tile tl = tile_at(p, cluster);

@@ -583,7 +583,6 @@ __global__ void __launch_bounds__(32 * W, (T == 1 && W == 8) ? 2 : 1) rn_matvec_
   }
   // every CTA of the cluster has to have started before the first sums go to
   // another one's shared memory; waited for behind the staging
-  __syncwarp();
   if (pl.split > 1) cluster_arrive();
   // nothing of the caller's memory is touched until the kernel before has completed
   pdl_launch_dependents();
@@ -640,7 +639,6 @@ __global__ void __launch_bounds__(32 * W, (T == 1 && W == 8) ? 2 : 1) rn_matvec_
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * 4),
                      "f"(cta_sum(i / (n * 32), i / 32 % n, i & 31))
                      : "memory");
-      __syncwarp();
       cluster_sync();
       if (rank == leader) {
         const auto sum = [&](int tile, int tok, int row) {
@@ -682,10 +680,7 @@ __global__ void __launch_bounds__(32 * W, (T == 1 && W == 8) ? 2 : 1) rn_matvec_
         __syncthreads();
         const int s_lo = lo + sl * pl.slab;
         inv = stage_tokens<WK, T, W>(p, s_lo, max(s_lo, min(s_lo + pl.slab, hi)), n0, n, smem_u32(xs), &wide);
-        if (pl.split > 1 && b0 == 0 && sl == 0) {
-          __syncwarp();
-          cluster_wait();
-        }
+        if (pl.split > 1 && b0 == 0 && sl == 0) cluster_wait();
       }
       const int c_lo = chunk_at(sl, wk), c_hi = chunk_at(sl, wk + 1);
       const uint32_t x = smem_u32(xs) + (c_lo - lo - sl * pl.slab) * (M::J * frag_row(n));

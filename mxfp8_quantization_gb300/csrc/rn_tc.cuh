@@ -20,10 +20,14 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // The cluster's barrier, and its two halves: what a thread does between them is
 // ordered neither way.  Another CTA's shared memory may be touched only after
 // a barrier of the whole cluster: until then that CTA need not have started.
+// The instructions are the warp's (.aligned), so its lanes come together first:
+// the code in front often ends with a branch of one lane.
 __device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_sync() {

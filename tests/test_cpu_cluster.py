@@ -48,7 +48,7 @@ def test_few_token_kernel_meets_before_its_first_remote_store():
     assert k.index("cluster_arrive();") < k.index("stage_tokens<") < meet < k.index("for (int j = b0") < first_held
     # once, by every thread of a cluster and by no other CTA
     assert re.search(r"if \(pl\.split > 1\) cluster_arrive\(\);", k)
-    assert re.search(r"if \(pl\.split > 1 && b0 == 0 && sl == 0\) \{\s*(__syncwarp\(\);\s*)?cluster_wait\(\);", k)
+    assert re.search(r"if \(pl\.split > 1 && b0 == 0 && sl == 0\) cluster_wait\(\);", k)
     assert k.count("cluster_arrive();") == k.count("cluster_wait();") == 1
 
 
@@ -57,6 +57,14 @@ def test_block_kernel_meets_before_its_first_remote_operation():
     meet = k.index("cluster_sync();")
     for op in ("tma_load_2d(", "mma_bf16_pair(", "mma_commit(", "map_to_rank(", "split_epilogue<"):
         assert meet < k.index(op), op
+
+
+def test_cluster_barriers_take_whole_warps():
+    """barrier.cluster.*.aligned is executed by a converged warp, whatever branch came before it."""
+    for half in ("cluster_arrive", "cluster_wait"):
+        b = body(source("rn_tc.cuh"), half)
+        assert b.index("__syncwarp();") < b.index(".aligned")
+    assert "barrier.cluster" not in source("rn_matvec.cu") + source("rn_ffn.cu")
 
 
 @pytest.mark.parametrize("name", ["rn_matvec.cu", "rn_ffn.cu"])
