@@ -406,19 +406,23 @@ def _matrix(t, name, dtype):
 
 
 def _refuse_block(x, w, **more):
-    """The refusal of a block's tensors; ``more``: name=(tensor, dtype, (rows, columns) from N, H) pairs."""
+    """The refusal of a block's tensors; ``more``: name=(tensor, dtype, shape from N and H)."""
     N, K = _matrix(x, "x", _BF)
     R = _matrix(w, "w", _BF)[0]
     if R % 2 or w.shape[1] != K:
         raise RNError(f"w must have shape (2 H, {K}), got {tuple(w.shape)}")
     for name, (t, dtype, shape) in more.items():
-        if t is not None:
+        if t is not None or name != "scales":
             _need(t, name, dtype, shape(N, R // 2))
     raise RNError("unsupported tensors")
 
 
 def _refuse_nvfp4(x, w, scales, halves):
     N, K = _matrix(x, "x", _BF)
+    if w is None:
+        raise RNError("w is required")
+    if not hasattr(w, "row_scales"):
+        raise RNError(f"w must be an NVFP4Output, got {type(w).__name__}")
     R, half = _matrix(w.data, "w.data", _U8)
     if K % 16 or half * 2 != K:
         raise RNError(f"w must hold rows of {K} elements (a multiple of 16), got {2 * half}")
@@ -461,22 +465,38 @@ def _scales_ok(scales, N, dev):
                               and scales.device.index == dev)
 
 
+# a tensor that is missing (None) is refused by its name, like any other
 def _block_ok(x, w, dev):
-    return (x.dtype is _BF and w.dtype is _BF and x.dim() == 2 and w.dim() == 2 and w.shape[1] == x.shape[1]
-            and w.shape[0] % 2 == 0 and x.is_contiguous() and w.is_contiguous() and x.device.index == dev
-            and w.device.index == dev and x.is_cuda and w.is_cuda)
+    try:
+        return (x.dtype is _BF and w.dtype is _BF and x.dim() == 2 and w.dim() == 2 and w.shape[1] == x.shape[1]
+                and w.shape[0] % 2 == 0 and x.is_contiguous() and w.is_contiguous() and x.device.index == dev
+                and w.device.index == dev and x.is_cuda and w.is_cuda)
+    except AttributeError:
+        return False
+
+
+def _grads_ok(dy, pre, x, w, dev):
+    try:
+        return (dy.dtype is _BF and pre.dtype is _BF and dy.shape == (x.shape[0], w.shape[0] // 2)
+                and pre.shape == (x.shape[0], w.shape[0]) and dy.is_contiguous() and pre.is_contiguous()
+                and dy.device.index == dev and pre.device.index == dev)
+    except AttributeError:
+        return False
 
 
 def _nvfp4_ok(x, w, dev):
-    d, b, si = w.data, w.row_scales, w.scale_inv
-    if not (x.dtype is _BF and d.dtype is _U8 and b.dtype is _U8 and si.dtype is _FP32 and x.dim() == 2
-            and d.dim() == 2):
+    try:
+        d, b, si = w.data, w.row_scales, w.scale_inv
+        if not (x.dtype is _BF and d.dtype is _U8 and b.dtype is _U8 and si.dtype is _FP32 and x.dim() == 2
+                and d.dim() == 2):
+            return False
+        K, R = x.shape[1], d.shape[0]
+        return (K % 16 == 0 and d.shape[1] * 2 == K and b.shape == (R, K // 16) and si.shape == (1,)
+                and x.is_contiguous() and d.is_contiguous() and b.is_contiguous() and si.is_contiguous()
+                and x.device.index == dev and d.device.index == dev and b.device.index == dev
+                and si.device.index == dev and x.is_cuda)
+    except AttributeError:
         return False
-    K, R = x.shape[1], d.shape[0]
-    return (K % 16 == 0 and d.shape[1] * 2 == K and b.shape == (R, K // 16) and si.shape == (1,)
-            and x.is_contiguous() and d.is_contiguous() and b.is_contiguous() and si.is_contiguous()
-            and x.device.index == dev and d.device.index == dev and b.device.index == dev
-            and si.device.index == dev and x.is_cuda)
 
 
 def gated_ffn_fwd(x, w, act="swiglu", scales=None, quant="none", limit=7.0, alpha=1.702, scale=None,
@@ -519,10 +539,7 @@ def gated_ffn_bwd(dy, x, w, pre, act="swiglu", scales=None, limit=7.0, alpha=1.7
     lib = _lib or _load()
     code = _gated(act)
     dev = torch.cuda.current_device()
-    if not (_block_ok(x, w, dev) and _scales_ok(scales, x.shape[0], dev) and dy.dtype is _BF
-            and pre.dtype is _BF and dy.shape == (x.shape[0], w.shape[0] // 2)
-            and pre.shape == (x.shape[0], w.shape[0]) and dy.is_contiguous() and pre.is_contiguous()
-            and dy.device.index == dev and pre.device.index == dev):
+    if not (_block_ok(x, w, dev) and _scales_ok(scales, x.shape[0], dev) and _grads_ok(dy, pre, x, w, dev)):
         _refuse_block(x, w, dy=(dy, _BF, lambda n, h: (n, h)), pre=(pre, _BF, lambda n, h: (n, 2 * h)),
                       scales=(scales, _FP32, lambda n, h: (n,)))
     N, K = x.shape

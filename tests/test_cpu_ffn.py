@@ -201,3 +201,26 @@ def test_binding_nvfp4_refusals(lib, dev0, w, match):
 def test_binding_nvfp4_gated_needs_two_halves(lib, dev0):
     with pytest.raises(rn.RNError, match="even"):
         rn.nvfp4_gated_ffn(Fake((4, 64)), _w(R=63))
+
+
+@pytest.mark.parametrize("name", ["x", "w", "dy", "pre"])
+def test_binding_names_a_missing_tensor(lib, dev0, name):
+    # pre is None after a forward without save_pre
+    a = {"dy": Fake((4, 32)), "x": Fake((4, 64)), "w": Fake((64, 64)), "pre": Fake((4, 64)), name: None}
+    with pytest.raises(rn.RNError, match=f"{name} is required"):
+        rn.gated_ffn_bwd(a["dy"], a["x"], a["w"], a["pre"])
+    if name in ("x", "w"):
+        with pytest.raises(rn.RNError, match=f"{name} is required"):
+            rn.gated_ffn_fwd(a["x"], a["w"])
+
+
+@pytest.mark.parametrize("x,w,match", [
+    (None, _w(), "x is required"), (Fake((4, 64)), None, "w is required"),
+    (Fake((4, 64)), Fake((64, 64)), "NVFP4Output"), (Fake((4, 64)), _w(data=None), "w.data is required"),
+    (Fake((4, 64)), _w(row_scales=None), "w.row_scales is required"),
+    (Fake((4, 64)), _w(scale_inv=None), "w.scale_inv is required")], ids=lambda v: str(v)[:20])
+def test_binding_names_what_is_missing_of_nvfp4_weights(lib, dev0, x, w, match):
+    with pytest.raises(rn.RNError, match=match):
+        rn.nvfp4_matvec(x, w)
+    with pytest.raises(rn.RNError, match=match):
+        rn.nvfp4_gated_ffn(x, w)
