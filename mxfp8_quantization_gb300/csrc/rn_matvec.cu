@@ -41,6 +41,7 @@
 #include "rn_act_math.cuh"
 #include "rn_device.cuh"
 #include "rn_internal.h"
+#include "rn_matvec_plan.h"
 #include "rn_tc.cuh"
 
 namespace rn {
@@ -50,7 +51,6 @@ __device__ unsigned g_err_mv;
 
 constexpr int kWBytes = 128;     // of a row's weights in a chunk
 constexpr int kSBytes = 16;      // of its scales (NVFP4)
-constexpr int kPartStride = 36;  // floats per token of a warp's sums (32 rows, no bank conflicts)
 
 // items in flight per warp: two only with 32 tokens, where a CTA is 8 warps of
 // up to 255 registers
@@ -59,24 +59,9 @@ constexpr int kDepth = T == 4 ? 2 : 1;
 
 enum WeightKind : int { kWBf16 = 0, kWNvfp4 = 1 };
 
-// Bytes of one fragment of n tokens: 4 lanes x 16 bytes each, and 16 that keep
-// the staging of neighbouring fragments off the same banks (with 16 tokens its
-// stores had taken 32 turns each).
-__host__ __device__ constexpr int frag_row(int n) { return n * 64 + 16; }
-
 // how the weights' rows can be read: in whole chunks and on 32 bytes, in
 // whole 32-byte pieces of a lane, in whole 16-byte halves of one, or any
 enum RowKind : int { kRowsChunks = 0, kRowsPieces = 1, kRowsHalves = 2, kRowsAny = 3 };
-
-struct MvPlan {
-  int kw;       // warps along the reduction
-  int split;    // CTAs of a cluster along the reduction
-  int chunks;   // chunks (256 NVFP4 / 64 bf16 elements) of the reduction
-  int part;     // chunks per CTA of the cluster
-  int slab;     // chunks whose tokens are in shared memory at a time
-  int steps;    // groups of W / kw row tiles
-  int batch;    // steps whose sums are kept while the slabs change (slab < part)
-};
 
 // weights: read once, so 32-byte loads (a whole sector) leave L1 alone; of
 // narrower ones several share a sector, which L1 keeps for them (13 x 5136 x
@@ -739,67 +724,13 @@ __global__ void __launch_bounds__(32 * W, (T == 1 && W == 8) ? 2 : 1) rn_matvec_
   if (pl.split > 1) cluster_sync();  // no CTA leaves while another writes to it
 }
 
-constexpr size_t kMvSmem = 224 * 1024;  // shared memory of a CTA
-
 template <int ACT, int WK, int T, int W>
 rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
-  using M = Mv<WK, T>;
   auto k = rn_matvec_kernel<ACT, WK, T, W>;
-  constexpr int RO = ACT == kActNone ? 32 : 16;  // outputs of a row tile
-  MvPlan pl{};
-  pl.chunks = (p.K + M::CK - 1) / M::CK;
-  const int n = p.N < 8 * T ? p.N : 8 * T;
-  const int64_t ny = ((int64_t)p.N + 8 * T - 1) / (8 * T);
-  const int tiles = (p.H + RO - 1) / RO;
-  const size_t chunk_bytes = (size_t)M::J * frag_row(n);
-  constexpr int PER_SM = T == 1 && W == 8 ? 2 : 1;
-  const size_t fixed_bytes = 2 * (size_t)W * n * kPartStride * 4;
-  // few row tiles: the reduction over a cluster, while its CTAs' warps keep
-  // two chunks each
-  pl.split = 1;
-  while (pl.split < 8 && tiles * ny * pl.split < sms && pl.chunks >= 2 * W * pl.split) pl.split *= 2;
-  pl.part = (pl.chunks + pl.split - 1) / pl.split;
-  // warps along the reduction: fewer where it is short and the rows are many
-  // (an MXFP8 block needs two row tiles a step), or where its slabs are short
-  pl.kw = p.mode == kFfnMx ? W / 2 : W;
-  constexpr int kLong = T == 1 ? 1 : 4;  // chunks a warp should have of a step
-  while (pl.kw > 1 && pl.part < kLong * pl.kw && (int64_t)tiles * ny * pl.split * pl.kw >= (int64_t)sms * W)
-    pl.kw /= 2;
-  size_t step_bytes = 0;
-  int per = 1;
-  for (;; pl.kw /= 2) {
-    const int rw = W / pl.kw;
-    pl.steps = (tiles + rw - 1) / rw;
-    step_bytes = (size_t)rw * n * 32 * 4;
-    // the tokens whole where there is room; else in slabs (and no cluster)
-    pl.slab = pl.part;
-    size_t cluster_bytes = pl.split > 1 ? pl.split * step_bytes : 0;
-    if (pl.slab * chunk_bytes + fixed_bytes + cluster_bytes > kMvSmem / PER_SM) {
-      pl.split = 1;
-      pl.part = pl.slab = pl.chunks;
-      cluster_bytes = 0;
-    }
-    per = PER_SM * sms / pl.split;  // clusters or CTAs of one token group
-    if (per > pl.steps) per = pl.steps;
-    if (per < 1) per = 1;
-    pl.batch = (pl.steps + per - 1) / per;
-    const size_t room = kMvSmem / PER_SM - fixed_bytes - cluster_bytes;
-    if (pl.slab * chunk_bytes <= room) break;
-    // a third of the room at most for the steps' sums
-    const int fit = (int)(room / 3 / step_bytes);
-    if (pl.batch > fit) pl.batch = fit;
-    if (pl.batch < 1) return RN_ERR_UNSUPPORTED;
-    pl.slab = (int)((room - pl.batch * step_bytes) / chunk_bytes);
-    if (pl.slab < 1) return RN_ERR_UNSUPPORTED;
-    const int slabs = (pl.part + pl.slab - 1) / pl.slab;
-    pl.slab = (pl.part + slabs - 1) / slabs;
-    if (pl.slab >= kLong * pl.kw || pl.kw == 1 || pl.steps < 2 * per) break;
-  }
-  size_t smem = pl.slab * chunk_bytes + fixed_bytes;
-  if (pl.split > 1)
-    smem += pl.split * step_bytes;
-  else if (pl.slab < pl.part)
-    smem += pl.batch * step_bytes;
+  MvLaunch l{};
+  if (!mv_plan({p.N, p.K, p.H, WK == kWNvfp4, ACT != kActNone, p.mode == kFfnMx, T, W}, sms, &l))
+    return RN_ERR_UNSUPPORTED;
+  const MvPlan& pl = l.plan;
   static std::atomic<int> kept[kMaxDevices];
   if (once_per_device(kept, [&] {
         return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMvSmem) == cudaSuccess
@@ -807,12 +738,11 @@ rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
                    : -1;
       }) < 1)
     return RN_ERR_CUDA;
-  if (ny > 65535) return RN_ERR_UNSUPPORTED;
-  const int groups = per;
+  if (l.ny > 65535) return RN_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(groups * pl.split), (unsigned)ny);
+  cfg.gridDim = dim3((unsigned)(l.groups * pl.split), (unsigned)l.ny);
   cfg.blockDim = dim3(32 * W);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = l.smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   int na = 0;
@@ -832,18 +762,11 @@ rn_status launch_t(const MvParams& p, int sms, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? RN_OK : RN_ERR_CUDA;
 }
 
-// groups of 8, 16 or 32 tokens
 template <int ACT, int WK>
 rn_status launch_n(const MvParams& p, int sms, cudaStream_t s) {
-  // up to 8 tokens: two CTAs an SM of 8 warps while their tokens are small
-  // (each CTA stages its own), else one of 16
-  if (p.N <= 8 && (int64_t)p.N * p.K <= 40960) return launch_t<ACT, WK, 1, 8>(p, sms, s);
-  if (p.N <= 8) return launch_t<ACT, WK, 1, 16>(p, sms, s);
-  // 9 to 16: 12 warps, what 65536 registers hold without spills (16 x 4096 x
-  // 8192 gated NVFP4 21.5 us, 24.2 with 8 warps, 24.4 with 8 of two items in
-  // flight; 13 x 5136 x 8200 27.5, 29.0, 29.2)
-  if (p.N <= 16) return launch_t<ACT, WK, 2, 12>(p, sms, s);
-  return launch_t<ACT, WK, 4, 8>(p, sms, s);
+  const MvVariant v = mv_variant(p.N, p.K);
+  if (v.T == 1) return v.W == 8 ? launch_t<ACT, WK, 1, 8>(p, sms, s) : launch_t<ACT, WK, 1, 16>(p, sms, s);
+  return v.T == 2 ? launch_t<ACT, WK, 2, 12>(p, sms, s) : launch_t<ACT, WK, 4, 8>(p, sms, s);
 }
 
 }  // namespace

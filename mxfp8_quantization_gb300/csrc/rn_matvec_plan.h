@@ -1,0 +1,130 @@
+// How the few-token kernel (rn_matvec.cu) splits its work: host arithmetic
+// only, no CUDA, so that it can be compiled and examined by itself.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#if defined(__CUDACC__)
+#define RN_HOST_DEVICE __host__ __device__
+#else
+#define RN_HOST_DEVICE
+#endif
+
+namespace rn {
+
+constexpr int kPartStride = 36;  // floats per token of a warp's sums (32 rows, no bank conflicts)
+
+// Bytes of one fragment of n tokens: 4 lanes x 16 bytes each, and 16 that keep
+// the staging of neighbouring fragments off the same banks (with 16 tokens its
+// stores had taken 32 turns each).
+RN_HOST_DEVICE constexpr int frag_row(int n) { return n * 64 + 16; }
+
+constexpr size_t kMvSmem = 224 * 1024;  // shared memory of an SM's CTAs
+
+struct MvPlan {
+  int kw;       // warps along the reduction
+  int split;    // CTAs of a cluster along the reduction
+  int chunks;   // chunks (256 NVFP4 / 64 bf16 elements) of the reduction
+  int part;     // chunks per CTA of the cluster
+  int slab;     // chunks whose tokens are in shared memory at a time
+  int steps;    // groups of W / kw row tiles
+  int batch;    // steps whose sums are kept while the slabs change (slab < part)
+};
+
+// the problem as the kernel variant sees it
+struct MvShape {
+  int N, K, H;   // tokens, reduction, outputs
+  bool nvfp4;    // else bf16 weights
+  bool gated;    // a row tile is 16 gate and 16 linear rows (else 32 rows)
+  bool mx;       // MXFP8 output
+  int T, W;      // groups of 8 tokens a CTA holds, its warps
+};
+
+// Groups of 8 tokens a CTA holds and its warps, for N tokens.  Up to 8 tokens:
+// two CTAs an SM of 8 warps while their tokens are small (each CTA stages its
+// own), else one of 16.  9 to 16: 12 warps, what 65536 registers hold without
+// spills (16 x 4096 x 8192 gated NVFP4 21.5 us, 24.2 with 8 warps, 24.4 with 8 of
+// two items in flight; 13 x 5136 x 8200 27.5, 29.0, 29.2).
+struct MvVariant {
+  int T, W;
+};
+inline MvVariant mv_variant(int N, int K) {
+  if (N <= 8) return {1, (int64_t)N * K <= 40960 ? 8 : 16};
+  if (N <= 16) return {2, 12};
+  return {4, 8};
+}
+
+struct MvLaunch {
+  MvPlan plan;
+  int groups;    // clusters (or CTAs) a group of tokens gets
+  int64_t ny;    // groups of tokens
+  size_t smem;   // dynamic shared memory of a CTA
+};
+
+// false: no plan
+inline bool mv_plan(const MvShape& s, int sms, MvLaunch* out) {
+  const int T = s.T, W = s.W;
+  const int CK = s.nvfp4 ? 256 : 64, J = CK / 32;
+  const int RO = s.gated ? 16 : 32;  // outputs of a row tile
+  MvPlan pl{};
+  pl.chunks = (s.K + CK - 1) / CK;
+  const int n = s.N < 8 * T ? s.N : 8 * T;
+  const int64_t ny = ((int64_t)s.N + 8 * T - 1) / (8 * T);
+  const int tiles = (s.H + RO - 1) / RO;
+  const size_t chunk_bytes = (size_t)J * frag_row(n);
+  const int per_sm = T == 1 && W == 8 ? 2 : 1;
+  const size_t fixed_bytes = 2 * (size_t)W * n * kPartStride * 4;
+  // few row tiles: the reduction over a cluster, while its CTAs' warps keep
+  // two chunks each
+  pl.split = 1;
+  while (pl.split < 8 && tiles * ny * pl.split < sms && pl.chunks >= 2 * W * pl.split) pl.split *= 2;
+  pl.part = (pl.chunks + pl.split - 1) / pl.split;
+  // warps along the reduction: fewer where it is short and the rows are many
+  // (an MXFP8 block needs two row tiles a step), or where its slabs are short
+  pl.kw = s.mx ? W / 2 : W;
+  const int long_ = T == 1 ? 1 : 4;  // chunks a warp should have of a step
+  while (pl.kw > 1 && pl.part < long_ * pl.kw && (int64_t)tiles * ny * pl.split * pl.kw >= (int64_t)sms * W)
+    pl.kw /= 2;
+  size_t step_bytes = 0;
+  int per = 1;
+  for (;; pl.kw /= 2) {
+    const int rw = W / pl.kw;
+    pl.steps = (tiles + rw - 1) / rw;
+    step_bytes = (size_t)rw * n * 32 * 4;
+    // the tokens whole where there is room; else in slabs (and no cluster)
+    pl.slab = pl.part;
+    size_t cluster_bytes = pl.split > 1 ? pl.split * step_bytes : 0;
+    if (pl.slab * chunk_bytes + fixed_bytes + cluster_bytes > kMvSmem / per_sm) {
+      pl.split = 1;
+      pl.part = pl.slab = pl.chunks;
+      cluster_bytes = 0;
+    }
+    per = per_sm * sms / pl.split;  // clusters or CTAs of one token group
+    if (per > pl.steps) per = pl.steps;
+    if (per < 1) per = 1;
+    pl.batch = (pl.steps + per - 1) / per;
+    const size_t room = kMvSmem / per_sm - fixed_bytes - cluster_bytes;
+    if (pl.slab * chunk_bytes <= room) break;
+    // a third of the room at most for the steps' sums
+    const int fit = (int)(room / 3 / step_bytes);
+    if (pl.batch > fit) pl.batch = fit;
+    if (pl.batch < 1) return false;
+    pl.slab = (int)((room - pl.batch * step_bytes) / chunk_bytes);
+    if (pl.slab < 1) return false;
+    const int slabs = (pl.part + pl.slab - 1) / pl.slab;
+    pl.slab = (pl.part + slabs - 1) / slabs;
+    if (pl.slab >= long_ * pl.kw || pl.kw == 1 || pl.steps < 2 * per) break;
+  }
+  out->smem = pl.slab * chunk_bytes + fixed_bytes;
+  if (pl.split > 1)
+    out->smem += pl.split * step_bytes;
+  else if (pl.slab < pl.part)
+    out->smem += pl.batch * step_bytes;
+  out->plan = pl;
+  out->groups = per;
+  out->ny = ny;
+  return true;
+}
+
+}  // namespace rn

@@ -1,0 +1,47 @@
+"""The few-token kernel's plan on the host: that it covers the work, and fits."""
+import math
+import random
+
+import pytest
+
+from matvec_plan import plan
+
+STATIC = 1024  # the kernel's own shared memory is below that, and the driver keeps 1 KB a CTA
+
+
+def draws(n=4000, seed=1):
+    r = random.Random(seed)
+
+    def logs(lo, hi, step):
+        return max(step, int(math.exp(r.uniform(math.log(lo), math.log(hi)))) // step * step)
+
+    for _ in range(n):
+        nvfp4 = r.random() < 0.75
+        gated = not nvfp4 or r.random() < 0.5
+        N = logs(1, 200, 1) if nvfp4 else logs(1, 32, 1)
+        mx = gated and r.random() < 0.3
+        yield dict(N=N, K=logs(8, 131072, 16 if nvfp4 else 8), H=logs(1, 200000, 32 if mx else 1), nvfp4=nvfp4,
+                   gated=gated, mx=mx)
+
+
+def test_every_plan_covers_the_work_and_fits():
+    for c in draws():
+        p = plan(**c)
+        assert p is not None, c
+        ck = 256 if c["nvfp4"] else 64
+        assert p.chunks * ck >= c["K"] > (p.chunks - 1) * ck, c
+        assert p.split in (1, 2, 4, 8) and p.split * p.part >= p.chunks, c
+        assert p.W % p.kw == 0 and 1 <= p.kw <= p.W, c
+        assert p.steps * p.rw >= p.tiles > (p.steps - 1) * p.rw, c
+        assert 1 <= p.groups <= p.steps and p.ny * 8 * p.T >= c["N"], c
+        assert 1 <= p.slab <= p.part and p.batch >= 1, c
+        if c["mx"]:
+            assert p.rw * 16 % 32 == 0, c          # a step's outputs are whole blocks
+        # tokens, two steps' sums, a cluster's sums, and the sums that are kept while slabs change
+        step = p.rw * p.n * 32 * 4
+        need = p.slab * (ck // 32) * (p.n * 64 + 16) + 2 * p.W * p.n * 36 * 4
+        need += p.split * step if p.split > 1 else 0
+        need += p.batch * step if p.slabs > 1 else 0
+        assert p.smem == need, c
+        assert (p.smem + STATIC) * p.per_sm <= 227 * 1024, c
+        assert p.batch >= p.rounds or p.slabs > 1, c
