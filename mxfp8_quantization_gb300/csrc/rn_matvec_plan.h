@@ -62,6 +62,30 @@ struct MvLaunch {
   size_t smem;   // dynamic shared memory of a CTA
 };
 
+// The last halving of the warps along the reduction may leave fewer steps than
+// SMs (12 warps go from 3 to 1).  Then more of them are taken if the warp with
+// the most to do gets clearly less that way, a sixth: its chunks are those of a
+// step times the rounds of steps, and with 9 tokens or more a step costs about
+// a third of a chunk besides (its sums).  us, 12 / 6 / 4 / 3 / 2 / 1 warps along
+// the reduction of 16 x 2048 x 20000: 18.9 / 19.3 / 18.0 / 21.5 / 17.4 / 24.4,
+// 16 x 2048 x 32768: 23.9 / 24.0 / 24.0 / 22.0 / 28.2 / 25.6, 9 x 528 x 21128: 18.2 /
+// 13.8 / 11.9 / 11.9 / 10.5 / 13.4; 8 / 4 / 2 / 1, 1 x 624 x 8797 gated: 8.2 / 6.8 /
+// 8.0 / 10.8 and, kept at 1 with its 79 steps, 30 x 1040 x 20000: 26.1 / 28.3 / 29.1 /
+// 26.0.
+inline int mv_more_along(const MvShape& s, int tiles, int64_t ny, const MvPlan& pl, int sms, int per_sm) {
+  const auto steps = [&](int kw) { return (tiles + s.W / kw - 1) / (s.W / kw) * ny * pl.split; };
+  const auto work = [&](int kw) {
+    const int64_t rounds = (steps(kw) + (int64_t)sms * per_sm - 1) / ((int64_t)sms * per_sm);
+    return 3 * rounds * ((pl.part + kw - 1) / kw) + (s.T > 1 ? rounds : 0);
+  };
+  int best = pl.kw;
+  if (steps(pl.kw) < sms)
+    for (int kw = pl.kw + 1; kw <= s.W; ++kw)
+      if (s.W % kw == 0 && !(s.mx && s.W / kw % 2 != 0) && work(kw) < work(best) && 6 * work(kw) < 5 * work(pl.kw))
+        best = kw;
+  return best;
+}
+
 // false: no plan
 inline bool mv_plan(const MvShape& s, int sms, MvLaunch* out) {
   const int T = s.T, W = s.W;
@@ -82,10 +106,11 @@ inline bool mv_plan(const MvShape& s, int sms, MvLaunch* out) {
   pl.part = (pl.chunks + pl.split - 1) / pl.split;
   // warps along the reduction: fewer where it is short and the rows are many
   // (an MXFP8 block needs two row tiles a step), or where its slabs are short
-  pl.kw = s.mx ? W / 2 : W;
   const int long_ = T == 1 ? 1 : 4;  // chunks a warp should have of a step
+  pl.kw = s.mx ? W / 2 : W;
   while (pl.kw > 1 && pl.part < long_ * pl.kw && (int64_t)tiles * ny * pl.split * pl.kw >= (int64_t)sms * W)
     pl.kw /= 2;
+  pl.kw = mv_more_along(s, tiles, ny, pl, sms, per_sm);
   size_t step_bytes = 0;
   int per = 1;
   for (;; pl.kw /= 2) {

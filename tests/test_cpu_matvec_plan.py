@@ -45,3 +45,30 @@ def test_every_plan_covers_the_work_and_fits():
         assert p.smem == need, c
         assert (p.smem + STATIC) * p.per_sm <= 227 * 1024, c
         assert p.batch >= p.rounds or p.slabs > 1, c
+
+
+def busiest(p, kw):
+    """Chunks of the warp with the most to do, tokens whole, with kw warps along the reduction."""
+    steps = -(-p.tiles // (p.W // kw)) * p.ny * p.split
+    return -(-steps // (152 * p.per_sm)) * -(-p.part // kw)
+
+
+def test_no_plan_leaves_sms_idle_that_would_help():
+    """Where a plan has fewer CTAs than SMs, no other number of warps along the reduction gives the busiest warp
+    half as much to do or less (with at most twice the rounds of steps)."""
+    for c in [dict(N=16, K=2048, H=20000), dict(N=16, K=2048, H=10240, gated=True), *draws()]:
+        p = plan(**c)
+        if p.ctas >= 152 or p.slabs > 1:
+            continue
+        now = busiest(p, p.kw)
+        for kw in range(p.kw + 1, p.W + 1):
+            steps = -(-p.tiles // (p.W // kw)) * p.ny * p.split
+            if p.W % kw or (c.get("mx") and p.W // kw % 2) or steps > 2 * 152 * p.per_sm:
+                continue
+            assert 2 * busiest(p, kw) > now, (c, p.kw, kw)
+
+
+def test_twelve_warps_take_the_divisors_in_between():
+    # 3 warps along the reduction halve to 1, which leaves 53 and 86 CTAs
+    assert plan(16, 2048, 20000).ctas == 105 and plan(16, 2048, 32768).ctas == 152
+    assert plan(30, 1040, 20000).ctas == 79      # kept: no number of warps gives the busiest less

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import mxfp8_quantization_gb300 as rn
+import matvec_plan
 from ffn_check import ALPHA, LIM, check_codes, check_mx, check_value, ep_bound, y_bound
 from oracle import ffn as F
 from test_gpu_ffn import MODES, f64, np_scales
@@ -110,6 +111,20 @@ def test_many_rows(N, K):
     check_value(f64(rn.nvfp4_matvec(x, w, out_dtype=torch.float32)), p, ep, False, "y")
     _check_gated(N, K, 9984, "swiglu", True, "mxfp8", K)
     _check_gated(N, K, 9999, "clamped_swiglu", False, "bf16", K)
+
+
+@pytest.mark.parametrize("N,K,H,gated,mode,kw", [(16, 2048, 20000, False, "f32", 2), (16, 2048, 32768, False, "f32", 3),
+                                                 (12, 2208, 16068, True, "bf16", 3), (11, 784, 6000, True, "f32", 4),
+                                                 (10, 512, 10240, True, "mxfp8", 2), (1, 624, 8797, True, "fp8_delayed", 4)])
+def test_warps_along_the_reduction(N, K, H, gated, mode, kw):
+    """Numbers of warps along the reduction that the halving alone does not come to."""
+    assert matvec_plan.plan(N, K, H, True, gated, mode == "mxfp8").kw == kw
+    if gated:
+        _check_gated(N, K, H, "swiglu", True, mode, N)
+    else:
+        x, w = tokens(N, K, N), weights(H, K, K)
+        p, ep = proj(x, w)
+        check_value(f64(rn.nvfp4_matvec(x, w, out_dtype=torch.float32)), p, ep, False, "y")
 
 
 def shifted(t, by=16):
