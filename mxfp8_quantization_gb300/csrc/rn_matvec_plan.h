@@ -86,23 +86,18 @@ inline int mv_more_along(const MvShape& s, int tiles, int64_t ny, const MvPlan& 
   return best;
 }
 
-// false: no plan
-inline bool mv_plan(const MvShape& s, int sms, MvLaunch* out) {
+// The plan whose reduction is split over clusters of pl.split CTAs, at most
+// `clusters` of them a group of tokens; false: there is none.
+inline bool mv_plan_split(const MvShape& s, int sms, MvPlan pl, int clusters, MvLaunch* out) {
   const int T = s.T, W = s.W;
-  const int CK = s.nvfp4 ? 256 : 64, J = CK / 32;
+  const int J = s.nvfp4 ? 8 : 2;     // 16-byte pieces of a token a lane reads per chunk
   const int RO = s.gated ? 16 : 32;  // outputs of a row tile
-  MvPlan pl{};
-  pl.chunks = (s.K + CK - 1) / CK;
   const int n = s.N < 8 * T ? s.N : 8 * T;
   const int64_t ny = ((int64_t)s.N + 8 * T - 1) / (8 * T);
   const int tiles = (s.H + RO - 1) / RO;
-  const size_t chunk_bytes = (size_t)J * frag_row(n);
+  const int64_t chunk_bytes = (int64_t)J * frag_row(n);
   const int per_sm = T == 1 && W == 8 ? 2 : 1;
-  const size_t fixed_bytes = 2 * (size_t)W * n * kPartStride * 4;
-  // few row tiles: the reduction over a cluster, while its CTAs' warps keep
-  // two chunks each
-  pl.split = 1;
-  while (pl.split < 8 && tiles * ny * pl.split < sms && pl.chunks >= 2 * W * pl.split) pl.split *= 2;
+  const int64_t fixed_bytes = 2ll * W * n * kPartStride * 4;
   pl.part = (pl.chunks + pl.split - 1) / pl.split;
   // warps along the reduction: fewer where it is short and the rows are many
   // (an MXFP8 block needs two row tiles a step), or where its slabs are short
@@ -111,28 +106,22 @@ inline bool mv_plan(const MvShape& s, int sms, MvLaunch* out) {
   while (pl.kw > 1 && pl.part < long_ * pl.kw && (int64_t)tiles * ny * pl.split * pl.kw >= (int64_t)sms * W)
     pl.kw /= 2;
   pl.kw = mv_more_along(s, tiles, ny, pl, sms, per_sm);
-  size_t step_bytes = 0;
+  int64_t step_bytes = 0, cluster_bytes = 0;
   int per = 1;
   for (;; pl.kw /= 2) {
     const int rw = W / pl.kw;
     pl.steps = (tiles + rw - 1) / rw;
-    step_bytes = (size_t)rw * n * 32 * 4;
-    // the tokens whole where there is room; else in slabs (and no cluster)
-    pl.slab = pl.part;
-    size_t cluster_bytes = pl.split > 1 ? pl.split * step_bytes : 0;
-    if (pl.slab * chunk_bytes + fixed_bytes + cluster_bytes > kMvSmem / per_sm) {
-      pl.split = 1;
-      pl.part = pl.slab = pl.chunks;
-      cluster_bytes = 0;
-    }
-    per = per_sm * sms / pl.split;  // clusters or CTAs of one token group
-    if (per > pl.steps) per = pl.steps;
+    step_bytes = (int64_t)rw * n * 32 * 4;
+    cluster_bytes = pl.split > 1 ? pl.split * step_bytes : 0;
+    per = clusters < pl.steps ? clusters : pl.steps;
     if (per < 1) per = 1;
     pl.batch = (pl.steps + per - 1) / per;
-    const size_t room = kMvSmem / per_sm - fixed_bytes - cluster_bytes;
+    // the tokens whole where there is room, else in slabs
+    pl.slab = pl.part;
+    const int64_t room = (int64_t)(kMvSmem / per_sm) - fixed_bytes - cluster_bytes;
     if (pl.slab * chunk_bytes <= room) break;
     // a third of the room at most for the steps' sums
-    const int fit = (int)(room / 3 / step_bytes);
+    const int fit = room > 0 ? (int)(room / 3 / step_bytes) : 0;
     if (pl.batch > fit) pl.batch = fit;
     if (pl.batch < 1) return false;
     pl.slab = (int)((room - pl.batch * step_bytes) / chunk_bytes);
@@ -141,15 +130,60 @@ inline bool mv_plan(const MvShape& s, int sms, MvLaunch* out) {
     pl.slab = (pl.part + slabs - 1) / slabs;
     if (pl.slab >= long_ * pl.kw || pl.kw == 1 || pl.steps < 2 * per) break;
   }
-  out->smem = pl.slab * chunk_bytes + fixed_bytes;
-  if (pl.split > 1)
-    out->smem += pl.split * step_bytes;
-  else if (pl.slab < pl.part)
-    out->smem += pl.batch * step_bytes;
+  out->smem = (size_t)(pl.slab * chunk_bytes + fixed_bytes + cluster_bytes);
+  if (pl.slab < pl.part) out->smem += (size_t)(pl.batch * step_bytes);
   out->plan = pl;
   out->groups = per;
   out->ny = ny;
   return true;
+}
+
+// What a plan in slabs costs, in the time a CTA takes to stage the tokens of a
+// chunk (32 tokens: 1.1 us): every batch of steps stages them again, a round of
+// steps has in each slab the chunks of its busiest warp at about 2 and 1 for
+// the sums, and in a cluster 2 a row tile to exchange them.  us against the
+// cost, clusters of 1 / 2 / 4 / 8: 32 x 16384 x 1024 86 (88), 46 (46), 25 (24), 37
+// (28); 32 x 16384 x 4096 87 (88), 66 (60), 60 (54); 20 x 16384 x 2048 57, 32 (44),
+// 26 (30), 36 (42); 12 x 65536 x 40 121, 66, 34, 20.
+inline int64_t mv_slab_cost(const MvShape& s, const MvLaunch& l) {
+  const MvPlan& p = l.plan;
+  const int64_t rounds = (p.steps + l.groups - 1) / l.groups;
+  const int64_t slabs = (p.part + p.slab - 1) / p.slab;
+  const int64_t batches = slabs > 1 ? (rounds + p.batch - 1) / p.batch : 1;
+  return batches * p.part + rounds * slabs * (2 * ((p.slab + p.kw - 1) / p.kw) + 1) +
+         (p.split > 1 ? 2 * rounds * (s.W / p.kw) : 0);
+}
+
+// false: no plan
+inline bool mv_plan(const MvShape& s, int sms, MvLaunch* out) {
+  const int CK = s.nvfp4 ? 256 : 64;
+  const int RO = s.gated ? 16 : 32;
+  const int64_t ny = ((int64_t)s.N + 8 * s.T - 1) / (8 * s.T);
+  const int tiles = (s.H + RO - 1) / RO;
+  const int per_sm = s.T == 1 && s.W == 8 ? 2 : 1;
+  MvPlan pl{};
+  pl.chunks = (s.K + CK - 1) / CK;
+  // few row tiles: the reduction over a cluster, while its CTAs' warps keep
+  // two chunks each
+  pl.split = 1;
+  while (pl.split < 8 && tiles * ny * pl.split < sms && pl.chunks >= 2 * s.W * pl.split) pl.split *= 2;
+  const bool found = mv_plan_split(s, sms, pl, per_sm * sms / pl.split, out);
+  if (pl.split == 1 || (found && out->plan.slab == out->plan.part)) return found;
+  // The tokens of a cluster's CTA do not fit: in slabs, by the cheapest split
+  // (up to 8 tokens fit a cluster of 8 up to K = 88064: no slabs in clusters for
+  // them).  So many clusters of 1, 2, 4, 8 CTAs with an SM each run at a time on a
+  // GB300 of 152 SMs.
+  const int resident[4] = {sms, sms / 2, sms * 36 / 152, sms * 15 / 152};
+  bool any = false;
+  for (int i = 0; i < 4; ++i) {
+    pl.split = 1 << i;
+    MvLaunch l{};
+    if (!mv_plan_split(s, sms, pl, resident[i] > ny ? (int)(resident[i] / ny) : 1, &l)) continue;
+    if (s.T == 1 && i > 0 && l.plan.slab < l.plan.part) continue;
+    if (!any || mv_slab_cost(s, l) < mv_slab_cost(s, *out)) *out = l;
+    any = true;
+  }
+  return any;
 }
 
 }  // namespace rn

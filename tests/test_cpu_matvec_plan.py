@@ -72,3 +72,24 @@ def test_twelve_warps_take_the_divisors_in_between():
     # 3 warps along the reduction halve to 1, which leaves 53 and 86 CTAs
     assert plan(16, 2048, 20000).ctas == 105 and plan(16, 2048, 32768).ctas == 152
     assert plan(30, 1040, 20000).ctas == 79      # kept: no number of warps gives the busiest less
+
+
+def test_clusters_whose_tokens_do_not_fit_go_on_in_slabs():
+    """Few rows and a long reduction: the reduction stays split over clusters where a CTA's tokens do not fit."""
+    assert plan(24, 16384, 512).ctas == 128
+    for N, K, H, least in [(32, 16384, 64, 16), (32, 16384, 512, 64), (32, 16384, 1024, 128), (32, 16384, 2048, 128),
+                           (32, 12288, 1024, 128), (32, 12288, 4096, 128), (12, 65536, 40, 16), (8, 88064, 64, 16)]:
+        assert plan(N, K, H).ctas >= least, (N, K, H)
+    for K in range(4096, 16385, 512):
+        for N in range(17, 32):
+            a, b = plan(N, K, 512), plan(N + 1, K, 512)
+            assert 2 * b.ctas >= a.ctas, (N, K)  # a token more does not idle most of the machine
+
+
+def test_slabs_of_a_cluster():
+    for c in draws(seed=2):
+        p = plan(**c)
+        if p.split > 1 and p.slabs > 1:
+            assert p.T > 1
+            assert p.slab * p.slabs >= p.part and (p.slabs - 1) * p.slab < p.part, c
+            assert p.groups * p.ny <= max(p.ny, 152 // p.split), c  # no second wave of clusters

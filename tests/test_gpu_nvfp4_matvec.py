@@ -127,6 +127,78 @@ def test_warps_along_the_reduction(N, K, H, gated, mode, kw):
         check_value(f64(rn.nvfp4_matvec(x, w, out_dtype=torch.float32)), p, ep, False, "y")
 
 
+def codes(R, K, seed):
+    """Any codes, block scales in [0.5, 2], projections of spread about 2 for tokens of spread 1; made on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    si = torch.full((1,), 0.6 / K ** 0.5, device="cuda")
+    return rn.NVFP4Output(torch.randint(0, 256, (R, K // 2), generator=g, dtype=torch.uint8, device="cuda"),
+                          torch.randint(0x30, 0x41, (R, K // 16), generator=g, dtype=torch.uint8, device="cuda"),
+                          1 / si, si, si)
+
+
+def some_outputs(H):
+    """Blocks of 32 outputs at the start, in the middle and at the end, and the last ones."""
+    at = {0, H // 64 * 32, max(0, H // 32 * 32 - 32)}
+    cols = sorted({c for a in at for c in range(a, min(a + 32, H))} | set(range(H // 32 * 32, H)))
+    return torch.tensor(cols, device="cuda")
+
+
+def check_some(x, w, H, gated, mode):
+    """Some outputs against the oracle."""
+    cols = some_outputs(H)
+    rows = torch.cat([cols, cols + H]) if gated else cols
+    part = rn.NVFP4Output(w.data[rows], w.row_scales[rows], w.scale, w.scale_inv, w.amax)
+    p, ep = proj(x, part)
+    if not gated:
+        y = rn.nvfp4_matvec(x, w, out_dtype=torch.float32)
+        check_value(f64(y[:, cols]), p, ep, False, "y")
+        return
+    ref, err = F._act.scaled_act_fwd(p, None, "swiglu")["y"], y_bound(p, ep, None, "swiglu")
+    y32 = rn.nvfp4_gated_ffn(x, w, out_dtype=torch.float32)
+    check_value(f64(y32[:, cols]), ref, err, False, "y")
+    if mode == "bf16":
+        check_value(f64(rn.nvfp4_gated_ffn(x, w)[:, cols]), ref, err, True, "y")
+    elif mode == "fp8_delayed":
+        out = rn.nvfp4_gated_ffn(x, w, quant=mode, scale=3.5)
+        check_codes(out.data[:, cols].cpu().numpy(), ref, err, 3.5, "y")
+        assert float(out.amax) == float(y32.abs().max())        # the same sums
+    elif mode == "mxfp8":
+        out = rn.nvfp4_gated_ffn(x, w, quant=mode)
+        blocks = cols[::32] // 32
+        check_mx(out.data[:, cols].cpu().numpy(), out.row_scales[:, blocks].cpu().numpy(), ref, err, "y")
+
+
+@pytest.mark.parametrize("N,K,H,gated,mode,rounds,batches", [
+    (32, 16384, 64, False, "f32", 1, 1), (32, 16384, 1024, False, "f32", 1, 1), (32, 16384, 4096, False, "f32", 2, 1),
+    (30, 16384, 1024, True, "mxfp8", 1, 1), (32, 12288, 500, True, "fp8_delayed", 1, 1), (12, 65536, 40, False, "f32", 1, 1),
+    (16, 32768, 4096, False, "f32", 2, 1), (16, 49152, 500, True, "bf16", 2, 1), (24, 32768, 512, True, "mxfp8", 2, 1),
+    (40, 16384, 200, True, "bf16", 1, 1)])
+def test_clusters_with_slabs(N, K, H, gated, mode, rounds, batches):
+    """The reduction over a cluster whose CTAs take their tokens slab after slab."""
+    p = matvec_plan.plan(N, K, H, True, gated, mode == "mxfp8")
+    assert p.split > 1 and p.slabs > 1 and (p.rounds, p.batches) == (rounds, batches)
+    check_some(tokens(N, K, N), codes(H * (1 + gated), K, N), H, gated, mode)
+
+
+@pytest.mark.parametrize("N,K,H,split", [(9, 12288, 5000, 1), (17, 8192, 5000, 1), (32, 16384, 512, 4), (12, 65536, 40, 8)])
+@pytest.mark.parametrize("where", [0, 1])
+def test_slabs_of_different_scale(N, K, H, split, where):
+    """One slab's tokens span too much for f16 and stay bf16, another's are far smaller and scaled by their own
+    power of two."""
+    p = matvec_plan.plan(N, K, H)
+    assert p.split == split and p.slabs > 1
+    x, w = tokens(N, K, N), codes(H, K, N)
+    slab = p.slab * 256
+    if where == 0:
+        w.data[:, :8] = 0                                     # the large elements' weights are 0
+        x[:, :16] = 2.0 ** 60
+        x[:, slab:] *= 2.0 ** -20
+    else:
+        x[:, :slab] *= 2.0 ** -30
+        x[:, slab + 7] *= 2.0 ** -40                          # beside ordinary ones
+    check_some(x, w, H, False, "f32")
+
+
 def shifted(t, by=16):
     """A contiguous copy that starts `by` bytes past an allocation's start."""
     buf = torch.empty(t.numel() * t.element_size() + by, dtype=torch.uint8, device="cuda")
