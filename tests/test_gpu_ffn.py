@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import matvec_plan
 import mxfp8_quantization_gb300 as rn
 import oracle
 from ffn_check import (ALPHA, LIM, U, check_codes, check_grad, check_mx, check_value, dp_bound, ep_bound,
@@ -95,6 +96,36 @@ def test_forward_modes(mode, act, N, K, H):
 @pytest.mark.parametrize("N,K,H", [(40, 2568, 1056), (300, 2056, 160), (200, 1288, 2080), (130, 4104, 288)])
 def test_forward_shared_tiles(mode, N, K, H):
     _check_fwd(N, K, H, "clamped_swiglu" if N == 40 else "swiglu", N != 130, mode, True, seed=2)
+
+
+@pytest.mark.parametrize("N,K,H,mode,split,slabs,rounds", [
+    (8, 8192, 504, "bf16", 8, 1, 2), (9, 6144, 1504, "f32", 2, 1, 2), (32, 8192, 1024, "fp8_delayed", 4, 1, 2),
+    (12, 8192, 2560, "mxfp8", 1, 2, 1), (8, 16384, 8192, "bf16", 1, 2, 4), (32, 12288, 504, "bf16", 8, 2, 2),
+    (30, 20480, 512, "mxfp8", 8, 2, 2)])
+def test_few_token_plans_of_every_kind(N, K, H, mode, split, slabs, rounds):
+    """Clusters that run several steps, slabs of tokens, and both; some outputs of each against the oracle."""
+    p = matvec_plan.plan(N, K, H, nvfp4=False, gated=True, mx=mode == "mxfp8")
+    assert (p.split, p.slabs, p.rounds) == (split, slabs, rounds)
+    g = torch.Generator(device="cuda").manual_seed(N)
+    x = torch.randn(N, K, generator=g, device="cuda").bfloat16()
+    w = (torch.randn(2 * H, K, generator=g, device="cuda") * (2 / K ** 0.5)).bfloat16()
+    s = torch.rand(N, generator=g, device="cuda")
+    quant = "none" if mode in ("bf16", "f32") else mode
+    out, pre = rn.gated_ffn_fwd(x, w, "clamped_swiglu", s, quant=quant, scale=3.5 if mode == "fp8_delayed" else None,
+                                out_dtype=torch.float32 if mode == "f32" else None, save_pre=True)
+    cols = torch.tensor(sorted({c for a in (0, H // 64 * 32, H // 32 * 32 - 32) for c in range(a, a + 32)}
+                               | set(range(H // 32 * 32, H))), device="cuda")
+    x64, w64 = f64(x), f64(w[torch.cat([cols, cols + H])])
+    ref = F.gated_ffn_fwd(x64, w64, np_scales(s), "clamped_swiglu", limit=LIM, alpha=ALPHA)
+    ep = ep_bound(x64, w64)
+    err = y_bound(ref["p"], ep, np_scales(s), "clamped_swiglu")
+    check_value(f64(pre[:, torch.cat([cols, cols + H])]), ref["p"], ep, True, "pre")
+    if mode in ("bf16", "f32"):
+        check_value(f64(out[:, cols]), ref["y"], err, mode == "bf16", "y")
+    elif mode == "fp8_delayed":
+        check_codes(out.data[:, cols].cpu().numpy(), ref["y"], err, 3.5, "y")
+    else:
+        check_mx(out.data[:, cols].cpu().numpy(), out.row_scales[:, cols[::32] // 32].cpu().numpy(), ref["y"], err, "y")
 
 
 @pytest.mark.parametrize("i,size", list(enumerate(SIZES)), ids=lambda v: str(v))

@@ -180,6 +180,22 @@ def test_clusters_with_slabs(N, K, H, gated, mode, rounds, batches):
     check_some(tokens(N, K, N), codes(H * (1 + gated), K, N), H, gated, mode)
 
 
+@pytest.mark.parametrize("N,K,H,gated,mode,split,slabs,rounds,batches", [
+    # clusters that run several steps, so that their leaders change and the sums' places are used again
+    (8, 8192, 2500, False, "f32", 2, 1, 2, 1), (16, 20000, 500, False, "f32", 8, 1, 2, 1),
+    (17, 16384, 1500, True, "bf16", 4, 1, 2, 1), (9, 24576, 1504, True, "mxfp8", 8, 1, 2, 1),
+    (8, 40000, 2000, True, "fp8_delayed", 4, 1, 4, 1), (12, 49152, 2048, True, "bf16", 8, 1, 5, 1),
+    # slabs whose steps' sums are kept, plain and gated; two batches of steps over the slabs
+    (32, 4096, 32768, False, "f32", 1, 3, 2, 1), (32, 4096, 32768, True, "fp8_delayed", 1, 3, 2, 2),
+    (24, 4096, 10016, True, "mxfp8", 1, 2, 2, 1), (9, 12288, 5024, True, "mxfp8", 1, 2, 2, 1),
+    (8, 12288, 2500, True, "bf16", 1, 2, 2, 1), (32, 8192, 20000, False, "f32", 1, 5, 2, 1),
+    (16, 16384, 30000, False, "f32", 1, 4, 2, 1)])
+def test_plans_of_every_kind(N, K, H, gated, mode, split, slabs, rounds, batches):
+    p = matvec_plan.plan(N, K, H, True, gated, mode == "mxfp8")
+    assert (p.split, p.slabs, p.rounds, p.batches) == (split, slabs, rounds, batches)
+    check_some(tokens(N, K, N), codes(H * (1 + gated), K, N), H, gated, mode)
+
+
 @pytest.mark.parametrize("N,K,H,split", [(9, 12288, 5000, 1), (17, 8192, 5000, 1), (32, 16384, 512, 4), (12, 65536, 40, 8)])
 @pytest.mark.parametrize("where", [0, 1])
 def test_slabs_of_different_scale(N, K, H, split, where):
