@@ -344,6 +344,10 @@ rn_status rn_scaled_act_bwd(rn_act act, const void* dy, const void* x, rn_dtype 
  * dtype must be RN_BF16 (RN_F32 returns RN_ERR_UNSUPPORTED: the tensor cores
  * have no product that keeps fp32).  K % 8 == 0, H % 8 == 0, any N; x, w,
  * pre and out->data 16-byte aligned.  Outputs must not overlap inputs.
+ * The sums are the tensor cores' fp32, which cut off instead of rounding: an
+ * error below K 2^-23 of the magnitudes summed (measured relative to y: 2e-6 at
+ * K = 1024, 9e-6 at K = 4096), far below a rounding to bf16, FP8 or MXFP8; fp32
+ * outputs, amax and blocks whose maximum is next to a power of two show it.
  * Results do not depend on earlier calls and are the same from run to run.
  * Outputs of non-finite inputs are unspecified, and a row of x reaches no
  * other row's output (amax aside).  No workspace.

@@ -128,6 +128,36 @@ def test_few_token_plans_of_every_kind(N, K, H, mode, split, slabs, rounds):
         check_mx(out.data[:, cols].cpu().numpy(), out.row_scales[:, cols[::32] // 32].cpu().numpy(), ref["y"], err, "y")
 
 
+@pytest.mark.parametrize("act", ["swiglu", "clamped_swiglu"])
+@pytest.mark.parametrize("N", [8, 300])
+def test_gates_far_from_zero(N, act):
+    """Gates from -130 to 130, each projection one exact product, so that only the activation's own error is left:
+    2 + 1.17 |z| units of 2**-23 for the exponential (CUDA's documented bound for __expf), 2 for the division and one
+    for each of the sum, the product alpha a (whose half unit the exponential multiplies by |z|: another |z| / 2), the
+    products with a, b and s, relative to y; and sigmoids below 2**-125, which may come out as 0."""
+    H, K = 264, 8
+    g = torch.Generator().manual_seed(6)
+    x = torch.zeros(N, K)
+    x[torch.arange(N), torch.arange(N) % K] = 2.0 ** (torch.arange(N) % 3 - 1)
+    w = torch.cat([torch.linspace(-130, 130, H * K)[torch.randperm(H * K, generator=g)].view(H, K),
+                   torch.randn(H, K, generator=g) * 3]).bfloat16()
+    s = torch.rand(N, generator=g)
+    out, pre = rn.gated_ffn_fwd(x.bfloat16().cuda(), w.cuda(), act, s.cuda(), limit=LIM, alpha=ALPHA,
+                                out_dtype=torch.float32, save_pre=True)
+    p = f64(x) @ f64(w).T
+    assert np.array_equal(f64(pre), p)                           # exact in bf16 already
+    a, b = p[:, :H], p[:, H:]
+    if act == "swiglu":
+        z, mag = a, np.abs(a * b)
+    else:
+        a, b = np.minimum(a, LIM), np.clip(b, -LIM, LIM) + 1
+        z, mag = ALPHA * a, np.abs(a) * (np.abs(b - 1) + 1)      # the sum b + 1 rounds too
+    mag = mag * f64(s)[:, None]
+    y = F._act.scaled_act_fwd(p, np_scales(s), act, limit=LIM, alpha=ALPHA)["y"]
+    tol = 2.0 ** -23 * (9 + 1.67 * np.abs(z)) * mag * F._act.sigmoid(z) + 2.0 ** -125 * mag
+    assert np.all(np.abs(f64(out) - y) <= tol + 1e-37)
+
+
 @pytest.mark.parametrize("i,size", list(enumerate(SIZES)), ids=lambda v: str(v))
 def test_backward(i, size):
     N, K, H = size
