@@ -49,7 +49,12 @@ constexpr int kStages = 6;
 constexpr int kOperandBytes = 16384;              // 128 x 64 bf16
 constexpr int kStageBytes = 2 * kOperandBytes;    // A and B of one CTA
 constexpr int kEpiWarps = 8;                      // two for each 32 lanes of tensor memory
-constexpr int kThreads = 64 + 32 * kEpiWarps;     // and one warp each for copies and products
+// and one warp each for copies and products: up to 3 warps a scheduler, so at
+// most 168 registers a thread.  The forward's epilogues of bf16, FP8 and MXFP8
+// spill 16 to 44 bytes: with all 64 outputs of a thread read at once, which hands
+// the accumulator back before the stores (8192 x 1024 x 4096 MXFP8 76 us, 80-84
+// with 32 at a time and no spills).
+constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr size_t kSmemBytes = (size_t)kStages * kStageBytes + 1024;
 
 // one product of the launch: tiles of 256 x 256 (forward: 256 x 128 outputs)

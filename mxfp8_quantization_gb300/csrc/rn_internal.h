@@ -124,12 +124,14 @@ struct ActParams {
 constexpr int kActNone = -1;  // rn_nvfp4_matvec: no activation
 
 // The bf16 block of few tokens: up to 8 the few-token kernel, up to 32 while
-// the outputs are few (us, few-token kernel against tensor-core tiles, K = H
-// unless given: 8 tokens 2048 8.1 / 10.6, 8 x 4096 x 8192 28 / 26; 16 tokens
-// 1024 x 512 4.8 / 9.4, 2048 9.0 / 10.7, 4096 x 8192 39 / 26; 32 tokens 2048
-// 12.7 / 10.6, 4096 26.5 / 15.8).
+// the outputs are few (us in a graph, weights in rotation, few-token kernel
+// against tensor-core tiles.  K x H 2048 x 2048: 1 token 8.1 / 13.1, 8 8.6 / 11.6,
+// 16 9.6 / 11.6, 32 13.6 / 11.6; 4096 x 8192: 1 25.7 / 37.4, 8 29.5 / 36.2, 16 32.6 /
+// 26.7, 32 53.0 / 27.0; 8192 x 8192: 2 46.6 / 65.2, 8 51.0 / 50.5, 16 59.5 / 50.6;
+// 8192 x 4096, tiles shared: 4 28.3 / 43.2, 8 30.1 / 28.8; 5120 x 13824: 8 60.0 / 64.0)
 inline bool few_tokens(int64_t N, int64_t H) { return N <= 8 || (N <= 32 && N * H <= 32768); }
-// few-token kernel: 8 rows apart stays within 32 bits; groups of 32 tokens in gridDim.y
+// few-token kernel: positions along the reduction, up to a chunk past a row's end,
+// are int; groups of 32 tokens are gridDim.y
 constexpr int64_t kMvMaxK = int64_t(1) << 26, kMvMaxN = int64_t(1) << 20;
 
 enum FfnOut : int { kFfnBf16 = 0, kFfnF32 = 1, kFfnFp8 = 2, kFfnMx = 3 };

@@ -230,10 +230,11 @@ struct Mv {
     } else if (T == 2 && left >= 128) {
       // The piece, and four blocks behind it, are in the row: its codes from
       // fixed offsets, its scales as the two words around them, put together
-      // when they are used (13 x 5136 x 8200 20.5 us; put together here, where
-      // the warp has to wait for them, 22.8).  Not with other numbers of tokens,
-      // whose registers are all in use: 1 x 8192 x 65536 64.5 us instead of
-      // 61.1, 5 x 2080 x 5000 gated 13.7 instead of 12.4.
+      // when they are used (against put together here, where the warp has to
+      // wait for them: 9 x 5136 x 8200 19.2 / 20.9 us, 13 tokens 20.7 / 22.4, 16
+      // 23.6 / 25.2, 16 x 8208 x 65536 177 / 199, 9 x 1040 x 8200 7.7 / 7.9).  Not with
+      // other numbers of tokens, whose registers are all in use: 1 x 8192 x 65536
+      // 64.5 us instead of 61.1, 5 x 2080 x 5000 gated 13.7 instead of 12.4.
       it.off = 0;
 #pragma unroll
       for (int m = 0; m < 2; ++m)
@@ -750,7 +751,7 @@ rn_status launch_plan(const MvParams& p, const MvLaunch& l, cudaStream_t s) {
                    : -1;
       }) < 1)
     return RN_ERR_CUDA;
-  if (l.ny > 65535) return RN_ERR_UNSUPPORTED;
+  static_assert(kMvMaxN / 32 <= 65535, "groups of tokens are gridDim.y");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(l.groups * pl.split), (unsigned)l.ny);
   cfg.blockDim = dim3(32 * W);
