@@ -659,7 +659,9 @@ FfnBwdPlan ffn_bwd_plan(int64_t N, int64_t K, int64_t H) {
   const int64_t dx_tiles = (N + 255) / 256 * kc, dx_slices = (R + 63) / 64;
   const int64_t dw_tiles = (R + 255) / 256 * kc, dw_slices = (N + 63) / 64;
   if (N > 0) {
-    const int64_t share = (dx_tiles * dx_slices + dw_tiles * dw_slices) / kPairs + 1;
+    // (in double: the sizes' product can pass 64 bits; exact where it matters)
+    const double work = (double)dx_tiles * (double)dx_slices + (double)dw_tiles * (double)dw_slices;
+    const int64_t share = work < 9e15 ? (int64_t)work / kPairs + 1 : INT64_MAX / 2;
     p.dx = split_for(dx_tiles, dx_slices, share);
     p.dw = split_for(dw_tiles, dw_slices, share);
   }

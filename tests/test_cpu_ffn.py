@@ -1,6 +1,9 @@
 """Host-side argument checks of the gated feed-forward block and the NVFP4
 products: each answers before any device work (no GPU is touched)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -8,6 +11,7 @@ import torch
 import mxfp8_quantization_gb300 as rn
 from mxfp8_quantization_gb300 import _build
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
 f32 = ctypes.c_float
 
@@ -102,6 +106,16 @@ def test_backward_workspace_query(lib):
     assert _bwd(lib, **none, K=60)[0] == UNSUPPORTED
     assert _bwd(lib, n=need - 1)[0] == WORKSPACE
     assert rn.gated_ffn_bwd_workspace_bytes(65536, 64, 65536) >= 2 ** 34  # past 32 bits
+
+
+@pytest.mark.parametrize("N,K,H", [(733841920, 573239040, 229906560), (880610304, 573239040, 229906560),
+                                   (2 ** 31 - 1, 2 ** 31 - 8, 2 ** 30 - 8)])
+def test_backward_workspace_query_of_any_size(lib, N, K, H):
+    # the product of the sizes passes 64 bits, for the first two to just below zero; asked in a process of its own
+    code = f"import mxfp8_quantization_gb300 as rn; print(rn.gated_ffn_bwd_workspace_bytes({N}, {K}, {H}))"
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert r.returncode == 0, r.returncode
+    assert int(r.stdout) == (4 * N * H + 255) // 256 * 256      # the bf16 gradient; so many tiles are not split
 
 
 GATED = dict(act=1, x=0x1000, dtype=0, codes=0x2000, blocks=0x3000, si=0x4000, scales=None, N=4, K=64,
