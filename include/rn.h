@@ -342,8 +342,9 @@ rn_status rn_scaled_act_bwd(rn_act act, const void* dy, const void* x, rn_dtype 
  *   pre     bf16 [N, 2H] or NULL: [a | b], each rounded once, for
  *           rn_gated_ffn_bwd.
  * dtype must be RN_BF16 (RN_F32 returns RN_ERR_UNSUPPORTED: the tensor cores
- * have no product that keeps fp32).  K % 8 == 0, H % 8 == 0, any N; x, w,
- * pre and out->data 16-byte aligned.  Outputs must not overlap inputs.
+ * have no product that keeps fp32).  K % 8 == 0 up to 2^26 (beyond:
+ * RN_ERR_UNSUPPORTED), H % 8 == 0, any N; x, w, pre and out->data 16-byte
+ * aligned.  Outputs must not overlap inputs.
  * The sums are the tensor cores' fp32, which cut off instead of rounding: an
  * error below K 2^-23 of the magnitudes summed (measured relative to y: 2e-6 at
  * K = 1024, 9e-6 at K = 4096), far below a rounding to bf16, FP8 or MXFP8; fp32
@@ -371,7 +372,8 @@ rn_status rn_gated_ffn_fwd(rn_act act, const void* x, const void* w, rn_dtype dt
  * *workspace_bytes (it depends on N, K and H only); otherwise a missing or
  * smaller workspace returns RN_ERR_WORKSPACE.  The workspace is 16-byte
  * aligned, need not be initialized and must not be shared by calls that may
- * run concurrently.  dtype, sizes and alignment as for the forward.
+ * run concurrently.  dtype, sizes (but any K % 8 == 0) and alignment as for the
+ * forward.
  */
 rn_status rn_gated_ffn_bwd(rn_act act, const void* dy, const void* x, const void* w, const void* pre,
                            rn_dtype dtype, const float* scales, int64_t N, int64_t K, int64_t H,

@@ -972,7 +972,7 @@ rn_status rn_gated_ffn_fwd(rn_act act, const void* x, const void* w, rn_dtype dt
   if (N > 0 && (x == nullptr || w == nullptr)) return RN_ERR_INVALID;
   int kind = 0;
   if ((st = ffn_out(mode, out, N, H, &kind)) != RN_OK) return st;
-  if (K % 8 != 0 || H % 8 != 0 || !aligned(x, 16) || !aligned(w, 16) || !aligned(pre, 16))
+  if (K % 8 != 0 || K > kFfnMaxK || H % 8 != 0 || !aligned(x, 16) || !aligned(w, 16) || !aligned(pre, 16))
     return RN_ERR_UNSUPPORTED;
   DeviceInfo di;
   if ((st = device_info(&di)) != RN_OK) return st;
@@ -980,7 +980,7 @@ rn_status rn_gated_ffn_fwd(rn_act act, const void* x, const void* w, rn_dtype dt
   if (kind == kFfnFp8 && (st = launch_fwd_init(out->amax, out->scale, out->scale_inv, s)) != RN_OK)
     return st;
   if (N == 0) return RN_OK;
-  if (few_tokens(N, H) && K <= kMvMaxK) {
+  if (few_tokens(N, H)) {
     MvParams m{};
     m.x = x;
     m.w = w;

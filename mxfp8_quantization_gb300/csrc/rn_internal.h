@@ -134,6 +134,12 @@ inline bool few_tokens(int64_t N, int64_t H) { return N <= 8 || (N <= 32 && N * 
 // are int; groups of 32 tokens are gridDim.y
 constexpr int64_t kMvMaxK = int64_t(1) << 26, kMvMaxN = int64_t(1) << 20;
 
+// The forward's reduction: a tile's epilogue waits for all of it, and waits run
+// out after about 2 s.  2^26 is 2^20 slices of 64 at 0.25 us each; 2^31, shared
+// by four pairs, would be 2.1 s.
+constexpr int64_t kFfnMaxK = int64_t(1) << 26;
+static_assert(kFfnMaxK <= kMvMaxK, "the few-token kernel takes every K of the block");
+
 enum FfnOut : int { kFfnBf16 = 0, kFfnF32 = 1, kFfnFp8 = 2, kFfnMx = 3 };
 
 struct FfnParams {

@@ -68,7 +68,8 @@ SHARED = [
 
 @pytest.mark.parametrize("kw,want", SHARED + [
     (dict(w=None), INVALID), (dict(w=0x2004), UNSUPPORTED), (dict(pre=0x7008), UNSUPPORTED),
-    (dict(K=68), UNSUPPORTED), (dict(H=36), UNSUPPORTED)], ids=str)
+    (dict(K=68), UNSUPPORTED), (dict(H=36), UNSUPPORTED), (dict(K=2 ** 26 + 8), UNSUPPORTED),
+    (dict(N=64, K=2 ** 31 - 8, H=4096), UNSUPPORTED)], ids=str)
 def test_forward_refusals(lib, kw, want):
     assert _fwd(lib, **kw) == want
 
