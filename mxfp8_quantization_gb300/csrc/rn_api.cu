@@ -40,6 +40,9 @@ int pick_ng(int nchunks, int cap, int max_ng) {
 }  // namespace
 
 rn_status device_info(DeviceInfo* out) {
+  // the runtime keeps the error of an earlier call that failed (a launch into
+  // an invalidated capture) until it is asked for: it would fail this one
+  cudaGetLastError();
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return RN_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return RN_ERR_UNSUPPORTED;
@@ -813,6 +816,7 @@ rn_status rn_delayed_scaling_update(float* amax_history, int64_t history_len, co
   if (history_len > kMaxHistory) return RN_ERR_UNSUPPORTED;
   if (!aligned(amax_history, 4) || !aligned(amax, 4) || !aligned(scale, 4) || !aligned(scale_inv, 4))
     return RN_ERR_UNSUPPORTED;
+  cudaGetLastError();  // as in device_info
   return launch_amax_history(amax_history, (int)history_len, amax, scale, scale_inv,
                              static_cast<cudaStream_t>(stream));
 }
