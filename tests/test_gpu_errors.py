@@ -1,9 +1,11 @@
-"""A call that fails on the host fails alone: the next good one succeeds.
-
-The failure is a launch into a stream whose capture was invalidated (by a
+"""What the state of the host does to a call.  A call that fails on the host
+fails alone: the next good one succeeds.  The failure is a launch into a stream whose capture was invalidated (by a
 synchronize inside it), which the runtime refuses before anything reaches the
 GPU."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -12,6 +14,7 @@ import mxfp8_quantization_gb300 as rn
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 THREAD_LOCAL, CUDA_ERROR = 1, 4
 
 
@@ -72,3 +75,37 @@ def test_a_failed_launch_does_not_fail_the_next_call(driver):
         assert f(h) == 0, name
         torch.cuda.synchronize()
     assert rn.device_error() == 0
+
+
+FIRST = """
+import torch, mxfp8_quantization_gb300 as rn
+g = torch.Generator(device="cuda").manual_seed(1)
+r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+x, w, dy, t = r(300, 264), r(2 * 136, 264) / 16, r(300, 136), r(3, 4112)
+w4 = rn.NVFP4Output(torch.randint(0, 256, (64, 2056), generator=g, dtype=torch.uint8, device="cuda"),
+                    torch.randint(0x30, 0x41, (64, 257), generator=g, dtype=torch.uint8, device="cuda"),
+                    None, torch.ones(1, device="cuda"), None)
+def step():
+    y, pre = rn.gated_ffn_fwd(x, w, save_pre=True)
+    few, _ = rn.gated_ffn_fwd(x[:3], w, quant="fp8_delayed", scale=torch_one)
+    return (y, pre, few.data, few.amax, *rn.gated_ffn_bwd(dy, x, w, pre), rn.nvfp4_matvec(t, w4),
+            rn.nvfp4_gated_ffn(t, w4))
+torch_one = torch.ones(1, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = step()
+graph.replay()
+want = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, want))
+assert rn.device_error() == 0
+print("same")
+"""
+
+
+def test_first_use_inside_a_capture():
+    """Nothing that a kernel's first launch sets up (its shared memory, the tensor maps' encoder, the clusters that fit)
+    breaks a capture: a process whose first calls are captured."""
+    r = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, cwd=ROOT, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
