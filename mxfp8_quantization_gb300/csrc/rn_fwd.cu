@@ -419,6 +419,17 @@ __global__ void __launch_bounds__(max_threads<NC>(), 1) rn_fwd_kernel(const FwdP
       kg = kgp = i >> lg;
       jr = i & (rps - 1);
       r = (seq.group(kg) << lg) + jr;
+      // the short last group of all: its missing rows are skipped by every
+      // warp of the group.  Walked forwards that slot is never used again;
+      // backwards it is the CTA's first (kg 0), and the producer waits for
+      // all its rows before the slot's next use
+      if (r >= p.N) {
+        if (PASS2 && p.reverse) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&empty[pos.slot]));
+        }
+        continue;
+      }
     }
     const uint32_t s = pos.slot;
     // before waiting for this use of the slot, wait for the previous use to
@@ -426,16 +437,6 @@ __global__ void __launch_bounds__(max_threads<NC>(), 1) rn_fwd_kernel(const FwdP
     // match a phase one lap old (alias-free since NGR <= (Q - 1) rps: a group
     // reaching this slot has already seen every earlier use of it issued)
     if (kg >= (int)Q) mbar_wait(smem_u32(&empty[s]), pos.phase ^ 1u, &g_err_fwd, kErrStatsWait);
-    if constexpr (!ONE) {
-      // the short last group of all: the rows it lacks are given back as soon
-      // as the slot is its own (walked from the last row, that group comes
-      // first and its slot is used again)
-      if (r >= p.N) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&empty[s]));
-        continue;
-      }
-    }
     mbar_wait(smem_u32(&full[s]), pos.phase, &g_err_fwd, kErrFullWait);
     const unsigned char* rowp = ring + (size_t)s * slot_bytes + (size_t)jr * row_bytes;
     Raw raw[NC];

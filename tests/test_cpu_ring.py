@@ -12,13 +12,26 @@ CSRC = os.path.join(os.path.dirname(os.path.abspath(rn.__file__)), "csrc")
 
 
 def missing_rows_arrive():
-    """Whether the kernel's branch for a row past the end gives the slot back, in its turn: after the wait for the
-    slot's previous use."""
+    """For rows past the end: whether the kernel's branch gives their part of the slot back when the rows are walked
+    backwards (in the passes that do so); it may not where the slot could still be in its previous use."""
     text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "rn_fwd.cu")).read())
     k = text[text.index("rn_fwd_kernel(const FwdParams p)"):]
-    at = re.search(r"if \(r >= p\.N\)\s*(\{[^}]*\}|continue;)", k)
-    turn = k.index("mbar_wait(smem_u32(&empty[s]), pos.phase ^ 1u, &g_err_fwd, kErrStatsWait)")
-    return "mbar_arrive(smem_u32(&empty[s]))" in at.group(1) and turn < at.start()
+    start = at = k.index("{", k.index("if (r >= p.N)")) if "if (r >= p.N) {" in k else None
+    if start is None:
+        return False
+    depth = 1
+    while depth:
+        at += 1
+        depth += (k[at] == "{") - (k[at] == "}")
+    branch = k[start:at]
+    return re.search(r"if \(PASS2 && p\.reverse\) \{\s*__syncwarp\(\);\s*if \(lane == 0\) "
+                     r"mbar_arrive\(smem_u32\(&empty\[pos\.slot\]\)\);\s*\}\s*continue;", branch) is not None
+
+
+def test_only_the_second_passes_walk_backwards():
+    api = open(os.path.join(CSRC, "rn_api.cu")).read()
+    launches = re.findall(r"q\.reverse = 1;(.{0,900}?)launch_fwd(?:_res)?\([^;]*?(kQ\w+)", api, flags=re.S)
+    assert [q for _, q in launches] and {q for _, q in launches} <= {"kQNvfp4", "kQCurQuant"}
 
 
 def replay(N, rps, Q, grid, reverse):
@@ -33,7 +46,9 @@ def replay(N, rps, Q, grid, reverse):
         for kg in range(count):
             start = (first + kg * (-grid if reverse else grid)) * rps
             for j in range(rps):
-                given[kg] += start + j < N or arrive
+                given[kg] += start + j < N or (arrive and reverse)
+            if start + rps > N:
+                assert kg == (0 if reverse else count - 1)       # no previous use, or none to come
         for i in range(Q, count):    # the producer waits for use i - Q of the slot
             if given[i - Q] < rps:
                 stuck.append((b, i))
