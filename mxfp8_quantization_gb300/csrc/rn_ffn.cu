@@ -17,11 +17,13 @@
 // tile while the next is being summed.
 //
 // What bounds it is the tensor pipe: 93 % (forward) and 97 % (backward) of the
-// active cycles; 8192 x 4096 x 8192 (N x K x H) forward 541 us, 2032 TFLOP/s in a
-// burst (1690 in a long loop, at the power cap), backward's products 1130 us,
-// 1945 TFLOP/s.  Eight epilogue warps with 32-byte stores: a forward that keeps
-// the projections, 8192 x 1024 x 4096, 120 us with four and 16-byte stores, 90 us
-// so.  Small problems split a tile's reduction: the backward over the
+// active cycles.  8192 x 4096 x 8192 (N x K x H) in a burst, on two boxes: forward
+// 539 and 552 us (2039 and 1992 TFLOP/s; the library's plain product of that
+// size 530 and 540 us), the backward's products 1113 and 1157 us (1976 and 1900);
+// in a long loop, at the power cap, the forward that keeps the projections
+// takes 645 to 666 us (1705 to 1651 TFLOP/s).  Eight epilogue warps with 32-byte
+// stores: that forward at 8192 x 1024 x 4096 120 us with four and 16-byte stores,
+// 85-87 us so.  Small problems split a tile's reduction: the backward over the
 // workspace, the forward over the pairs of a cluster (below).
 //
 // Forward tiles hold 128 gate and 128 linear columns: the leader's B is 128

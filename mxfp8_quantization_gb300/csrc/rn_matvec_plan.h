@@ -45,7 +45,8 @@ struct MvShape {
 // two CTAs an SM of 8 warps while their tokens are small (each CTA stages its
 // own), else one of 16.  9 to 16: 12 warps, what 65536 registers hold without
 // spills (16 x 4096 x 8192 gated NVFP4 21.5 us, 24.2 with 8 warps, 24.4 with 8 of
-// two items in flight; 13 x 5136 x 8200 27.5, 29.0, 29.2).
+// two items in flight; 13 x 5136 x 8200 27.5, 29.0, 29.2 with the loads of that
+// time, 20.7 now).
 struct MvVariant {
   int T, W;
 };
