@@ -17,7 +17,7 @@
 // tile while the next is being summed.
 //
 // What bounds it is the tensor pipe: 93 % (forward) and 97 % (backward) of the
-// active cycles.  8192 x 4096 x 8192 (N x K x H) in a burst, on two boxes: forward
+// active cycles.  8192 x 4096 x 8192 (N x K x H) in a burst, on two GB300s: forward
 // 539 and 552 us (2039 and 1992 TFLOP/s; the library's plain product of that
 // size 530 and 540 us), the backward's products 1113 and 1157 us (1976 and 1900);
 // in a long loop, at the power cap, the forward that keeps the projections
