@@ -418,6 +418,113 @@ rn_status rn_quantize_only(const float* y, int64_t N, int64_t H,
                            rn_quant_mode mode, const rn_output* out,
                            void* stream);
 
+/*
+ * Paged 8-bit key/value cache (the pages have no counterpart: the formats are
+ * those of the library's other outputs).  A sequence's positions stand in
+ * blocks of RN_KV_PAGE = 64; block i of sequence b is page table[b, i] of
+ *   k         E4M3 codes [pages, heads, 64, dim]
+ *   v         E4M3 codes [pages, heads, dim, 64] (values transposed)
+ *   k_scales  E8M0 bytes [pages, heads]: an element stands for its code's
+ *   v_scales  value * 2^(byte - 127)
+ * All are the caller's and need not be initialized.  k and v 16-byte aligned; dim
+ * 64, 128, 192 or 256; up to 65535 heads.
+ */
+#define RN_KV_PAGE 64
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int64_t pages;
+  int64_t heads;
+  int64_t dim;
+} rn_kv_cache;
+
+/*
+ * The sequences of a call, all three arrays on the device: nothing about
+ * their lengths is known on the host, and a captured call follows them.
+ *   starts  int32 [sequences + 1], ascending: rows starts[b] .. starts[b+1] - 1
+ *           of the call's row tensors belong to sequence b
+ *   lens    int32 [sequences]: positions that sequence b has with these rows.
+ *           They are its last ones: with n rows, row starts[b] + i is position
+ *           lens[b] - n + i
+ *   table   int32 [sequences, table_width]
+ *   tokens  rows of the call's row tensors
+ * Rows outside every sequence (before starts[0], from starts[sequences] on)
+ * are neither read nor written.  A page number outside [0, pages) and a block
+ * past table_width mean that the block's positions are not cached: they are
+ * not written, read as 0, and no query sees them; the same holds for a row
+ * whose position is negative.  starts are cut to [0, tokens], so that no
+ * contents of the arrays lead out of the caller's memory; starts that descend
+ * give unspecified results.  Up to 2^24 sequences, 2^30 - 1 rows and 2^25 - 1
+ * blocks a sequence.
+ */
+typedef struct {
+  const int32_t* table;
+  const int32_t* starts;
+  const int32_t* lens;
+  int64_t sequences;
+  int64_t table_width;
+  int64_t tokens;
+} rn_kv_seqs;
+
+/*
+ * Quantizes the rows' keys and values into their pages.
+ *   k, v  [tokens, heads, dim] in `dtype`; rows are k_stride / v_stride elements
+ *         apart (>= heads * dim, whole 16 bytes), 16-byte aligned
+ * Per page and head: e is the smallest exponent with amax <= 448 * 2^e, amax
+ * the largest finite magnitude of the page's new elements, clamped to [-120,
+ * 120]; code = E4M3(x * 2^-e) (to nearest even, saturating, NaN -> 0x7F).  A
+ * page whose block begins before the rows keeps the larger of that e and its
+ * own, e'; where e is larger the codes in front of the rows become
+ * E4M3(value * 2^(e' - e)), which is exact unless they become subnormal.  A
+ * page whose first position is written begins anew, whatever it held; codes of
+ * positions behind the sequence's end stay as they are.  Two sequences of a
+ * call must not write the same page (its contents would be unspecified);
+ * shared pages that are only read are fine.  Deterministic.
+ */
+rn_status rn_kv_cache_write(const void* k, const void* v, rn_dtype dtype, int64_t k_stride,
+                            int64_t v_stride, const rn_kv_cache* cache, const rn_kv_seqs* seqs,
+                            void* stream);
+
+/*
+ * The rows' positions as numbers: k, v [tokens, heads, dim] in out_dtype,
+ * 16-byte aligned; every value is exact in either type.  lens[b] rows of
+ * sequence b give all of it, fewer its last positions.
+ */
+rn_status rn_kv_cache_read(const rn_kv_cache* cache, const rn_kv_seqs* seqs, void* k, void* v,
+                           rn_dtype out_dtype, void* stream);
+
+/*
+ * Attention of the rows' queries with the cached positions of their sequences
+ * (with the rows' own, which are written first):
+ *   q    bf16 [tokens, q_heads, dim] (dtype RN_BF16; RN_F32 returns
+ *        RN_ERR_UNSUPPORTED), rows q_stride elements apart; q_heads a multiple of
+ *        the cache's heads: query heads g * G .. g * G + G - 1 read head g
+ *   s    = scale * q . k, then softcap * tanh(s / softcap) if softcap > 0, then
+ *        + slopes[q head] * (j - p) if slopes (fp32 [q_heads]) is not NULL, for the
+ *        query's position p and the cached position j
+ *   seen j < lens[b]; if causal, j <= p; if window > 0, j > p - window
+ *   out  bf16 [tokens, q_heads, dim] = softmax over the seen j of s, times v; a
+ *        query that sees nothing gets 0
+ *   lse  fp32 [tokens, q_heads] or NULL: log(sum of exp(s)), -infinity where
+ *        nothing is seen
+ * scale > 0.  Scores and sums are fp32; the weights are rounded once to 11
+ * significant bits, the output once to bf16.  The sums are the tensor cores'
+ * fp32, which cut off instead of rounding.  What a query does not see has no part in its
+ * output, whatever it holds; outputs of queries that see a NaN, or hold a
+ * non-finite value themselves, are unspecified.  Results are the same from run
+ * to run.  Workspace protocol as for rn_layernorm_bwd: with workspace and out
+ * NULL the call stores the required byte count in *workspace_bytes.  It depends
+ * on dim only; the workspace need not be initialized and must not be shared
+ * by calls that may run concurrently.
+ */
+rn_status rn_kv_attention(const void* q, rn_dtype dtype, int64_t q_stride, int64_t q_heads,
+                          const rn_kv_cache* cache, const rn_kv_seqs* seqs, float scale,
+                          int causal, int64_t window, float softcap, const float* slopes,
+                          void* out, float* lse, void* workspace, size_t* workspace_bytes,
+                          void* stream);
+
 /* Static message for a status code. */
 const char* rn_status_str(rn_status s);
 

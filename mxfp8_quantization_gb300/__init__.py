@@ -26,6 +26,8 @@ and other MOE optimizations"; ``gated_ffn_fwd`` / ``gated_ffn_bwd`` are the
 gated feed-forward block around them (both projections, the activation and
 the product), ``nvfp4_matvec`` / ``nvfp4_gated_ffn`` the products of one or a
 few tokens with the NVFP4 weights that ``quantize_only`` makes.
+``kv_cache_write`` / ``kv_cache_read`` keep keys and values in a paged 8-bit
+cache, and ``kv_attention`` is the attention that reads it.
 """
 from __future__ import annotations
 
@@ -44,6 +46,8 @@ __all__ = [
     "QUANT_MODES", "ACTS", "scaled_act_fwd", "scaled_act_bwd",
     "gated_ffn_fwd", "gated_ffn_bwd", "gated_ffn_bwd_workspace_bytes", "nvfp4_matvec",
     "nvfp4_gated_ffn",
+    "KV_PAGE", "KVCache", "KVSequences", "kv_cache_alloc", "kv_cache_write", "kv_cache_read", "kv_attention",
+    "kv_attention_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -69,6 +73,16 @@ class _Output(ctypes.Structure):
         ("amax", ctypes.c_void_p),
         ("out_dtype", ctypes.c_int),
     ]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scales", "v_scales")] + \
+               [(n, ctypes.c_int64) for n in ("pages", "heads", "dim")]
+
+
+class _KVSeqs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("table", "starts", "lens")] + \
+               [(n, ctypes.c_int64) for n in ("sequences", "table_width", "tokens")]
 
 
 _lib = None
@@ -108,6 +122,10 @@ def _load():
     lib.rn_nvfp4_matvec.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, i32, vp, vp]
     lib.rn_nvfp4_gated_ffn.argtypes = [i32, vp, i32, vp, vp, vp, vp, i64, i64, i64, f32, f32, i32,
                                        outp, vp]
+    cachep, seqsp = ctypes.POINTER(_KVCache), ctypes.POINTER(_KVSeqs)
+    lib.rn_kv_cache_write.argtypes = [vp, vp, i32, i64, i64, cachep, seqsp, vp]
+    lib.rn_kv_cache_read.argtypes = [cachep, seqsp, vp, vp, i32, vp]
+    lib.rn_kv_attention.argtypes = [vp, i32, i64, i64, cachep, seqsp, f32, i32, i64, f32, vp, vp, vp, vp, szp, vp]
     lib.rn_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint)]
     lib.rn_status_str.argtypes = [i32]
     lib.rn_status_str.restype = ctypes.c_char_p
@@ -115,7 +133,8 @@ def _load():
               "rn_quantize_only", "rn_device_error", "rn_abi_version", "rn_layernorm_bwd_noalloc",
               "rn_layernorm_add_fwd", "rn_rmsnorm_add_fwd", "rn_delayed_scaling_update",
               "rn_scaled_act_fwd", "rn_scaled_act_bwd", "rn_gated_ffn_fwd", "rn_gated_ffn_bwd",
-              "rn_nvfp4_matvec", "rn_nvfp4_gated_ffn"):
+              "rn_nvfp4_matvec", "rn_nvfp4_gated_ffn", "rn_kv_cache_write", "rn_kv_cache_read",
+              "rn_kv_attention"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -601,6 +620,191 @@ def nvfp4_gated_ffn(x, w, act="swiglu", scales=None, quant="none", limit=7.0, al
     if st:
         _check(st, "rn_nvfp4_gated_ffn")
     return res
+
+
+KV_PAGE = 64   # positions of a page of the key/value cache
+_I32 = torch.int32
+
+
+@dataclass
+class KVCache:
+    """A paged 8-bit key/value cache (``kv_cache_alloc``): an element stands for its code's value times
+    2 ** (scale - 127) of its page and head."""
+    k: torch.Tensor         # uint8 E4M3 [pages, heads, 64, dim]
+    v: torch.Tensor         # uint8 E4M3 [pages, heads, dim, 64] (transposed)
+    k_scales: torch.Tensor  # uint8 E8M0 [pages, heads]
+    v_scales: torch.Tensor
+
+
+@dataclass
+class KVSequences:
+    """The sequences of a call, on the device: rows starts[b] .. starts[b + 1] - 1 of the call's row
+    tensors are the last of the lens[b] positions of sequence b, whose block of 64 positions i stands in
+    page table[b, i] (none where that number is not a page)."""
+    table: torch.Tensor   # int32 [sequences, width]
+    starts: torch.Tensor  # int32 [sequences + 1]
+    lens: torch.Tensor    # int32 [sequences]
+
+
+def kv_cache_alloc(pages, heads, dim, device=None) -> KVCache:
+    """A zeroed cache of ``pages`` pages of 64 positions."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    zeros = functools.partial(torch.zeros, dtype=torch.uint8, device=dev)
+    return KVCache(zeros((pages, heads, KV_PAGE, dim)), zeros((pages, heads, dim, KV_PAGE)), zeros((pages, heads)),
+                   zeros((pages, heads)))
+
+
+def _kv_ok(cache, seqs, dev):
+    try:
+        k, v, ks, vs = cache.k, cache.v, cache.k_scales, cache.v_scales
+        tb, st, ln = seqs.table, seqs.starts, seqs.lens
+        P, H, n, D = k.shape
+        B, _ = tb.shape
+        return (n == KV_PAGE and v.shape == (P, H, D, KV_PAGE) and ks.shape == (P, H) and vs.shape == (P, H)
+                and st.shape == (B + 1,) and ln.shape == (B,) and k.dtype is _U8 and v.dtype is _U8
+                and ks.dtype is _U8 and vs.dtype is _U8 and tb.dtype is _I32 and st.dtype is _I32
+                and ln.dtype is _I32 and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous()
+                and vs.is_contiguous() and tb.is_contiguous() and st.is_contiguous() and ln.is_contiguous()
+                and k.is_cuda and k.device.index == dev and v.device.index == dev and ks.device.index == dev
+                and vs.device.index == dev and tb.device.index == dev and st.device.index == dev
+                and ln.device.index == dev)
+    except (AttributeError, ValueError):
+        return False
+
+
+def _refuse_kv(cache, seqs):
+    if not hasattr(cache, "k_scales"):
+        raise RNError(f"cache must be a KVCache, got {type(cache).__name__}")
+    if not hasattr(seqs, "starts"):
+        raise RNError(f"seqs must be KVSequences, got {type(seqs).__name__}")
+    _need(cache.k, "cache.k", _U8)
+    if cache.k.dim() != 4 or cache.k.shape[2] != KV_PAGE:
+        raise RNError(f"cache.k must have shape (pages, heads, {KV_PAGE}, dim), got {tuple(cache.k.shape)}")
+    P, H, _, D = cache.k.shape
+    _need(cache.v, "cache.v", _U8, (P, H, D, KV_PAGE))
+    _need(cache.k_scales, "cache.k_scales", _U8, (P, H))
+    _need(cache.v_scales, "cache.v_scales", _U8, (P, H))
+    B = _matrix(seqs.table, "seqs.table", _I32)[0]
+    _need(seqs.starts, "seqs.starts", _I32, (B + 1,))
+    _need(seqs.lens, "seqs.lens", _I32, (B,))
+    raise RNError("unsupported tensors")
+
+
+def _kv_args(cache, seqs, tokens, dev):
+    if not _kv_ok(cache, seqs, dev):
+        _refuse_kv(cache, seqs)
+    k = cache.k
+    P, H, _, D = k.shape
+    B, width = seqs.table.shape
+    return (_KVCache(k.data_ptr(), cache.v.data_ptr(), cache.k_scales.data_ptr(), cache.v_scales.data_ptr(), P, H, D),
+            _KVSeqs(seqs.table.data_ptr(), seqs.starts.data_ptr(), seqs.lens.data_ptr(), B, width, tokens))
+
+
+def _kv_rows(t, name, heads, dim, dev, dtypes):
+    """The distance of the rows of t [tokens, heads, dim], whose heads and dims are contiguous."""
+    try:
+        ok = (t.dtype in dtypes and t.is_cuda and t.device.index == dev and t.shape[1:] == (heads, dim)
+              and t.dim() == 3 and (t.stride(2) == 1 or t.numel() == 0) and (heads == 1 or t.stride(1) == dim
+                                                                            or t.numel() == 0))
+    except AttributeError:
+        ok = False
+    if not ok:
+        if t is None:
+            raise RNError(f"{name} is required")
+        if not getattr(t, "is_cuda", False):
+            raise RNError(f"{name} must be a CUDA tensor")
+        if t.device.index != dev:
+            raise RNError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+        if t.dtype not in dtypes:
+            raise RNError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+        if t.dim() != 3 or t.shape[1:] != (heads, dim):
+            raise RNError(f"{name} must have shape (tokens, {heads}, {dim}), got {tuple(t.shape)}")
+        raise RNError(f"the heads and dims of {name} must be contiguous (its rows may lie apart)")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def kv_cache_write(cache, seqs, k, v):
+    """Quantizes the new rows k, v [tokens, heads, dim] (bf16 or fp32; their rows may lie apart, as in a
+    slice of a joint projection) into the pages of their sequences, in place."""
+    lib = _lib or _load()
+    dev = torch.cuda.current_device()
+    if k is None:
+        raise RNError("k is required")
+    c, q = _kv_args(cache, seqs, k.shape[0], dev)
+    ks = _kv_rows(k, "k", c.heads, c.dim, dev, (_BF, _FP32))
+    vs = _kv_rows(v, "v", c.heads, c.dim, dev, (k.dtype,))
+    if v.shape[0] != k.shape[0]:
+        raise RNError(f"v must have shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    st = lib.rn_kv_cache_write(k.data_ptr(), v.data_ptr(), _BF16 if k.dtype is _BF else _F32, ks, vs, c, q,
+                               _raw_stream(dev))
+    if st:
+        _check(st, "rn_kv_cache_write")
+
+
+def kv_cache_read(cache, seqs, tokens, out_dtype=torch.bfloat16):
+    """The last positions of each sequence (as many as it has rows) -> (k, v) [tokens, heads, dim] in
+    bfloat16 or float32, both exact.  Rows outside every sequence are left uninitialized."""
+    lib = _lib or _load()
+    dev = torch.cuda.current_device()
+    c, q = _kv_args(cache, seqs, int(tokens), dev)
+    shape = (q.tokens, c.heads, c.dim)
+    k = torch.empty(shape, dtype=out_dtype, device=cache.k.device)
+    v = torch.empty(shape, dtype=out_dtype, device=cache.k.device)
+    st = lib.rn_kv_cache_read(c, q, k.data_ptr(), v.data_ptr(), _dtype_code(k), _raw_stream(dev))
+    if st:
+        _check(st, "rn_kv_cache_read")
+    return k, v
+
+
+@functools.lru_cache(maxsize=64)
+def _kv_attention_bytes(tokens, q_heads, sequences, heads, dim):
+    c = _KVCache(16, 16, 16, 16, 1, heads, dim)
+    q = _KVSeqs(16, 16, 16, sequences, 1, tokens)
+    n = ctypes.c_size_t(0)
+    st = _load().rn_kv_attention(None, _BF16, 0, q_heads, c, q, 1.0, 1, 0, 0.0, None, None, None, None,
+                                 ctypes.byref(n), None)
+    _check(st, "workspace query")
+    return int(n.value)
+
+
+def kv_attention_workspace_bytes(tokens, q_heads, sequences, heads, dim) -> int:
+    """Workspace bytes ``kv_attention`` needs (the query step of the protocol)."""
+    return _kv_attention_bytes(int(tokens), int(q_heads), int(sequences), int(heads), int(dim))
+
+
+def kv_attention(q, cache, seqs, scale=None, causal=True, window=0, softcap=0.0, slopes=None, return_lse=False,
+                 workspace=None):
+    """Attention of the queries q bf16 [tokens, q_heads, dim] (rows may lie apart) with the cached positions
+    of their sequences -> out bf16 [tokens, q_heads, dim], or (out, lse fp32 [tokens, q_heads]) with
+    ``return_lse``.  ``scale``: 1 / sqrt(dim) by default; ``causal``: positions up to the query's own;
+    ``window`` > 0: the last ``window`` of those; ``softcap`` > 0: softcap * tanh(score / softcap);
+    ``slopes`` fp32 [q_heads]: + slope * (position - the query's).  Rows outside every sequence are left
+    uninitialized."""
+    lib = _lib or _load()
+    dev = torch.cuda.current_device()
+    if q is None:
+        raise RNError("q is required")
+    c, s = _kv_args(cache, seqs, q.shape[0], dev)
+    if q.dim() != 3 or c.heads == 0 or q.shape[1] % c.heads or q.shape[1] == 0:
+        raise RNError(f"q must have shape (tokens, a multiple of {c.heads}, {c.dim}), got {tuple(q.shape)}")
+    T, heads, D = q.shape
+    qs = _kv_rows(q, "q", heads, c.dim, dev, (_BF,))
+    if slopes is not None:
+        _need(slopes, "slopes", _FP32, (heads,))
+    need = _kv_attention_bytes(T, heads, s.sequences, c.heads, c.dim)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=_U8, device=q.device)
+    else:
+        _need(workspace, "workspace")
+    n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
+    out = torch.empty((T, heads, D), dtype=_BF, device=q.device)
+    lse = torch.empty((T, heads), dtype=_FP32, device=q.device) if return_lse else None
+    st = lib.rn_kv_attention(q.data_ptr(), _BF16, qs, heads, c, s, D ** -0.5 if scale is None else float(scale),
+                             int(bool(causal)), int(window), float(softcap), _addr(slopes), out.data_ptr(),
+                             _addr(lse), workspace.data_ptr(), ctypes.byref(n), _raw_stream(dev))
+    if st:
+        _check(st, "rn_kv_attention")
+    return (out, lse) if return_lse else out
 
 
 def bwd_workspace_bytes(N, H, dtype, layernorm=True) -> int:

@@ -1156,7 +1156,9 @@ rn_status rn_device_error(unsigned int* code) {
   if ((st = read_clear_error_ffn(&d)) != RN_OK) return st;
   unsigned e = 0;
   if ((st = read_clear_error_mv(&e)) != RN_OK) return st;
-  *code = a ? a : (b ? b : (c ? c : (d ? d : e)));
+  unsigned f = 0;
+  if ((st = read_clear_error_kv(&f)) != RN_OK) return st;
+  *code = a ? a : (b ? b : (c ? c : (d ? d : (e ? e : f))));
   return RN_OK;
 }
 

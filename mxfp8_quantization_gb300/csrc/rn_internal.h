@@ -195,6 +195,55 @@ struct MvParams {
   int mode;               // FfnOut
 };
 
+// paged 8-bit key/value cache (include/rn.h: rn_kv_cache, rn_kv_seqs)
+struct KvCache {
+  uint8_t* k;             // E4M3 [pages, heads, 64, dim]
+  uint8_t* v;             // E4M3 [pages, heads, dim, 64]
+  uint8_t* ks;            // E8M0 [pages, heads]
+  uint8_t* vs;
+  int64_t pages;
+  int heads;
+};
+struct KvSeqs {
+  const int* table;       // [B, width]
+  const int* starts;      // [B + 1]
+  const int* lens;        // [B]
+  int B, width, tokens;   // tokens: rows of the call's row tensors
+};
+struct KvWriteParams {
+  KvCache c;
+  KvSeqs q;
+  const void* k;          // [tokens, heads, dim], rows `k_stride` elements apart
+  const void* v;
+  int64_t k_stride, v_stride;
+};
+struct KvReadParams {
+  KvCache c;
+  KvSeqs q;
+  void* k;                // [tokens, heads, dim]
+  void* v;
+};
+struct KvAttnParams {
+  KvCache c;
+  KvSeqs q;
+  const void* x;          // queries, bf16 [tokens, heads * group, dim], rows `stride` elements apart
+  int64_t stride;
+  int group;              // query heads of a key/value head
+  float scale;
+  int causal;
+  int window;             // 0: none
+  float softcap;          // 0: none
+  const float* slopes;    // [heads * group] or NULL
+  void* out;              // bf16 [tokens, heads * group, dim]
+  float* lse;             // [tokens, heads * group] or NULL
+  void* ws;
+};
+rn_status launch_kv_write(const KvWriteParams& p, int dim, bool bf16, cudaStream_t s);
+rn_status launch_kv_read(const KvReadParams& p, int dim, bool bf16, cudaStream_t s);
+rn_status launch_kv_attn(const KvAttnParams& p, int dim, int sms, cudaStream_t s);
+// bytes of the attention's workspace
+size_t kv_attn_bytes(int64_t tokens, int64_t B, int group, int dim);
+
 // launch shape shared by the persistent kernels
 struct Launch {
   int work;             // independent work items (tiles / chunks): grid upper bound
@@ -308,5 +357,6 @@ rn_status read_clear_error_mx(unsigned* code);
 rn_status read_clear_error_bwd(unsigned* code);
 rn_status read_clear_error_ffn(unsigned* code);
 rn_status read_clear_error_mv(unsigned* code);
+rn_status read_clear_error_kv(unsigned* code);
 
 }  // namespace rn
