@@ -15,7 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "librn.so")
 SOURCES = ["rn_api.cu", "rn_fwd.cu", "rn_fwd_res.cu", "rn_mx.cu", "rn_bwd.cu", "rn_scaling.cu", "rn_act.cu",
-           "rn_ffn.cu", "rn_matvec.cu", "rn_kv.cu", "rn_kv_attn.cu", "rn_kv_api.cu"]
+           "rn_ffn.cu", "rn_matvec.cu", "rn_kv.cu", "rn_kv_attn.cu", "rn_kv_tile.cu",
+           "rn_kv_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 

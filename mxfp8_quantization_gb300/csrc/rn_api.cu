@@ -1158,7 +1158,9 @@ rn_status rn_device_error(unsigned int* code) {
   if ((st = read_clear_error_mv(&e)) != RN_OK) return st;
   unsigned f = 0;
   if ((st = read_clear_error_kv(&f)) != RN_OK) return st;
-  *code = a ? a : (b ? b : (c ? c : (d ? d : (e ? e : f))));
+  unsigned g = 0;
+  if ((st = read_clear_error_kv_tile(&g)) != RN_OK) return st;
+  *code = a ? a : (b ? b : (c ? c : (d ? d : (e ? e : (f ? f : g)))));
   return RN_OK;
 }
 

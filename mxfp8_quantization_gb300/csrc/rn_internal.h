@@ -242,7 +242,7 @@ rn_status launch_kv_write(const KvWriteParams& p, int dim, bool bf16, cudaStream
 rn_status launch_kv_read(const KvReadParams& p, int dim, bool bf16, cudaStream_t s);
 rn_status launch_kv_attn(const KvAttnParams& p, int dim, int sms, cudaStream_t s);
 // bytes of the attention's workspace
-size_t kv_attn_bytes(int64_t tokens, int64_t B, int group, int dim);
+size_t kv_attn_bytes(int dim);
 
 // launch shape shared by the persistent kernels
 struct Launch {
@@ -358,5 +358,6 @@ rn_status read_clear_error_bwd(unsigned* code);
 rn_status read_clear_error_ffn(unsigned* code);
 rn_status read_clear_error_mv(unsigned* code);
 rn_status read_clear_error_kv(unsigned* code);
+rn_status read_clear_error_kv_tile(unsigned* code);
 
 }  // namespace rn

@@ -100,7 +100,7 @@ rn_status rn_kv_attention(const void* q, rn_dtype dtype, int64_t q_stride, int64
     return RN_ERR_INVALID;
   const int64_t group = q_heads / p.c.heads;
   if (dtype != RN_BF16 || group > 4096 || p.q.tokens * group / 8 + p.q.B > INT32_MAX / 2) return RN_ERR_UNSUPPORTED;
-  const size_t need = kv_attn_bytes(p.q.tokens, p.q.B, (int)group, cache->dim);
+  const size_t need = kv_attn_bytes((int)cache->dim);
   if (workspace == nullptr && out == nullptr) {
     if (workspace_bytes == nullptr) return RN_ERR_INVALID;
     *workspace_bytes = need;

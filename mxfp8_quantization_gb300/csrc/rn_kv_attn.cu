@@ -37,84 +37,18 @@
 #include "rn_device.cuh"
 #include "rn_internal.h"
 #include "rn_kv.cuh"
+#include "rn_kv_plan.cuh"
 
 namespace rn {
 namespace {
 
 __device__ unsigned g_err_kv;
 
-constexpr int kMaxCtas = 160;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
 // warps of a CTA and slots of a warp: 192 KB of slots an SM
 template <int D>
 constexpr int kWarps = D <= 128 ? 8 : 4;
 template <int D>
 constexpr int kSlots = 196608 / (kWarps<D> * 64 * D);
-constexpr int kMaxWorkers = kMaxCtas * 8;
-// sequences whose rows and lengths are kept in shared memory
-constexpr int kSeqsInSmem = 1024;
-
-// the (row tile, head) that a worker begins last and does not finish
-struct Desc {
-  int parts;   // workers that share it, this one the first (0: none)
-  int item, rows, head;
-};
-
-// a row tile of a sequence
-struct Item {
-  int b;
-  int s0;          // first row of the sequence
-  int r0, rows;    // its rows of (query, query head of the group), query-major
-  int p0;          // position of query 0
-  int len;
-  int lo, hi;      // positions that any row sees
-  int blk0, nblk;  // pages; one without positions where the rows see none
-};
-
-struct Plan {
-  const int* starts;  // shared or global
-  const int* lens;
-  int B, tokens, group, causal, window;
-  int reach;          // positions that the page table has room for
-};
-
-template <int R>
-__device__ __forceinline__ int item_base(const Plan& a, int b) {
-  return (int)((int64_t)min(max(a.starts[b], 0), a.tokens) * a.group / R) + b;
-}
-
-// item i of the call; nblk = 0 where it has no rows.  The sequence with r rows
-// (times the group) has ceil(r / R) items, at most one more than base(b + 1) -
-// base(b) - 1 counts.
-template <int R>
-__device__ __forceinline__ Item item_at(const Plan& a, int i) {
-  int lo = 0, hi = a.B;  // the last b with base(b) <= i
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (item_base<R>(a, mid) <= i) lo = mid;
-    else hi = mid;
-  }
-  Item t;
-  t.b = lo;
-  const KvRows r = kv_rows(a.starts, lo, a.tokens);
-  const int n = r.s1 - r.s0;
-  const int64_t all = (int64_t)n * a.group, first = (int64_t)(i - item_base<R>(a, lo)) * R;
-  t.s0 = r.s0;
-  t.nblk = 0;
-  t.rows = 0;
-  if (first < 0 || first >= all) return t;
-  t.r0 = (int)first;
-  t.rows = (int)min((int64_t)R, all - first);
-  t.len = max(a.lens[lo], 0);
-  t.p0 = t.len - n;
-  const int i0 = t.r0 / a.group, i1 = (t.r0 + t.rows - 1) / a.group;
-  t.hi = min(a.causal ? max(t.p0 + i1 + 1, 0) : t.len, a.reach);
-  t.lo = a.window > 0 ? max(t.p0 + i0 - a.window + 1, 0) : 0;
-  t.blk0 = t.lo >> 6;
-  t.nblk = t.hi > t.lo ? ((t.hi - 1) >> 6) - t.blk0 + 1 : 1;
-  return t;
-}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -137,18 +71,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// c tanh(z / c) = c - 2 c / (e^(2 z / c) + 1): absolute error about c 2^-22
-__device__ __forceinline__ float capped(float z, float cap, float two_over_cap_log2) {
-  const float x = z * two_over_cap_log2;
-  return cap - __fdividef(2.0f * cap, ex2(x > 126.0f ? 126.0f : x) + 1.0f);
 }
 
 // over the 8 lanes with the same t
@@ -176,125 +98,46 @@ __device__ __forceinline__ uint32_t byte_range(int from, int to) {
   return m;
 }
 
-// partial results of a worker's slot: R rows of dims, then their log2 sums
-template <int D, int R>
-constexpr int kPartFloats = R * D + R;
-
-// Where the copies stand in the worker's range: 32 page numbers are read at a
-// time, one a lane.
-struct Cursor {
-  Item it;
-  int item, head, blk;     // the next page
-  int64_t left;            // pages until the end of the range
-  int page;                // this lane's number of the batch
-  int batch;               // the batch's first page
-};
-
 template <int D, int NB, bool EXTRA>
 __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvAttnParams p, int items) {
   constexpr int R = 8 * NB, W = kWarps<D>, S = kSlots<D>, SLOT = 64 * D;
   extern __shared__ __align__(1024) unsigned char raw[];
   __shared__ __align__(8) uint64_t full_b[W][S];
-  __shared__ int64_t sums[W];
-  __shared__ int64_t found_base[W];
-  __shared__ int found_item[W];
-  __shared__ int seq_s[2 * kSeqsInSmem + 1];
+  __shared__ Ranges<W, W> sh;
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   if (lane == 0) {
     for (int s = 0; s < S; ++s) mbar_init(smem_u32(&full_b[warp][s]), 1);
     fence_barrier_init();
   }
-  if (lane == 0) found_item[warp] = -1;
   pdl_launch_dependents();
   pdl_wait();
 
-  // ------------------------------------------------------------- the range
-  Plan pl{p.q.starts, p.q.lens, p.q.B, p.q.tokens, p.group, p.causal, p.window, p.q.width * 64};
-  if (p.q.B <= kSeqsInSmem) {
-    for (int i = tid; i <= p.q.B; i += 32 * W) seq_s[i] = p.q.starts[i];
-    for (int i = tid; i < p.q.B; i += 32 * W) seq_s[kSeqsInSmem + 1 + i] = p.q.lens[i];
-    pl.starts = seq_s;
-    pl.lens = seq_s + kSeqsInSmem + 1;
-  }
-  __syncthreads();
-  int64_t mine = 0;
-  for (int i = tid; i < items; i += 32 * W) mine += item_at<R>(pl, i).nblk;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-  if (lane == 0) sums[warp] = mine;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int i = 0; i < W; ++i) total += sums[i];
-  total *= p.c.heads;
-  // few pages: fewer workers a CTA, so that every SM has some; a worker has one page at least
-  const int wpc = (int)min((int64_t)W, (total + gridDim.x - 1) / gridDim.x);
-  const int workers = (int)min((int64_t)wpc * gridDim.x, total);
-  const int me = (int)blockIdx.x * wpc + warp;
-  auto range_start = [&](int w) { return total * w / workers; };
-  if (total > 0) {
-    // the items that this CTA's workers begin in: one more pass over the sums
-    int64_t before = 0;
-    for (int i0 = 0; i0 < items; i0 += 32 * W) {
-      const int i = i0 + tid;
-      const int n = i < items ? item_at<R>(pl, i).nblk : 0;
-      int64_t incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      __syncthreads();
-      if (lane == 31) sums[warp] = incl;
-      __syncthreads();
-      int64_t all = 0;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        if (w < warp) incl += sums[w];
-        all += sums[w];
-      }
-      incl += before;
-      for (int w = 0; w < wpc; ++w) {
-        const int64_t f = range_start((int)blockIdx.x * wpc + w) / p.c.heads;
-        if (incl - n <= f && f < incl) {
-          found_item[w] = i;
-          found_base[w] = incl - n;
-        }
-      }
-      before += all;
-    }
-  }
-  __syncthreads();
+  Plan pl;
+  const Dealt dealt = deal_pages<R, W, 32 * W>(p, items, sh, pl);
+  const int me = (int)blockIdx.x * dealt.per_cta + warp;
   Desc* desc = static_cast<Desc*>(p.ws);
-  float* parts = reinterpret_cast<float*>(desc + kMaxWorkers);
-  if (warp >= wpc || me >= workers || found_item[warp] < 0) {  // no worker
+  if (warp >= dealt.per_cta || me >= dealt.workers) {  // no worker
+    const int rest = W - dealt.per_cta;
     if (lane == 0)
-      desc[warp < wpc ? me : (int)gridDim.x * wpc + (int)blockIdx.x * (W - wpc) + warp - wpc].parts = 0;
+      desc[warp < dealt.per_cta ? me : (int)gridDim.x * dealt.per_cta + (int)blockIdx.x * rest + warp - dealt.per_cta]
+          .parts = 0;
     return;
   }
-  const int64_t f0 = range_start(me), f1 = range_start(me + 1);
   const uint32_t ring = smem_u32(raw) + warp * (S * SLOT);
   auto bar = [&](int s) { return smem_u32(&full_b[warp][s]); };
 
   // ------------------------------------------------------------- copies
-  Cursor ld;
-  ld.item = found_item[warp];
-  ld.it = item_at<R>(pl, ld.item);
-  {
-    const int64_t rel = f0 - found_base[warp] * p.c.heads;
-    ld.head = (int)(rel / ld.it.nblk);
-    ld.blk = (int)(rel - (int64_t)ld.head * ld.it.nblk);
-  }
-  ld.left = f1 - f0;
+  // page numbers are read 32 at a time, one a lane
+  Walk<R> ld = walk_of<R>(pl, dealt, sh, p.c.heads, me, warp);
+  Walk<R> at = ld;
+  int pages = -1, batch = 0;
   auto fetch = [&]() {
-    ld.batch = ld.blk;
+    batch = ld.blk;
     const int b = ld.blk + lane;
-    ld.page = b < ld.it.nblk ? kv_page(p.q, p.c.pages, ld.it.b, ld.it.blk0 + b) : -1;
+    pages = b < ld.it.nblk ? kv_page(p.q, p.c.pages, ld.it.b, ld.it.blk0 + b) : -1;
   };
   fetch();
-  const Item it0 = ld.it;
-  const int head0 = ld.head, blk_first = ld.blk;
   uint32_t slot_l = 0;
   int ld_page = -1;
   bool ld_v = false;
@@ -304,8 +147,8 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
   auto issue = [&]() {
     if (!ld_v) {
       if (ld.left == 0) return;
-      if (ld.blk >= ld.batch + 32 || ld.blk < ld.batch) fetch();
-      ld_page = __shfl_sync(0xFFFFFFFFu, ld.page, ld.blk - ld.batch);
+      if (ld.blk >= batch + 32) fetch();
+      ld_page = __shfl_sync(0xFFFFFFFFu, pages, ld.blk - batch);
     }
     const int64_t ph = (int64_t)max(ld_page, 0) * p.c.heads + ld.head;
     if (lane == 0) {
@@ -317,19 +160,8 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
       sc_new = 256;
       if (ld_page >= 0 && lane < 2) sc_new = lane == 0 ? p.c.ks[ph] : p.c.vs[ph];
     } else {
-      --ld.left;
-      if (++ld.blk == ld.it.nblk && ld.left > 0) {
-        ld.blk = 0;
-        if (++ld.head == p.c.heads) {
-          ld.head = 0;
-          do {
-            ld.it = item_at<R>(pl, ++ld.item);
-          } while (ld.it.nblk == 0 && ld.item + 1 < items);
-          fetch();
-        } else if (ld.batch != 0) {
-          fetch();
-        }
-      }
+      const int item = ld.item;
+      if (ld.advance(pl, p.c.heads, 1) && (batch != 0 || ld.item != item)) fetch();
     }
     ld_v = !ld_v;
     if (++slot_l == S) slot_l = 0;
@@ -339,9 +171,6 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
   for (int i = 0; i < 2; ++i) issue();
 
   // ------------------------------------------------------------- the pages
-  Item it = it0;
-  int item = found_item[warp], head = head0, blk = blk_first;
-  int64_t left = f1 - f0;
   uint32_t slot_c = 0, phase = 0;
   int ahead = 2;   // slots begun and not yet worked on
   auto wait_slot = [&]() { mbar_wait(bar(slot_c), phase, &g_err_kv, kErrFullWait); };
@@ -353,9 +182,11 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
     }
     --ahead;
   };
-  while (left > 0) {
+  while (at.left > 0) {
+    const Item& it = at.it;
+    const int head = at.head, blk = at.blk;
     // queries of the segment as operands: lane (g, t) holds row g's dims
-    const int cnt = (int)min(left, (int64_t)(it.nblk - blk));
+    const int cnt = at.segment();
     const bool begins = blk == 0, ends = blk + cnt == it.nblk;
     uint32_t q[NB][D / 16][2];
     float qs[NB][2];      // scale of the scores of rows 2t, 2t + 1, without the page's
@@ -598,11 +429,8 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
       }
       free_slot();
     }
-    blk += cnt;
-    left -= cnt;
-
     // ----------------------------------------------------- the segment's end
-    float* part = parts + ((int64_t)me * 2 + (begins ? 1 : 0)) * kPartFloats<D, R>;
+    float* part = kv_part(p.ws, me, begins ? 1 : 0, R, D);
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -631,25 +459,10 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
           if (g == 0) part[R * D + r] = log2s;
         }
       }
-    if (left == 0 && lane == 0) {
-      Desc d{0, item, it.rows, head};
-      if (begins && !ends) {
-        const int64_t end = f1 + (it.nblk - blk);
-        int w = me + 1;  // the worker that holds the last page
-        while (range_start(w + 1) < end) ++w;
-        d.parts = w - me + 1;
-      }
-      desc[me] = d;
-    }
-    if (left > 0) {
-      blk = 0;
-      if (++head == p.c.heads) {
-        head = 0;
-        do {
-          it = item_at<R>(pl, ++item);
-        } while (it.nblk == 0 && item + 1 < items);
-      }
-    }
+    if (at.left == cnt && lane == 0)
+      desc[me] = desc_of(dealt, me, begins && !ends ? dealt.start(me + 1) + (it.nblk - blk - cnt) : 0, at.item, it.rows,
+                         head);
+    at.advance(pl, p.c.heads, cnt);
   }
 }
 
@@ -659,16 +472,14 @@ template <int D, int R>
 __global__ void __launch_bounds__(256) rn_kv_join_kernel(const KvAttnParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const Desc* desc = static_cast<const Desc*>(p.ws);
   const int w = blockIdx.x;
-  const Desc d = desc[w];
+  const Desc d = static_cast<const Desc*>(p.ws)[w];
   if (d.parts == 0) return;
-  const float* parts = reinterpret_cast<const float*>(desc + kMaxWorkers);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto part = [&](int i) { return parts + ((int64_t)(w + i) * 2 + (i == 0 ? 1 : 0)) * kPartFloats<D, R>; };
-  Plan pl{p.q.starts, p.q.lens, p.q.B, p.q.tokens, p.group, p.causal, p.window, p.q.width * 64};
+  auto part = [&](int i) -> const float* { return kv_part(p.ws, w + i, i == 0 ? 1 : 0, R, D); };
+  const Plan pl{p.q.starts, p.q.lens, p.q.B, p.q.tokens, p.group, p.causal, p.window, p.q.width * 64};
   const Item it = item_at<R>(pl, d.item);
-  for (int r = warp; r < d.rows; r += 8) {
+  for (int r = blockIdx.y * 8 + warp; r < d.rows; r += 8 * gridDim.y) {
     float top = -INFINITY;
     for (int i = lane; i < d.parts; i += 32) top = fmaxf(top, part(i)[R * D + r]);
 #pragma unroll
@@ -676,6 +487,7 @@ __global__ void __launch_bounds__(256) rn_kv_join_kernel(const KvAttnParams p) {
     if (top == -INFINITY) top = 0.0f;
     float sum = 0.0f;
     float acc[D / 32] = {};
+#pragma unroll 4
     for (int i = 0; i < d.parts; ++i) {
       const float wgt = ex2(part(i)[R * D + r] - top);
       sum += wgt;
@@ -692,22 +504,6 @@ __global__ void __launch_bounds__(256) rn_kv_join_kernel(const KvAttnParams p) {
   }
 }
 
-template <class... A>
-rn_status launch(void (*k)(A...), int grid, int threads, size_t smem, cudaStream_t s, A... a) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, k, a...) != cudaSuccess) return RN_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? RN_OK : RN_ERR_CUDA;
-}
-
 template <int D, int NB, bool EXTRA>
 rn_status launch_all(const KvAttnParams& p, int sms, cudaStream_t s) {
   constexpr int R = 8 * NB, W = kWarps<D>;
@@ -719,16 +515,28 @@ rn_status launch_all(const KvAttnParams& p, int sms, cudaStream_t s) {
       }) < 1)
     return RN_ERR_CUDA;
   const int items = (int)((int64_t)p.q.tokens * p.group / R) + p.q.B;
-  const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-  rn_status st = launch<KvAttnParams, int>(k, grid, 32 * W, smem, s, p, items);
+  const int grid = sms < kKvMaxCtas ? sms : kKvMaxCtas;
+  rn_status st = launch_pdl<KvAttnParams, int>(k, dim3(grid), 32 * W, smem, s, p, items);
   if (st != RN_OK) return st;
-  return launch<KvAttnParams>(rn_kv_join_kernel<D, R>, grid * W, 256, 0, s, p);
+  return launch_kv_join(p, D, R, grid * W, s);
+}
+
+template <int D>
+rn_status join_d(const KvAttnParams& p, int rows, int workers, cudaStream_t s) {
+  switch (rows) {
+    case 8: return launch_pdl<KvAttnParams>(rn_kv_join_kernel<D, 8>, dim3(workers), 256, 0, s, p);
+    case 16: return launch_pdl<KvAttnParams>(rn_kv_join_kernel<D, 16>, dim3(workers, 2), 256, 0, s, p);
+    case 128: return launch_pdl<KvAttnParams>(rn_kv_join_kernel<D, 128>, dim3(workers, 8), 256, 0, s, p);
+    default: return launch_pdl<KvAttnParams>(rn_kv_join_kernel<D, 256>, dim3(workers, 8), 256, 0, s, p);
+  }
 }
 
 template <int D>
 rn_status launch_d(const KvAttnParams& p, int sms, cudaStream_t s) {
   const bool extra = p.softcap > 0.0f || p.slopes != nullptr;
-  const bool one = (int64_t)p.q.tokens * p.group <= (int64_t)8 * p.q.B;
+  const int64_t rows = (int64_t)p.q.tokens * p.group;  // of a head, all sequences
+  if (rows > (int64_t)16 * p.q.B) return launch_kv_tile(p, D, sms, s);
+  const bool one = rows <= (int64_t)8 * p.q.B;
   if (one) return extra ? launch_all<D, 1, true>(p, sms, s) : launch_all<D, 1, false>(p, sms, s);
   return extra ? launch_all<D, 2, true>(p, sms, s) : launch_all<D, 2, false>(p, sms, s);
 }
@@ -744,8 +552,18 @@ rn_status launch_kv_attn(const KvAttnParams& p, int dim, int sms, cudaStream_t s
   }
 }
 
-size_t kv_attn_bytes(int64_t, int64_t, int, int dim) {
-  return sizeof(Desc) * kMaxWorkers + sizeof(float) * 2 * kMaxWorkers * (size_t)(16 * dim + 16);
+rn_status launch_kv_join(const KvAttnParams& p, int dim, int rows, int workers, cudaStream_t s) {
+  switch (dim) {
+    case 64: return join_d<64>(p, rows, workers, s);
+    case 128: return join_d<128>(p, rows, workers, s);
+    case 192: return join_d<192>(p, rows, workers, s);
+    default: return join_d<256>(p, rows, workers, s);
+  }
+}
+
+size_t kv_attn_bytes(int dim) {
+  const int64_t few = kKvMaxWorkers * part_floats(16, dim), tile = kKvMaxCtas * part_floats(256, dim);
+  return sizeof(Desc) * kKvMaxWorkers + sizeof(float) * 2 * (size_t)(few > tile ? few : tile);
 }
 
 rn_status read_clear_error_kv(unsigned* code) {

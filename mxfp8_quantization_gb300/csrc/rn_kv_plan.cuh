@@ -1,0 +1,256 @@
+// How the attention over the paged cache deals its work: row tiles of the
+// sequences, their pages, the workers' ranges, and where partial results lie.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "rn_internal.h"
+#include "rn_kv.cuh"
+
+namespace rn {
+
+constexpr int kKvMaxCtas = 160;
+constexpr int kKvMaxWorkers = kKvMaxCtas * 8;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// sequences whose rows and lengths are kept in shared memory
+constexpr int kSeqsInSmem = 1024;
+
+// the (row tile, head) that a worker begins last and does not finish
+struct Desc {
+  int parts;   // workers that share it, this one the first (0: none)
+  int item, rows, head;
+};
+
+// a row tile of a sequence
+struct Item {
+  int b;
+  int s0;          // first row of the sequence
+  int r0, rows;    // its rows of (query, query head of the group), query-major
+  int p0;          // position of query 0
+  int len;
+  int lo, hi;      // positions that any row sees
+  int blk0, nblk;  // pages; one without positions where the rows see none
+};
+
+struct Plan {
+  const int* starts;  // shared or global
+  const int* lens;
+  int B, tokens, group, causal, window;
+  int reach;          // positions that the page table has room for
+};
+
+template <int R>
+__device__ __forceinline__ int item_base(const Plan& a, int b) {
+  return (int)((int64_t)min(max(a.starts[b], 0), a.tokens) * a.group / R) + b;
+}
+
+// item i of the call; nblk = 0 where it has no rows.  The sequence with r rows
+// (times the group) has ceil(r / R) items, at most one more than base(b + 1) -
+// base(b) - 1 counts.
+template <int R>
+__device__ __forceinline__ Item item_at(const Plan& a, int i) {
+  int lo = 0, hi = a.B;  // the last b with base(b) <= i
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (item_base<R>(a, mid) <= i) lo = mid;
+    else hi = mid;
+  }
+  Item t;
+  t.b = lo;
+  const KvRows r = kv_rows(a.starts, lo, a.tokens);
+  const int n = r.s1 - r.s0;
+  const int64_t all = (int64_t)n * a.group, first = (int64_t)(i - item_base<R>(a, lo)) * R;
+  t.s0 = r.s0;
+  t.nblk = 0;
+  t.rows = 0;
+  if (first < 0 || first >= all) return t;
+  t.r0 = (int)first;
+  t.rows = (int)min((int64_t)R, all - first);
+  t.len = max(a.lens[lo], 0);
+  t.p0 = t.len - n;
+  const int i0 = t.r0 / a.group, i1 = (t.r0 + t.rows - 1) / a.group;
+  t.hi = min(a.causal ? max(t.p0 + i1 + 1, 0) : t.len, a.reach);
+  t.lo = a.window > 0 ? max(t.p0 + i0 - a.window + 1, 0) : 0;
+  t.blk0 = t.lo >> 6;
+  t.nblk = t.hi > t.lo ? ((t.hi - 1) >> 6) - t.blk0 + 1 : 1;
+  return t;
+}
+
+// A range of (row tile, head, page) triples, in this order, from its first on.
+template <int R>
+struct Walk {
+  Item it;
+  int item, head, blk;  // the next page
+  int64_t left;         // pages until the range's end
+
+  // pages of the (row tile, head) that the range still has
+  __device__ __forceinline__ int segment() const { return (int)min(left, (int64_t)(it.nblk - blk)); }
+
+  // n pages further, within a segment; true where that goes on to another (row tile, head)
+  __device__ __forceinline__ bool advance(const Plan& a, int heads, int n) {
+    left -= n;
+    blk += n;
+    if (blk < it.nblk || left == 0) return false;
+    blk = 0;
+    if (++head == heads) {
+      head = 0;
+      do {
+        it = item_at<R>(a, ++item);
+      } while (it.nblk == 0);  // pages are left, so an item with some follows
+    }
+    return true;
+  }
+};
+
+// what the workers of a CTA find out about their ranges
+template <int W, int WARPS>
+struct Ranges {
+  int64_t sums[WARPS];
+  int64_t base[W];
+  int item[W];
+  int seqs[2 * kSeqsInSmem + 1];
+};
+
+struct Dealt {
+  int64_t total;   // pages of the call, times heads
+  int per_cta;     // workers of a CTA; all of them are `workers`
+  int workers;
+  __device__ __forceinline__ int64_t start(int w) const { return total * w / workers; }
+};
+
+// Called by all NT threads: the call's plan, and the items that the CTA's
+// workers begin in (up to W of them; fewer where pages are few, so that every
+// SM has some, and a worker has one page at least).
+template <int R, int W, int NT>
+__device__ __forceinline__ Dealt deal_pages(const KvAttnParams& p, int items, Ranges<W, NT / 32>& sh, Plan& pl) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pl = Plan{p.q.starts, p.q.lens, p.q.B, p.q.tokens, p.group, p.causal, p.window, p.q.width * 64};
+  if (p.q.B <= kSeqsInSmem) {
+    for (int i = tid; i <= p.q.B; i += NT) sh.seqs[i] = p.q.starts[i];
+    for (int i = tid; i < p.q.B; i += NT) sh.seqs[kSeqsInSmem + 1 + i] = p.q.lens[i];
+    pl.starts = sh.seqs;
+    pl.lens = sh.seqs + kSeqsInSmem + 1;
+  }
+  if (tid < W) sh.item[tid] = -1;
+  __syncthreads();
+  int64_t mine = 0;
+  for (int i = tid; i < items; i += NT) mine += item_at<R>(pl, i).nblk;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+  if (lane == 0) sh.sums[warp] = mine;
+  __syncthreads();
+  Dealt d;
+  d.total = 0;
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) d.total += sh.sums[i];
+  d.total *= p.c.heads;
+  d.per_cta = (int)min((int64_t)W, (d.total + gridDim.x - 1) / gridDim.x);
+  d.workers = (int)min((int64_t)d.per_cta * gridDim.x, d.total);
+  if (d.total == 0) return d;
+  // one more pass over the sums
+  int64_t before = 0;
+  for (int i0 = 0; i0 < items; i0 += NT) {
+    const int i = i0 + tid;
+    const int n = i < items ? item_at<R>(pl, i).nblk : 0;
+    int64_t incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    __syncthreads();
+    if (lane == 31) sh.sums[warp] = incl;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      if (w < warp) incl += sh.sums[w];
+      all += sh.sums[w];
+    }
+    incl += before;
+    for (int w = 0; w < d.per_cta; ++w) {
+      const int me = (int)blockIdx.x * d.per_cta + w;
+      if (me >= d.workers) break;
+      const int64_t f = d.start(me) / p.c.heads;
+      if (incl - n <= f && f < incl) {
+        sh.item[w] = i;
+        sh.base[w] = incl - n;
+      }
+    }
+    before += all;
+  }
+  __syncthreads();
+  return d;
+}
+
+// the range of worker `me`, the CTA's number w
+template <int R, int W, int WARPS>
+__device__ __forceinline__ Walk<R> walk_of(const Plan& pl, const Dealt& d, const Ranges<W, WARPS>& sh, int heads,
+                                           int me, int w) {
+  Walk<R> k;
+  const int64_t f0 = d.start(me);
+  k.item = sh.item[w];
+  k.it = item_at<R>(pl, k.item);
+  const int64_t rel = f0 - sh.base[w] * heads;
+  k.head = (int)(rel / k.it.nblk);
+  k.blk = (int)(rel - (int64_t)k.head * k.it.nblk);
+  k.left = d.start(me + 1) - f0;
+  return k;
+}
+
+// What worker `me` leaves for the join: `end` is where the pages of the (row
+// tile, head) that it began and did not finish end, 0 if it has none.
+__device__ __forceinline__ Desc desc_of(const Dealt& d, int me, int64_t end, int item, int rows, int head) {
+  Desc r{0, item, rows, head};
+  if (end > 0) {
+    int w = me + 1;  // the worker that holds the last page
+    while (d.start(w + 1) < end) ++w;
+    r.parts = w - me + 1;
+  }
+  return r;
+}
+
+// Workspace: a Desc for every worker, then two partial results each: of the
+// (row tile, head) that its range begins within (0) and of the one that it
+// begins and does not finish (1): R rows of dims, then their log2 sums.
+__host__ __device__ inline int64_t part_floats(int rows, int dim) { return (int64_t)rows * dim + rows; }
+__device__ __forceinline__ float* kv_part(void* ws, int worker, int which, int rows, int dim) {
+  return reinterpret_cast<float*>(static_cast<Desc*>(ws) + kKvMaxWorkers) +
+         ((int64_t)worker * 2 + which) * part_floats(rows, dim);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// c tanh(z / c) = c - 2 c / (e^(2 z / c) + 1): absolute error about c 2^-22
+__device__ __forceinline__ float capped(float z, float cap, float two_over_cap_log2) {
+  const float x = z * two_over_cap_log2;
+  return cap - __fdividef(2.0f * cap, ex2(x > 126.0f ? 126.0f : x) + 1.0f);
+}
+
+// joins the partial results of tiles of `rows` rows left by up to `workers` workers
+rn_status launch_kv_join(const KvAttnParams& p, int dim, int rows, int workers, cudaStream_t s);
+// for more than a few rows a key/value head (rn_kv_tile.cu)
+rn_status launch_kv_tile(const KvAttnParams& p, int dim, int sms, cudaStream_t s);
+
+template <class... A>
+rn_status launch_pdl(void (*k)(A...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, k, a...) != cudaSuccess) return RN_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? RN_OK : RN_ERR_CUDA;
+}
+
+}  // namespace rn
