@@ -4,25 +4,31 @@
 //
 // Both products run on the tensor cores (tcgen05, f16 operands, fp32 sums) with
 // 128 rows of queries as M.  Tensor memory holds all that belongs to rows: the
-// queries (f16, the A operand of S = Q K^T), the scores S of one page (fp32, 64
-// columns), the weights in their place (f16, the A operand of O = P V) and the
-// output O (fp32); so shared memory holds keys and values only, as B operands
-// in f16 (128-byte swizzle): K [64 positions, dim] and V^T [dim, 64 positions],
-// both as the cache has them.
+// queries (f16, the A operand of S = Q K^T), the scores S of a page (fp32), the
+// weights in their place (f16, the A operand of O = P V) and the output O (fp32);
+// so shared memory holds keys and values only, as B operands in f16 (128-byte
+// swizzle): K [64 positions, dim] and V^T [dim, 64 positions], as the cache has them.
 //
 // Roles of a CTA (one an SM):
-//   NG groups of 4 warps   softmax: a thread owns a row of a tile
-//   4 warps                codes -> f16: pages are read two ahead into registers
-//   1 warp of 4            issues the products (the others give their registers away)
+//   1 warp                 issues the products
+//   1 warp                 copies pages (bulk copies of 64 dim bytes) into a ring of codes
+//   4 warps                codes -> f16
+//   8 warps a tile         softmax: a warp owns 16 rows, a thread 16 of the 64 scores of two of them
+// The softmax of a page is a long chain of few instructions for its warps (an
+// exchange of maxima between 4 lanes, 32 exponentials a thread), so many warps
+// share it: with 4 warps a tile and a row a thread, a page of two tiles took 2220
+// cycles, the products 1024.
 // dim <= 128, NG = 2: two tiles of 128 rows take turns, so the tensor cores work
-// on one while the other's scores become weights.  Where a (row tile, head)
-// has 128 rows or fewer, the two groups take its even and odd pages instead and
-// the first one adds both results up at the end.  dim > 128, NG = 1: the output
-// takes half of the tensor memory; one tile, two buffers of scores.
+// on one while the other's scores become weights in their place.  Where a (row
+// tile, head) has 128 rows or fewer, the two tiles' warps take its even and odd
+// pages instead and the first ones add both results up at the end.  dim > 128, NG =
+// 1: the output takes half of the tensor memory; one tile, two buffers of scores.
 //
 // The weights' reference M is not raised for less than 2^8 (weights up to 2^8
 // fit f16 as well), which leaves few rescalings of O in tensor memory.
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "rn_device.cuh"
 #include "rn_internal.h"
@@ -41,25 +47,27 @@ template <int D>
 constexpr int kTileRows = 128 * kGroups<D>;
 template <int D>
 constexpr int kTileThreads = 128 * (kGroups<D> + 2);
-// Registers a thread: the launch gives 65536 / threads, which the last group hands to the others
-// (two groups: 2 * 160 + 128 + 64 = 4 * 128; one: 200 + 208 + 96 = 3 * 168)
+// Registers a thread: the launch gives 128 (512 threads) or 168 (384); the products' and the converting group hand
+// some to the softmax's (2 * 176 + 2 * 80 = 4 * 128, 248 + 2 * 128 = 3 * 168)
 template <int D>
-constexpr int kRegsSoft = kGroups<D> == 2 ? 160 : 200;
+constexpr int kRegsSoft = kGroups<D> == 2 ? 176 : 248;
 template <int D>
-constexpr int kRegsConv = kGroups<D> == 2 ? 128 : 208;
-template <int D>
-constexpr int kRegsMma = kGroups<D> == 2 ? 64 : 96;
-// a stage: f16 keys and values of a page
+constexpr int kRegsRest = kGroups<D> == 2 ? 80 : 128;
+// a stage: f16 keys and values of a page; a slot: its codes
 template <int D>
 constexpr int kStageBytesKv = 2 * 64 * D * 2;
 template <int D>
-constexpr int kStagesKv = D == 64 ? 8 : 196608 / kStageBytesKv<D>;
+constexpr int kSlotBytes = 2 * 64 * D;
+template <int D>
+constexpr int kStagesKv = D == 64 ? 6 : D == 128 ? 4 : 2;
+template <int D>
+constexpr int kSlotsKv = D == 64 ? 12 : D == 256 ? 2 : 4;
 
 // tensor memory columns
 template <int D>
 struct Cols {
   static constexpr int kQ = D / 2;                            // of a tile's queries
-  static constexpr int kS = kGroups<D> * kQ;                  // two score buffers of 64
+  static constexpr int kS = kGroups<D> * kQ;                  // two buffers of scores
   static constexpr int kO = kS + 128;
   static_assert(kO + kGroups<D> * D <= 512, "tensor memory");
 };
@@ -72,20 +80,58 @@ __device__ __forceinline__ void tmem_free1(uint32_t taddr) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(taddr));
 }
 
-// D (+)= A B: A f16 in tensor memory, B f16 in shared memory; one elected lane of a converged warp issues it
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
+// f16 x f16 -> fp32, M = 128
+__host__ __device__ constexpr uint32_t idesc_f16(int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
-__device__ __forceinline__ void mma_commit1(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-      : "memory");
+
+// What the products' warp issues for a page and tile, by one election: P V into the output (o, from the weights at
+// p and the values at vd; add: not the first page), then its arrivals, then the scores of a later page (s, from the
+// queries at q and the keys at kd) with theirs.  An election for each product took 94 cycles whatever its size; so
+// a product of N columns takes its N / 2 cycles.
+#define RN_PV(A, B, ACC) \
+  "add.u32 ra, %1, " #A ";\n\tadd.u64 rb, %2, " #B ";\n\t" \
+  "@po tcgen05.mma.cta_group::1.kind::f16 [%0], [ra], rb, %3, " ACC ";\n\t"
+#define RN_QK(A, B, ACC) \
+  "add.u32 ra, %5, " #A ";\n\tadd.u64 rb, %6, " #B ";\n\t" \
+  "@ps tcgen05.mma.cta_group::1.kind::f16 [%4], [ra], rb, %7, " ACC ";\n\t"
+#define RN_ARRIVE(P, BAR) "@" P " tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [" BAR "];\n\t"
+#define RN_HEAD                                                                                                      \
+  "{\n\t.reg .pred e, po, ps, pe, add, yes, no;\n\t.reg .b32 ra;\n\t.reg .b64 rb;\n\t"                               \
+  "setp.ne.u32 add, %8, 0;\n\tsetp.ne.u32 po, %9, 0;\n\tsetp.ne.u32 ps, %10, 0;\n\tsetp.ne.u32 pe, %11, 0;\n\t"      \
+  "setp.eq.u32 yes, %8, %8;\n\tsetp.ne.u32 no, %8, %8;\n\telect.sync _|e, 0xffffffff;\n\t"                           \
+  "and.pred po, po, e;\n\tand.pred ps, ps, e;\n\tand.pred pe, pe, e;\n\t"                                            \
+  RN_PV(0, 0, "add") RN_PV(8, 2, "yes") RN_PV(16, 4, "yes") RN_PV(24, 6, "yes")                                      \
+  RN_ARRIVE("pe", "%12") RN_ARRIVE("po", "%13")                                                                      \
+  RN_QK(0, 0, "no") RN_QK(8, 2, "yes") RN_QK(16, 4, "yes") RN_QK(24, 6, "yes")
+#define RN_TAIL                                                                                                      \
+  RN_ARRIVE("ps", "%14")                                                                                             \
+  "}" ::"r"(o), "r"(p), "l"(vd), "r"(ido), "r"(s), "r"(q), "l"(kd), "r"(ids), "r"((uint32_t)add),                    \
+      "r"((uint32_t)has_o), "r"((uint32_t)has_s), "r"((uint32_t)frees), "r"(empty), "r"(obar), "r"(sbar) : "memory"
+#define RN_QK64(A0, A1, A2, A3, B0, B1, B2, B3) \
+  RN_QK(A0, B0, "yes") RN_QK(A1, B1, "yes") RN_QK(A2, B2, "yes") RN_QK(A3, B3, "yes")
+template <int D>
+__device__ __forceinline__ void issue_task(bool has_o, uint32_t o, uint32_t p, uint64_t vd, bool add, bool frees,
+                                           uint32_t empty, uint32_t obar, bool has_s, uint32_t s, uint32_t q,
+                                           uint64_t kd, uint32_t sbar) {
+  constexpr uint32_t ido = idesc_f16(D), ids = idesc_f16(64);
+  if constexpr (D == 64)
+    asm volatile(RN_HEAD RN_TAIL);
+  else if constexpr (D == 128)
+    asm volatile(RN_HEAD RN_QK64(32, 40, 48, 56, 512, 514, 516, 518) RN_TAIL);
+  else if constexpr (D == 192)
+    asm volatile(RN_HEAD RN_QK64(32, 40, 48, 56, 512, 514, 516, 518)
+                     RN_QK64(64, 72, 80, 88, 1024, 1026, 1028, 1030) RN_TAIL);
+  else
+    asm volatile(RN_HEAD RN_QK64(32, 40, 48, 56, 512, 514, 516, 518) RN_QK64(64, 72, 80, 88, 1024, 1026, 1028, 1030)
+                     RN_QK64(96, 104, 112, 120, 1536, 1538, 1540, 1542) RN_TAIL);
 }
+#undef RN_PV
+#undef RN_QK
+#undef RN_QK64
+#undef RN_ARRIVE
+#undef RN_HEAD
+#undef RN_TAIL
 
 template <int N>
 __device__ __forceinline__ void regs_up() {
@@ -110,29 +156,47 @@ __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// f16 x f16 -> fp32, M = 128
-__host__ __device__ constexpr uint32_t idesc_f16(int n) {
-  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
-}
-
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-__device__ __forceinline__ uint4 ldg_codes(const void* p) {
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
+// 16 codes -> two 16-byte units of a swizzled row of f16
+__device__ __forceinline__ void store16_f16(uint32_t row_addr, int row8, int sub, const uint4& v) {
+  uint32_t h[8];
+  e4m3x4_f16x4(v.x, h[0], h[1]);
+  e4m3x4_f16x4(v.y, h[2], h[3]);
+  e4m3x4_f16x4(v.z, h[4], h[5]);
+  e4m3x4_f16x4(v.w, h[6], h[7]);
+  sts128(row_addr + (((2 * sub) ^ row8) << 4), h[0], h[1], h[2], h[3]);
+  sts128(row_addr + (((2 * sub + 1) ^ row8) << 4), h[4], h[5], h[6], h[7]);
+}
+
+// the largest; NaN where all are
+__device__ __forceinline__ float max_of3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// what the copying warp says about a slot's page
+struct SlotInfo {
+  int from, to;        // positions of it that any row sees; none where there is no page
+  int some;            // some rows may see only some of those
+};
 // what the converting warps say about a stage's page
 struct PageInfo {
-  int ek, ev;          // exponents; ek = kNoPage: no page
   uint32_t nan[2];     // positions whose values hold a NaN that is not in the stage
 };
-constexpr int kNoPage = 1 << 20;
+constexpr int kNoPage = 0x7FFF;
 
 struct Stats {
   float m, M, l;
@@ -143,14 +207,17 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
   constexpr int NG = kGroups<D>, R = kTileRows<D>, NT = kTileThreads<D>, NS = kStagesKv<D>;
   using C = Cols<D>;
   extern __shared__ unsigned char raw[];
-  __shared__ __align__(8) uint64_t full_b[NS], empty_b[NS], s_b[2], p_b[2], q_b, o_b[2];
+  constexpr int NC = kSlotsKv<D>;
+  __shared__ __align__(8) uint64_t full_b[NS], empty_b[NS], in_b[NC], out_b[NC], s_b[2], p_b[2], q_b, o_b[2];
   __shared__ uint32_t tmem_at;
   __shared__ PageInfo info[NS];
+  __shared__ SlotInfo slot_info[NC];
   __shared__ Stats other[128];
   __shared__ Ranges<1, NT / 32> sh;
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
-  constexpr int kConv = 4 * NG, kMma = kConv + 4;
+  const uint32_t codes = ring + NS * kStageBytesKv<D>;
+  constexpr int kMma = 0, kCopy = 1, kConv = 4, kSoft = 8;
   unsigned* err = &g_err_kv_tile;
 
   if (tid == 0) {
@@ -158,12 +225,16 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
       mbar_init(smem_u32(&full_b[s]), 4);   // the converting warps
       mbar_init(smem_u32(&empty_b[s]), 1);  // the products that read the stage
     }
+    for (int s = 0; s < NC; ++s) {
+      mbar_init(smem_u32(&in_b[s]), 1);
+      mbar_init(smem_u32(&out_b[s]), 4);    // the converting warps
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_b[i]), 1);      // scores
-      mbar_init(smem_u32(&p_b[i]), 4);      // weights: a group's warps
+      mbar_init(smem_u32(&p_b[i]), 4);      // weights: a tile's warps
       mbar_init(smem_u32(&o_b[i]), 1);      // a page's part of the output
     }
-    mbar_init(smem_u32(&q_b), 4 * NG);      // queries: every softmax warp
+    mbar_init(smem_u32(&q_b), 4 * NG);      // queries: 4 warps a tile
     fence_barrier_init();
   }
   if (warp == kMma) tmem_alloc1(smem_u32(&tmem_at));
@@ -173,126 +244,119 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
   Plan pl;
   const Dealt dealt = deal_pages<R, 1, NT>(p, items, sh, pl);  // has barriers
   tc_fence_after();
-  const uint32_t tmem = tmem_at;
   const int me = (int)blockIdx.x;
   Desc* desc = static_cast<Desc*>(p.ws);
   if (me >= dealt.workers) {
     if (tid == 0) desc[me].parts = 0;
-  } else if (warp >= kMma) {
-    // ------------------------------------------------------ products
-    regs_down<kRegsMma<D>>();
+  } else if (warp < kConv) {
+    regs_down<kRegsRest<D>>();
     Walk<R> at = walk_of<R>(pl, dealt, sh, p.c.heads, me, 0);
-    constexpr uint32_t kIdS = idesc_f16(64), kIdO = idesc_f16(D);
+    if (warp == kCopy) {
+      // ---------------------------------------------------- copies
+      // page numbers are read 32 at a time, one a lane
+      int page = -1, batch = 0;
+      auto fetch = [&]() {
+        batch = at.blk;
+        const int b = at.blk + lane;
+        page = b < at.it.nblk ? kv_page(p.q, p.c.pages, at.it.b, at.it.blk0 + b) : -1;
+      };
+      fetch();
+      RingPos r{0, 0};
+      while (at.left > 0) {
+        if (at.blk >= batch + 32) fetch();
+        const int pg = __shfl_sync(0xFFFFFFFFu, page, at.blk - batch);
+        mbar_wait(smem_u32(&out_b[r.slot]), r.phase ^ 1u, err, kErrEmptyWait);
+        if (lane == 0) {
+          const Item& it = at.it;
+          const int base = (it.blk0 + at.blk) * 64;
+          const int i0 = it.r0 / p.group, i1 = (it.r0 + it.rows - 1) / p.group;
+          const bool some = i1 > i0 && (base + 64 > (p.causal ? it.p0 + i0 + 1 : it.len) ||
+                                        (p.window > 0 && base < it.p0 + i1 - p.window + 1));
+          slot_info[r.slot] = SlotInfo{max(it.lo - base, 0), pg >= 0 ? min(it.hi - base, 64) : 0, some};
+          // a page that is none is masked: any other stands for it
+          const int64_t ph = (int64_t)max(pg, 0) * p.c.heads + at.head;
+          const uint32_t to = codes + r.slot * kSlotBytes<D>, bar = smem_u32(&in_b[r.slot]);
+          mbar_arrive_expect_tx(bar, kSlotBytes<D>);
+          bulk_g2s(to, p.c.k + ph * 64 * D, 64 * D, bar);
+          bulk_g2s(to + 64 * D, p.c.v + ph * 64 * D, 64 * D, bar);
+        }
+        __syncwarp();
+        r.advance(1, NC);
+        const int item = at.item;
+        if (at.advance(pl, p.c.heads, 1) && (batch != 0 || at.item != item)) fetch();
+      }
+    }
+    // ------------------------------------------------------ products
     RingPos rs{0, 0}, ro{0, 0};          // stages of the scores' pages, and of the outputs'
-    uint32_t p_ph[2] = {0, 0}, q_ph = 0;
+    uint32_t p_ph0 = 0, p_ph1 = 0, q_ph = 0;
+    const uint64_t kd0 = smem_desc(ring, false), vd0 = smem_desc(ring + 64 * D * 2, false);
+    constexpr uint32_t kStep = kStageBytesKv<D> >> 4;  // of the descriptors, a stage
     while (warp == kMma && at.left > 0) {
       const int cnt = at.segment();
       const bool both = NG == 2 && at.it.rows > 128;   // every page for both tiles
       const int tasks = both ? 2 * cnt : cnt;
       mbar_wait_warp(smem_u32(&q_b), q_ph, err, kErrReadyWait);
       q_ph ^= 1u;
-      tc_fence_after();
-      auto scores = [&](int i) {
-        if (!both || (i & 1) == 0) mbar_wait_warp(smem_u32(&full_b[rs.slot]), rs.phase, err, kErrFullWait);
-        tc_fence_after();
-        const int x = i & 1;
-        const uint32_t d = tmem + C::kS + 64 * x, q = tmem + (NG == 2 ? x * C::kQ : 0);
-        const uint32_t kb = ring + rs.slot * kStageBytesKv<D>;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-          mma_f16_ts(d, q + 8 * s, smem_desc(kb + (s / 4) * 8192, false) + 2 * (s % 4), kIdS, s > 0);
-        mma_commit1(smem_u32(&s_b[x]));
-        if (!both || x == 1) rs.advance(1, NS);
-      };
-      scores(0);
-      if (tasks > 1) scores(1);
-      for (int i = 0; i < tasks; ++i) {
-        const int x = i & 1;
-        mbar_wait_warp(smem_u32(&p_b[x]), p_ph[x], err, kErrStatsWait);
-        p_ph[x] ^= 1u;
-        tc_fence_after();
-        const uint32_t a = tmem + C::kS + 64 * x, d = tmem + C::kO + (NG == 2 ? x * D : 0);
-        const uint32_t vb = ring + ro.slot * kStageBytesKv<D> + 64 * D * 2;
-        const bool begun = NG == 2 ? i > 1 : i > 0;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) mma_f16_ts(d, a + 8 * s, smem_desc(vb, false) + 2 * s, kIdO, begun || s > 0);
-        if (!both || x == 1) {
-          mma_commit1(smem_u32(&empty_b[ro.slot]));
-          ro.advance(1, NS);
+      // task i: a page and the tile (or score buffer) x = i & 1; its scores are asked for two tasks ahead
+      auto task = [&](auto xc, int i) {
+        constexpr int x = decltype(xc)::value;
+        constexpr uint32_t kSx = C::kS + 64 * x, kOx = C::kO + (NG == 2 ? x * D : 0), kQx = NG == 2 ? x * C::kQ : 0;
+        const bool has_o = i >= 0, has_s = i + 2 < tasks;
+        const bool frees = has_o && (x == 1 || !both);
+        auto issue = [&](bool outputs, bool scores) {
+          tc_fence_after();
+          issue_task<D>(outputs, kOx, kSx, vd0 + ro.slot * kStep, i >= NG, outputs && frees,
+                        smem_u32(&empty_b[ro.slot]), smem_u32(&o_b[x]), scores, kSx, kQx,
+                        kd0 + rs.slot * kStep, smem_u32(&s_b[x]));
+        };
+        if (has_o) {
+          uint32_t& ph = x ? p_ph1 : p_ph0;
+          mbar_wait_warp(smem_u32(&p_b[x]), ph, err, kErrStatsWait);
+          ph ^= 1u;
+          // with two stages the page that the scores wait for needs the one that this frees
+          if (NS == 2) issue(true, false);
         }
-        mma_commit1(smem_u32(&o_b[x]));
-        if (i + 2 < tasks) scores(i + 2);
+        if (has_s && (x == 0 || !both)) mbar_wait_warp(smem_u32(&full_b[rs.slot]), rs.phase, err, kErrFullWait);
+        if (NS > 2 || has_s) issue(NS > 2 && has_o, has_s);
+        if (frees) ro.advance(1, NS);
+        if (has_s && (x == 1 || !both)) rs.advance(1, NS);
+      };
+      for (int i = -2; i < tasks; i += 2) {
+        task(std::integral_constant<int, 0>{}, i);
+        if (i + 1 < tasks) task(std::integral_constant<int, 1>{}, i + 1);
       }
       at.advance(pl, p.c.heads, cnt);
     }
-  } else if (warp >= kConv) {
+  } else if (warp < kSoft) {
     // ------------------------------------------------------ codes to f16
-    if constexpr (NG == 1) regs_up<kRegsConv<D>>();
-    Walk<R> at = walk_of<R>(pl, dealt, sh, p.c.heads, me, 0);
-    const int ct = tid - 32 * kConv, cw = warp - kConv;
-    constexpr int N = D / 32;          // 16-byte pieces a thread, of keys and of values
-    constexpr int DEPTH = 2;           // pages read ahead
-    // keys: a warp takes 8 positions x 64 dims (4 pieces each); values: 8 dims x 64 positions
-    const int sub = lane & 3, row8 = lane >> 2;
-    uint4 k[DEPTH][N], v[DEPTH][N];
-    struct Ahead {
-      int page, head, from, to, base;  // positions [from, to) of the page are seen
-      bool some;                       // only some rows may see them all
-      uint32_t ks, vs;
-    } a[DEPTH];
-    int pages = -1, batch = 0;
-    auto fetch = [&]() {
-      batch = at.blk;
-      const int b = at.blk + lane;
-      pages = b < at.it.nblk ? kv_page(p.q, p.c.pages, at.it.b, at.it.blk0 + b) : -1;
-    };
-    fetch();
-    auto load = [&](int d) {
-      if (at.left == 0) return;
-      if (at.blk >= batch + 32) fetch();
-      Ahead& x = a[d];
-      x.page = __shfl_sync(0xFFFFFFFFu, pages, at.blk - batch);
-      x.head = at.head;
-      x.base = (at.it.blk0 + at.blk) * 64;
-      x.from = max(at.it.lo - x.base, 0);
-      x.to = min(at.it.hi - x.base, 64);
-      const int i0 = at.it.r0 / p.group, i1 = (at.it.r0 + at.it.rows - 1) / p.group;
-      x.some = i1 > i0 && (x.base + 64 > (p.causal ? at.it.p0 + i0 + 1 : at.it.len) ||
-                           (p.window > 0 && x.base < at.it.p0 + i1 - p.window + 1));
-      if (x.page >= 0) {
-        const int64_t ph = (int64_t)x.page * p.c.heads + at.head;
-        const uint8_t* kp = p.c.k + ph * 64 * D + sub * 16;
-        const uint8_t* vp = p.c.v + ph * 64 * D + sub * 16;
-        // piece i of the warp: keys: positions 8 (i % 2 + 2 cw) .., dims 64 (i / 2) ..; values: dims 8 (4 i + cw) ..
-#pragma unroll
-        for (int i = 0; i < N; ++i) k[d][i] = ldg_codes(kp + (8 * ((i & 1) + 2 * cw) + row8) * D + 64 * (i >> 1));
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[d][i] = ldg_codes(vp + (8 * (4 * i + cw) + row8) * 64);
-        x.ks = p.c.ks[ph];
-        x.vs = p.c.vs[ph];
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) k[d][i] = v[d][i] = make_uint4(0, 0, 0, 0);
-        x.ks = x.vs = 127;
-      }
-      const int item = at.item;
-      if (at.advance(pl, p.c.heads, 1) && (batch != 0 || at.item != item)) fetch();
-    };
-    int64_t todo = at.left;
-    load(0);
-    load(1);
-    RingPos r{0, 0};
-    auto convert = [&](int d) {
-      Ahead& x = a[d];
+    regs_down<kRegsRest<D>>();
+    const int cw = warp - kConv, sub = lane & 3, row8 = lane >> 2;
+    RingPos r{0, 0}, in{0, 0};
+    for (int64_t todo = dealt.start(me + 1) - dealt.start(me); todo > 0; --todo) {
+      mbar_wait(smem_u32(&in_b[in.slot]), in.phase, err, kErrFullWait);
+      const SlotInfo si = slot_info[in.slot];
       mbar_wait(smem_u32(&empty_b[r.slot]), r.phase ^ 1u, err, kErrEmptyWait);
+      const uint32_t kc = codes + in.slot * kSlotBytes<D> + sub * 16, vc = kc + 64 * D;
       const uint32_t kb = ring + r.slot * kStageBytesKv<D>, vb = kb + 64 * D * 2;
-      if (ct == 0) {
-        info[r.slot].ek = x.page >= 0 ? kv_exp(x.ks) : kNoPage;
-        info[r.slot].ev = kv_exp(x.vs);
-        info[r.slot].nan[0] = info[r.slot].nan[1] = 0;
+      const bool plain = si.from <= 0 && si.to >= 64 && !si.some;
+      if (warp == kConv && lane == 0) info[r.slot] = PageInfo{{0u, 0u}};
+      // Keys: a warp takes 8 positions x 64 dims at a time, values 8 dims x 64 positions: 8 lanes read 128 bytes of
+      // different banks and write 128 bytes of different banks (of two rows; of two blocks of 64 dims where the
+      // rows lie a multiple of 128 bytes apart).
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int row = 8 * (cw + 4 * (i & 1)) + row8;
+        const int blk = D % 128 == 0 ? (i >> 1) ^ (row8 & 1) : i >> 1;
+        store16_f16(kb + blk * 8192 + row * 128, row8, sub, lds128(kc + row * D + blk * 64));
       }
-      if (x.from > 0 || x.to < 64 || x.some) {
-        // what no row sees is not looked at; a NaN that only some rows see reaches those by their weight
+      if (plain) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const int row = 8 * (4 * i + cw) + row8;
+          store16_f16(vb + row * 128, row8, sub, lds128(vc + row * 64));
+        }
+      } else {
+        // what no row sees is not looked at; a NaN that only some rows see reaches those by their weights
         uint32_t keep[4], nan[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -300,84 +364,60 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int pos = 16 * sub + 4 * j + q;
-            if (pos >= x.from && pos < x.to) keep[j] |= 0xFFu << (8 * q);
+            if (pos >= si.from && pos < si.to) keep[j] |= 0xFFu << (8 * q);
           }
         }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(&v[d][i]);
+#pragma unroll 1
+        for (int i = 0; i < D / 32; ++i) {
+          const int row = 8 * (4 * i + cw) + row8;
+          const uint4 v = lds128(vc + row * 64);
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             w[j] &= keep[j];
-            if (x.some) {
+            if (si.some) {
               const uint32_t bad = ((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
               nan[j] |= bad;
               w[j] &= ~((bad >> 7) * 0xFFu);
             }
           }
+          store16_f16(vb + row * 128, row8, sub, make_uint4(w[0], w[1], w[2], w[3]));
         }
-        // 16 positions of this lane as bits; then those of the warp
-        uint32_t bits = 0;
+        if (si.some) {
+          // 16 positions of this lane as bits; then those of the warp
+          uint32_t bits = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) bits |= (nan[j] >> (8 * q + 7) & 1u) << (4 * j + q);
-        bits <<= 16 * (sub & 1);
-        uint32_t lo = sub < 2 ? bits : 0u, hi = sub < 2 ? 0u : bits;
-        lo = __reduce_or_sync(0xFFFFFFFFu, lo);
-        hi = __reduce_or_sync(0xFFFFFFFFu, hi);
-        asm volatile("bar.sync 2, 128;" ::: "memory");  // the stage's bits are clear
-        if (lane == 0 && (lo | hi)) {
-          atomicOr(&info[r.slot].nan[0], lo);
-          atomicOr(&info[r.slot].nan[1], hi);
+            for (int q = 0; q < 4; ++q) bits |= (nan[j] >> (8 * q + 7) & 1u) << (4 * j + q);
+          bits <<= 16 * (sub & 1);
+          const uint32_t lo = __reduce_or_sync(0xFFFFFFFFu, sub < 2 ? bits : 0u);
+          const uint32_t hi = __reduce_or_sync(0xFFFFFFFFu, sub < 2 ? 0u : bits);
+          asm volatile("bar.sync 2, 128;" ::: "memory");  // the stage's bits are clear
+          if (lane == 0 && (lo | hi) != 0) {
+            atomicOr(&info[r.slot].nan[0], lo);
+            atomicOr(&info[r.slot].nan[1], hi);
+          }
         }
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int row = 8 * ((i & 1) + 2 * cw) + row8;
-        const uint32_t w[4] = {k[d][i].x, k[d][i].y, k[d][i].z, k[d][i].w};
-        uint32_t h[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) e4m3x4_f16x4(w[j], h[2 * j], h[2 * j + 1]);
-        const uint32_t o = kb + (i >> 1) * 8192 + row * 128;
-        sts128(o + (((2 * sub) ^ row8) << 4), h[0], h[1], h[2], h[3]);
-        sts128(o + (((2 * sub + 1) ^ row8) << 4), h[4], h[5], h[6], h[7]);
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int row = 8 * (4 * i + cw) + row8;
-        const uint32_t w[4] = {v[d][i].x, v[d][i].y, v[d][i].z, v[d][i].w};
-        uint32_t h[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) e4m3x4_f16x4(w[j], h[2 * j], h[2 * j + 1]);
-        const uint32_t o = vb + row * 128;
-        sts128(o + (((2 * sub) ^ row8) << 4), h[0], h[1], h[2], h[3]);
-        sts128(o + (((2 * sub + 1) ^ row8) << 4), h[4], h[5], h[6], h[7]);
       }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&full_b[r.slot]));
-      r.advance(1, NS);
-    };
-    while (todo > 0) {
-#pragma unroll
-      for (int d = 0; d < DEPTH; ++d) {
-        if (todo > 0) {
-          convert(d);
-          load(d);
-          --todo;
-        }
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&full_b[r.slot]));
+        mbar_arrive(smem_u32(&out_b[in.slot]));
       }
+      r.advance(1, NS);
+      in.advance(1, NC);
     }
   } else {
     // ------------------------------------------------------ softmax
     regs_up<kRegsSoft<D>>();
     Walk<R> at = walk_of<R>(pl, dealt, sh, p.c.heads, me, 0);
-    const int x = warp >> 2;                             // the group
+    const int x = (warp - kSoft) >> 2;                   // the tile
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tq = tmem + lanes + x * C::kQ, to = tmem + lanes + C::kO + x * D;
+    const uint32_t tq = lanes + x * C::kQ, to = lanes + C::kO + x * D;
     const int in_tile = (warp & 3) * 32 + lane;
-    uint32_t done[2] = {0, 0};                           // pages of each score buffer so far
+    uint32_t done0 = 0, done1 = 0;                       // pages of the buffers so far (NG = 2: of the tile's)
     RingPos r{0, 0};
     while (at.left > 0) {
       const Item& it = at.it;
@@ -437,21 +477,33 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
       float m = -INFINITY, M = -INFINITY, l = 0.0f;
       const int step = split ? 2 : 1, first = split ? x : 0;
       if (split && x == 1) r.advance(1, NS);
+      // the scales of 32 pages, one a lane: the keys' exponent in the low half (kNoPage: no page)
+      int scales = 0, batch = first - 32;
 #pragma unroll 1
       for (int c = first; c < cnt; c += step) {
-        const int buf = NG == 2 ? x : c & 1;
-        const uint32_t ts = tmem + lanes + C::kS + 64 * buf;
-        mbar_wait_warp(smem_u32(&full_b[r.slot]), r.phase, err, kErrFullWait);
-        const PageInfo& pg = info[r.slot];
-        const int ek = pg.ek, base = (it.blk0 + at.blk + c) * 64;
-        const float ev = (float)pg.ev;
+        if (c >= batch + 32) {
+          batch = c;
+          const int b = at.blk + c + lane;
+          const int pg = b < it.nblk ? kv_page(p.q, p.c.pages, it.b, it.blk0 + b) : -1;
+          const int64_t ph = (int64_t)pg * p.c.heads + head;
+          scales = pg >= 0 ? (kv_exp(p.c.vs[ph]) << 16) | (kv_exp(p.c.ks[ph]) & 0xFFFF) : kNoPage;
+        }
+        const int sc = __shfl_sync(0xFFFFFFFFu, scales, c - batch), ek = (int16_t)sc;
+        const int base = (it.blk0 + at.blk + c) * 64;
         const bool there = ek != kNoPage;
+        const float ev = (float)(sc >> 16);
         const float f = qs * pow2i(there ? ek : 0);
         const bool edge = !there || base < all_lo || base + 64 > all_hi;
         uint32_t nan[2] = {0, 0};
-        if (edge) nan[0] = pg.nan[0], nan[1] = pg.nan[1];
-        mbar_wait_warp(smem_u32(&s_b[buf]), done[buf] & 1, err, kErrStatsWait);
-        ++done[buf];
+        if (edge) {
+          mbar_wait(smem_u32(&full_b[r.slot]), r.phase, err, kErrFullWait);
+          nan[0] = info[r.slot].nan[0];
+          nan[1] = info[r.slot].nan[1];
+        }
+        const int buf = NG == 2 ? x : c & 1;
+        const uint32_t ts = lanes + C::kS + 64 * buf;
+        mbar_wait(smem_u32(&s_b[buf]), (NG == 2 || buf == 0 ? done0 : done1) & 1, err, kErrStatsWait);
+        __syncwarp();
         tc_fence_after();
         float s[64];
         tmem_load32(ts, reinterpret_cast<float(&)[32]>(s));
@@ -476,9 +528,12 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
             s[i] = z;
           }
         }
-        float top = s[0];
+        float top4[4];
 #pragma unroll
-        for (int i = 1; i < 64; ++i) top = fmaxf(top, s[i]);
+        for (int i = 0; i < 4; ++i) top4[i] = max_of3(s[3 * i], s[3 * i + 1], s[3 * i + 2]);
+#pragma unroll
+        for (int i = 12; i < 64; i += 2) top4[i / 2 & 3] = max_of3(top4[i / 2 & 3], s[i], s[i + 1]);
+        float top = fmaxf(max_of3(top4[0], top4[1], top4[2]), top4[3]);
         if (top != top) top = -INFINITY;  // NaN everywhere: the weights carry it
         top *= mul;
         const float m2 = fmaxf(m, top);
@@ -487,10 +542,11 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
         if (__any_sync(0xFFFFFFFFu, raise)) {
           const float M2 = raise ? top + ev : M;
           if (c != first) {
-            // The output holds the pages before: two groups ask for a page's scores after its own page
-            // before has been added; one group, only after the one before that.
+            // The output holds the pages before: with two tiles, a page's scores were asked for after the tile's page
+            // before had been added; with one, after the one before that.
             if constexpr (NG == 1)
-              mbar_wait_warp(smem_u32(&o_b[buf ^ 1]), (done[buf ^ 1] - 1) & 1, err, kErrStatsWait);
+              mbar_wait(smem_u32(&o_b[buf ^ 1]), ((buf == 0 ? done1 : done0) - 1) & 1, err, kErrStatsWait);
+            __syncwarp();
             tc_fence_after();
             const float shrink = raise ? ex2(M - M2) : 1.0f;
 #pragma unroll 1
@@ -507,23 +563,31 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
           }
           M = M2;
         }
-        const float sub = M == -INFINITY ? 0.0f : M - ev;  // 2^sub: the unit of this page's weights
-        float sum0 = 0.0f, sum1 = 0.0f;
+        // 2^sub: the unit of this page's weights.  Where the values are so small that no weight reaches f16, a finer
+        // one, in which the sum of the weights loses nothing.
+        const float sub = top == -INFINITY ? 0.0f : fminf(M - ev, top + 90.0f);
         uint32_t w[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float a = ex2(fmaf(s[2 * i], mul, -sub)), b = ex2(fmaf(s[2 * i + 1], mul, -sub));
-          sum0 += a;
-          sum1 += b;
-          w[i] = pack_f16x2(a, b);
+          const float2 z = fma2(make_float2(s[2 * i], s[2 * i + 1]), splat2(mul), splat2(-sub));
+          s[2 * i] = ex2(z.x);
+          s[2 * i + 1] = ex2(z.y);
+          w[i] = pack_f16x2(s[2 * i], s[2 * i + 1]);
         }
         tmem_store32(ts, w);
-        l = l * ex2(m - base_m) + (sum0 + sum1) * ex2(fminf(sub - base_m, 126.0f));
-        m = m2;
         tmem_store_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&p_b[buf]));
+        if (NG == 2 || buf == 0) ++done0;
+        else ++done1;
+        // the sum is not waited for
+        float2 sum[4] = {};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[i & 3] = add2(sum[i & 3], make_float2(s[2 * i], s[2 * i + 1]));
+        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l = l * ex2(m - base_m) + (sum[0].x + sum[0].y) * ex2(fminf(sub - base_m, 126.0f));
+        m = m2;
         r.advance(step, NS);
       }
       // the stages of the other group's last pages
@@ -542,9 +606,11 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
       }
 
       // ---------------------------------------------------- the segment's end
-      const bool any = !split || x < cnt;
-      const int last = NG == 2 ? x : (cnt - 1) & 1;
-      if (any) mbar_wait_warp(smem_u32(&o_b[last]), (done[last] - 1) & 1, err, kErrStatsWait);
+      if (!split || x < cnt) {
+        const int b = NG == 2 ? x : (cnt - 1) & 1;
+        mbar_wait(smem_u32(&o_b[b]), ((NG == 2 || b == 0 ? done0 : done1) - 1) & 1, err, kErrStatsWait);
+      }
+      __syncwarp();
       tc_fence_after();
       float mo = -INFINITY, Mo = -INFINITY, lo = 0.0f;   // of the odd pages
       if (split) {
@@ -595,7 +661,7 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
         }
       }
       tc_fence_before();
-      if (at.left == cnt && tid == 0)
+      if (at.left == cnt && warp == kSoft && lane == 0)
         desc[me] = desc_of(dealt, me, begins && !ends ? dealt.start(me + 1) + (it.nblk - at.blk - cnt) : 0, at.item,
                            it.rows, head);
       at.advance(pl, p.c.heads, cnt);
@@ -604,12 +670,12 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMma) tmem_free1(tmem);
+  if (warp == kMma) tmem_free1(tmem_at);
 }
 
 template <int D, bool EXTRA>
 rn_status launch_e(const KvAttnParams& p, int sms, cudaStream_t s) {
-  constexpr size_t smem = (size_t)kStagesKv<D> * kStageBytesKv<D> + 1024;
+  constexpr size_t smem = (size_t)kStagesKv<D> * kStageBytesKv<D> + (size_t)kSlotsKv<D> * kSlotBytes<D> + 1024;
   auto k = rn_kv_tile_kernel<D, EXTRA>;
   static std::atomic<int> kept[kMaxDevices];
   if (once_per_device(kept, [&] {
