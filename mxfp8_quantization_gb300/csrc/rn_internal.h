@@ -223,12 +223,24 @@ struct KvReadParams {
   void* k;                // [tokens, heads, dim]
   void* v;
 };
+// n / d for 0 <= n < 2^31 by a product: with 2^(s-1) < d <= 2^s, mul = ceil(2^(31 + s) / d) is below 2^32 and off by
+// less than 1, which makes the quotient wrong by less than n / 2^(31 + s) < 1 / d
+struct FastDiv {
+  uint32_t mul;
+  int shift;            // of the product's upper half
+  int d;
+};
+inline FastDiv fast_div(int d) {
+  int s = 0;
+  while ((int64_t(1) << s) < d) ++s;
+  return FastDiv{(uint32_t)(((uint64_t(1) << (31 + s)) + d - 1) / d), s - 1, d};
+}
 struct KvAttnParams {
   KvCache c;
   KvSeqs q;
   const void* x;          // queries, bf16 [tokens, heads * group, dim], rows `stride` elements apart
   int64_t stride;
-  int group;              // query heads of a key/value head
+  FastDiv group;          // query heads of a key/value head
   float scale;
   int causal;
   int window;             // 0: none

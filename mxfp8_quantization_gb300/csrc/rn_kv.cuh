@@ -28,6 +28,11 @@ __device__ __forceinline__ int kv_exp_of(uint32_t amax_bits) {
   return min(max(e, kKvExpMin), kKvExpMax);
 }
 
+// (d = 1: the product is n 2^31, its shift 31)
+__device__ __forceinline__ int quot(int n, const FastDiv& f) {
+  return f.shift < 0 ? n : (int)(__umulhi((uint32_t)n, f.mul) >> f.shift);
+}
+
 // rows [s0, s1) of sequence b, whatever the caller's array holds
 struct KvRows {
   int s0, s1;

@@ -99,7 +99,7 @@ rn_status rn_kv_attention(const void* q, rn_dtype dtype, int64_t q_stride, int64
       !(softcap >= 0.0f) || softcap > 1e30f)
     return RN_ERR_INVALID;
   const int64_t group = q_heads / p.c.heads;
-  if (dtype != RN_BF16 || group > 4096 || p.q.tokens * group / 8 + p.q.B > INT32_MAX / 2) return RN_ERR_UNSUPPORTED;
+  if (dtype != RN_BF16 || group > 4096 || p.q.tokens * group > INT32_MAX / 2) return RN_ERR_UNSUPPORTED;
   const size_t need = kv_attn_bytes((int)cache->dim);
   if (workspace == nullptr && out == nullptr) {
     if (workspace_bytes == nullptr) return RN_ERR_INVALID;
@@ -118,7 +118,7 @@ rn_status rn_kv_attention(const void* q, rn_dtype dtype, int64_t q_stride, int64
   if (!any) return RN_OK;
   p.x = q;
   p.stride = q_stride;
-  p.group = (int)group;
+  p.group = fast_div((int)group);
   p.scale = scale;
   p.causal = causal != 0;
   p.window = window > INT32_MAX / 2 ? 0 : (int)window;  // no position is that far away

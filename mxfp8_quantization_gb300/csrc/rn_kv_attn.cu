@@ -28,11 +28,14 @@
 //
 // A worker is one warp with a ring of slots of its own, filled by bulk copies
 // of whole pages (keys and values of 64 positions are contiguous, 64 dim
-// bytes each).  The (row tile, head, page) triples of the call, in this order,
-// are dealt evenly to all workers, so ragged lengths cost nothing; a (row
-// tile, head) that several workers share is joined from their partial results
-// by a second kernel, in the workers' order.
+// bytes each; half pages where dim > 128).  The (row tile, head, page) triples of
+// the call, in this order, are dealt evenly to all workers, so ragged lengths
+// cost nothing.  A (row tile, head) that several workers share is joined from
+// their partial results in the workers' order: by their CTA, and where it goes
+// beyond one CTA, by a second kernel.
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "rn_device.cuh"
 #include "rn_internal.h"
@@ -44,11 +47,16 @@ namespace {
 
 __device__ unsigned g_err_kv;
 
-// warps of a CTA and slots of a warp: 192 KB of slots an SM
+// A CTA's warps have 192 KB of slots, each of a page's keys or values, or half of
+// them (dim > 128: positions 0 .. 31 and 32 .. 63 of the keys, the dims' halves of
+// the values).
+constexpr int kWarps = 8;
 template <int D>
-constexpr int kWarps = D <= 128 ? 8 : 4;
+constexpr int kHalves = D > 128 ? 2 : 1;
 template <int D>
-constexpr int kSlots = 196608 / (kWarps<D> * 64 * D);
+constexpr int kPiece = 64 * D / kHalves<D>;
+template <int D>
+constexpr int kSlots = 196608 / (kWarps * kPiece<D>);
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -98,12 +106,126 @@ __device__ __forceinline__ uint32_t byte_range(int from, int to) {
   return m;
 }
 
+// A row put together from partial results, which are normalized: the weighted
+// mean and the log2 of the weights' sum (-infinity: none).  Lane i holds the dims
+// 2 i + 64 c and the one behind.
+template <int D>
+struct Joined {
+  float2 acc[D / 64];
+  float top, sum;
+};
+
+// parts i0, i0 + step .. of n, each R rows of D and then the rows' log2 sums
+template <int D, class Part>
+__device__ __forceinline__ Joined<D> join_parts(int n, int i0, int step, int lane, int row, int R, Part part) {
+  Joined<D> j;
+  j.top = -INFINITY;
+  for (int i = i0 + lane * step; i < n; i += 32 * step) j.top = fmaxf(j.top, part(i)[R * D + row]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) j.top = fmaxf(j.top, __shfl_xor_sync(0xFFFFFFFFu, j.top, o));
+  const float top = j.top == -INFINITY ? 0.0f : j.top;
+  j.sum = 0.0f;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) j.acc[c] = make_float2(0.0f, 0.0f);
+#pragma unroll 8
+  for (int i = i0; i < n; i += step) {
+    const float* at = part(i);
+    const float w = ex2(at[R * D + row] - top);
+    j.sum += w;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      const float2 v = *reinterpret_cast<const float2*>(at + row * D + c * 64 + 2 * lane);
+      j.acc[c].x = fmaf(w, v.x, j.acc[c].x);
+      j.acc[c].y = fmaf(w, v.y, j.acc[c].y);
+    }
+  }
+  const float inv = j.sum == 0.0f ? 0.0f : 1.0f / j.sum;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) j.acc[c] = make_float2(j.acc[c].x * inv, j.acc[c].y * inv);
+  j.top = j.sum == 0.0f ? -INFINITY : top + log2f(j.sum);
+  return j;
+}
+// the row as a partial result again
+template <int D>
+__device__ __forceinline__ void store_part(const Joined<D>& j, float* part, int row, int R, int lane) {
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) *reinterpret_cast<float2*>(part + row * D + c * 64 + 2 * lane) = j.acc[c];
+  if (lane == 0) part[R * D + row] = j.top;
+}
+template <int D>
+__device__ __forceinline__ void store_joined(const KvAttnParams& p, const Joined<D>& j, int64_t row, int lane) {
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D);
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) out[c * 32 + lane] = pack_bf16x2(j.acc[c].x, j.acc[c].y);
+  if (p.lse != nullptr && lane == 0) p.lse[row] = j.top * kLn2;
+}
+
+// Rows row0 .. row0 + RB - 1 of n parts at once, for one warp: the loads of a part's rows are on their way together.
+template <int D, int RB, class Part, class Store>
+__device__ __forceinline__ void join_rows(int n, int lane, int row0, int rows, int R, Part part, Store store) {
+  float2 acc[RB][D / 64];
+  float top[RB], sum[RB];
+#pragma unroll
+  for (int k = 0; k < RB; ++k) {
+    top[k] = -INFINITY;
+    sum[k] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) acc[k][c] = make_float2(0.0f, 0.0f);
+  }
+  for (int i = 0; i < n; ++i) {
+    const float* at = part(i);
+    float2 v[RB][D / 64];
+    float l[RB];
+#pragma unroll
+    for (int k = 0; k < RB; ++k) {
+      const int row = min(row0 + k, rows - 1);
+      l[k] = at[R * D + row];
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) v[k][c] = *reinterpret_cast<const float2*>(at + row * D + c * 64 + 2 * lane);
+    }
+#pragma unroll
+    for (int k = 0; k < RB; ++k) {
+      const float now = fmaxf(top[k], l[k]), base = now == -INFINITY ? 0.0f : now;
+      const float keep = ex2(top[k] - base), w = ex2(l[k] - base);
+      top[k] = now;
+      sum[k] = fmaf(sum[k], keep, w);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        acc[k][c].x = fmaf(acc[k][c].x, keep, w * v[k][c].x);
+        acc[k][c].y = fmaf(acc[k][c].y, keep, w * v[k][c].y);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < RB; ++k) {
+    if (row0 + k >= rows) break;
+    Joined<D> j;
+    const float inv = sum[k] == 0.0f ? 0.0f : 1.0f / sum[k];
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) j.acc[c] = make_float2(acc[k][c].x * inv, acc[k][c].y * inv);
+    j.top = sum[k] == 0.0f ? -INFINITY : top[k] + log2f(sum[k]);
+    store(row0 + k, j);
+  }
+}
+
+constexpr int kNoScales = 256;  // no page
+
+// what the join within the CTA has to know of a worker's range
+struct WorkerEnd {
+  int within, closes;        // it begins within a (row tile, head), and holds its last page
+  int opens;                 // it begins one that it does not finish
+  int item, rows, head;      // of that one; of the first where it begins none
+  int64_t end;               // where its pages end
+  int item0, rows0, head0;   // the one that it begins within
+};
+
 template <int D, int NB, bool EXTRA>
-__global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvAttnParams p, int items) {
-  constexpr int R = 8 * NB, W = kWarps<D>, S = kSlots<D>, SLOT = 64 * D;
+__global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttnParams p, int items) {
+  constexpr int R = 8 * NB, W = kWarps, S = kSlots<D>, PIECE = kPiece<D>, PH = kHalves<D>;
   extern __shared__ __align__(1024) unsigned char raw[];
   __shared__ __align__(8) uint64_t full_b[W][S];
   __shared__ Ranges<W, W> sh;
+  __shared__ WorkerEnd ends_of[W];
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   if (lane == 0) {
@@ -117,71 +239,85 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
   const Dealt dealt = deal_pages<R, W, 32 * W>(p, items, sh, pl);
   const int me = (int)blockIdx.x * dealt.per_cta + warp;
   Desc* desc = static_cast<Desc*>(p.ws);
-  if (warp >= dealt.per_cta || me >= dealt.workers) {  // no worker
-    const int rest = W - dealt.per_cta;
-    if (lane == 0)
-      desc[warp < dealt.per_cta ? me : (int)gridDim.x * dealt.per_cta + (int)blockIdx.x * rest + warp - dealt.per_cta]
-          .parts = 0;
-    return;
+  if (me >= dealt.workers && warp == 0) {  // nothing for this CTA
+    if (lane == 0) desc[blockIdx.x].parts = 0;
+    return;  // as its other warps do, below
   }
-  const uint32_t ring = smem_u32(raw) + warp * (S * SLOT);
+  if ((int)blockIdx.x * dealt.per_cta >= dealt.workers) return;
+  const bool works = warp < dealt.per_cta && me < dealt.workers;
+  const uint32_t ring = smem_u32(raw) + warp * (S * PIECE);
   auto bar = [&](int s) { return smem_u32(&full_b[warp][s]); };
 
   // ------------------------------------------------------------- copies
-  // page numbers are read 32 at a time, one a lane
-  Walk<R> ld = walk_of<R>(pl, dealt, sh, p.c.heads, me, warp);
+  // Page numbers are read 32 at a time, one a lane, and the next ones while these are used; the scales of a slot's
+  // page are in the lane with the slot's number.
+  Walk<R> ld{};
+  if (works) ld = walk_of<R>(pl, dealt, sh, p.c.heads, me, warp);
   Walk<R> at = ld;
-  int pages = -1, batch = 0;
-  auto fetch = [&]() {
-    batch = ld.blk;
-    const int b = ld.blk + lane;
-    pages = b < ld.it.nblk ? kv_page(p.q, p.c.pages, ld.it.b, ld.it.blk0 + b) : -1;
+  int pages = -1, pages_next = -1, batch = 0, ks = 0, vs = 0;
+  auto read_pages = [&](const Item& it, int blk) {
+    const int b = blk + lane;
+    return b < it.nblk ? kv_page(p.q, p.c.pages, it.b, it.blk0 + b) : -1;
   };
-  fetch();
-  uint32_t slot_l = 0;
-  int ld_page = -1;
-  bool ld_v = false;
-  // the scale bytes of the last two pages begun: lane 0 the keys', lane 1 the values'
-  uint32_t sc_new = 0, sc_cur = 0;
-  // begins the copy of the next page's keys, or values
-  auto issue = [&]() {
-    if (!ld_v) {
-      if (ld.left == 0) return;
-      if (ld.blk >= batch + 32) fetch();
-      ld_page = __shfl_sync(0xFFFFFFFFu, pages, ld.blk - batch);
+  // a batch begins at the cursor: asks for the one behind it
+  auto look_ahead = [&]() {
+    batch = ld.blk;
+    if (batch + 32 < ld.it.nblk) {
+      pages_next = read_pages(ld.it, batch + 32);
+    } else {
+      Walk<R> next = ld;
+      if (next.advance(pl, p.c.heads, next.segment())) pages_next = read_pages(next.it, 0);
     }
+  };
+  if (works) {
+    pages = read_pages(ld.it, ld.blk);
+    look_ahead();
+  }
+  uint32_t slot_l = 0;
+  int piece = 0, ld_page = -1;   // the next piece of the page: keys, then values
+  auto issue = [&]() {
+    if (ld.left == 0) return;
+    if (piece == 0) ld_page = __shfl_sync(0xFFFFFFFFu, pages, ld.blk - batch);
+    // a page that is none is masked: any other stands for it
     const int64_t ph = (int64_t)max(ld_page, 0) * p.c.heads + ld.head;
     if (lane == 0) {
-      mbar_arrive_expect_tx(bar(slot_l), SLOT);
-      bulk_g2s(ring + slot_l * SLOT, (ld_v ? p.c.v : p.c.k) + ph * SLOT, SLOT, bar(slot_l));
+      const uint8_t* from = (piece < PH ? p.c.k : p.c.v) + ph * 64 * D + (piece % PH) * PIECE;
+      mbar_arrive_expect_tx(bar(slot_l), PIECE);
+      bulk_g2s(ring + slot_l * PIECE, from, PIECE, bar(slot_l));
     }
-    if (!ld_v) {
-      // 256: no page
-      sc_new = 256;
-      if (ld_page >= 0 && lane < 2) sc_new = lane == 0 ? p.c.ks[ph] : p.c.vs[ph];
-    } else {
-      const int item = ld.item;
-      if (ld.advance(pl, p.c.heads, 1) && (batch != 0 || ld.item != item)) fetch();
+    if (piece == 0 && lane == slot_l) {
+      ks = ld_page >= 0 ? (int)p.c.ks[ph] : kNoScales;
+      vs = p.c.vs[ph];
     }
-    ld_v = !ld_v;
     if (++slot_l == S) slot_l = 0;
+    if (++piece == 2 * PH) {
+      piece = 0;
+      if (ld.advance(pl, p.c.heads, 1) || ld.blk == batch + 32) {
+        pages = pages_next;
+        look_ahead();
+      }
+    }
   };
-  // two or more slots ahead; the scales of a page are read while the one before is worked on
 #pragma unroll 1
-  for (int i = 0; i < 2; ++i) issue();
+  for (int i = 0; i < S; ++i) issue();
+  __syncwarp();
 
   // ------------------------------------------------------------- the pages
-  uint32_t slot_c = 0, phase = 0;
-  int ahead = 2;   // slots begun and not yet worked on
-  auto wait_slot = [&]() { mbar_wait(bar(slot_c), phase, &g_err_kv, kErrFullWait); };
-  auto free_slot = [&]() {
-    __syncwarp();
-    if (++slot_c == S) {
-      slot_c = 0;
-      phase ^= 1;
+  RingPos r{0, 0};
+  auto wait_slots = [&](int n) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const RingPos a = r.ahead(i, S);
+      mbar_wait(bar(a.slot), a.phase, &g_err_kv, kErrFullWait);
     }
-    --ahead;
   };
+  auto free_slots = [&](int n) {
+    __syncwarp();
+    r.advance(n, S);
+#pragma unroll
+    for (int i = 0; i < n; ++i) issue();
+  };
+  if (lane == 0) ends_of[warp] = WorkerEnd{};
   while (at.left > 0) {
     const Item& it = at.it;
     const int head = at.head, blk = at.blk;
@@ -195,13 +331,13 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
     int row_p[NB][2];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      const int r = it.r0 + n * 8 + g;
+      const int r = it.r0 + n * 8 + g, qi = quot(r, p.group);
       const bool real = n * 8 + g < it.rows;
       uint4 raw4[D / 64][2];
       uint32_t big = 0;
       const unsigned char* src =
           static_cast<const unsigned char*>(p.x) +
-          ((int64_t)(it.s0 + r / p.group) * p.stride + (int64_t)(head * p.group + r % p.group) * D + 16 * t) * 2;
+          ((int64_t)(it.s0 + qi) * p.stride + (int64_t)(head * p.group.d + r - qi * p.group.d) * D + 16 * t) * 2;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
 #pragma unroll
@@ -234,16 +370,17 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         qs[n][j] = __shfl_sync(0xFFFFFFFFu, own, (2 * t + j) * 4);
-        const int rr = it.r0 + min(n * 8 + 2 * t + j, it.rows - 1), i = rr / p.group;
+        const int rr = it.r0 + min(n * 8 + 2 * t + j, it.rows - 1), i = quot(rr, p.group);
         row_p[n][j] = it.p0 + i;
         row_hi[n][j] = p.causal ? row_p[n][j] + 1 : it.len;
         row_lo[n][j] = p.window > 0 ? row_p[n][j] - p.window + 1 : 0;
         if constexpr (EXTRA)
-          slope[n][j] = p.slopes != nullptr ? __ldg(p.slopes + head * p.group + rr % p.group) * kLog2e : 0.0f;
+          slope[n][j] =
+              p.slopes != nullptr ? __ldg(p.slopes + head * p.group.d + rr - i * p.group.d) * kLog2e : 0.0f;
       }
     }
     // every row sees [all_lo, all_hi)
-    const int i0 = it.r0 / p.group, i1 = (it.r0 + it.rows - 1) / p.group;
+    const int i0 = quot(it.r0, p.group), i1 = quot(it.r0 + it.rows - 1, p.group);
     const int all_hi = p.causal ? it.p0 + i0 + 1 : it.len;
     const int all_lo = p.window > 0 ? it.p0 + i1 - p.window + 1 : 0;
     const bool several = i1 > i0;
@@ -261,15 +398,10 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
 
 #pragma unroll 1
     for (int c = 0; c < cnt; ++c) {
-      // keep the ring full: this page's slots, then the next pages'
-      sc_cur = sc_new;
       const int base = (it.blk0 + blk + c) * 64;
-      const uint32_t kbyte = __shfl_sync(0xFFFFFFFFu, sc_cur, 0), vbyte = __shfl_sync(0xFFFFFFFFu, sc_cur, 1);
-      const bool there = kbyte < 256;
-      if (ahead < S && (ld.left > 0 || ld_v)) {
-        issue();
-        ++ahead;
-      }
+      wait_slots(PH);
+      const int kbyte = __shfl_sync(0xFFFFFFFFu, ks, r.slot), vbyte = __shfl_sync(0xFFFFFFFFu, vs, r.slot);
+      const bool there = kbyte != kNoScales;
       // positions of the page that any row sees
       const int from = there ? max(it.lo - base, 0) : 64, to = there ? min(it.hi - base, 64) : 0;
       const bool edge = !there || base < all_lo || base + 64 > all_hi;
@@ -281,9 +413,11 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
         for (int st = 0; st < 4; ++st)
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[n][st][i] = 0.0f;
-      wait_slot();
       {
-        const uint32_t at = ring + slot_c * SLOT + (16 * (g >> 1) + (g & 1)) * D + 16 * t;
+        // dim > 128: the positions 16 (g / 2) .. of lanes g >= 4 are in the second slot
+        const int key = 16 * (g >> 1) + (g & 1);
+        const uint32_t from_slot = PH == 1 ? r.slot : (g < 4 ? r.slot : r.ahead(1, S).slot);
+        const uint32_t at = ring + from_slot * PIECE + (PH == 1 ? key : key & 31) * D + 16 * t;
 #pragma unroll
         for (int st = 0; st < 4; ++st)
 #pragma unroll
@@ -300,14 +434,10 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
             }
           }
       }
-      free_slot();
-      if (ld.left > 0 || ld_v) {
-        issue();
-        ++ahead;
-      }
+      free_slots(PH);
 
       // scores in base 2, maxima, weights
-      const float ek = pow2i(there ? kv_exp(kbyte) : 0), ev = there ? (float)kv_exp(vbyte) : 0.0f;
+      const float unit = pow2i(there ? kv_exp(kbyte) : 0), ev = (float)kv_exp(vbyte);
       uint32_t pw[NB][4][2];
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
@@ -317,7 +447,7 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = i & 1, pos = base + 16 * (g >> 1) + 4 * st + 2 * (i >> 1) + (g & 1);
-            float z = s[n][st][i] * (qs[n][j] * ek);
+            float z = s[n][st][i] * (qs[n][j] * unit);
             if constexpr (EXTRA) {
               if (p.softcap > 0.0f) z = capped(z, p.softcap, 2.0f * kLog2e / p.softcap);
               z = fmaf(slope[n][j], (float)(pos - row_p[n][j]), z * kLog2e);
@@ -359,16 +489,60 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
         }
       }
 
-      wait_slot();
-      {
-        const uint32_t at = ring + slot_c * SLOT + g * 64 + 16 * t;
-        if (!edge) {
+      uint32_t keep[4];
+      if (edge) {
+        // what no row sees is not looked at: those codes may be anything
 #pragma unroll
-          for (int d = 0; d < D / 16; ++d) {
-            const uint4 v0 = lds128(at + d * 1024), v1 = lds128(at + d * 1024 + 512);
-            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+        for (int st = 0; st < 4; ++st) keep[st] = byte_range(from - 16 * t - 4 * st, to - 16 * t - 4 * st);
+        if (several) {
+          // a NaN that only some rows see: those get it by their weight
+          wait_slots(PH);
+          uint32_t nan[4] = {0, 0, 0, 0};
+#pragma unroll 1
+          for (int d = 0; d < D / 8; ++d) {
+            const uint32_t slot = PH == 1 || d < D / 16 ? r.slot : r.ahead(1, S).slot;
+            const uint4 v0 = lds128(ring + slot * PIECE + (PH == 1 ? d : d % (D / 16)) * 512 + g * 64 + 16 * t);
+            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w};
+#pragma unroll
+            for (int st = 0; st < 4; ++st)
+              nan[st] |= ((w0[st] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u & keep[st];
+          }
+#pragma unroll
+          for (int st = 0; st < 4; ++st) {
+            nan[st] = or_g(nan[st]);
+            keep[st] &= ~((nan[st] >> 7) * 0xFFu);
+          }
+          if (__any_sync(0xFFFFFFFFu, (nan[0] | nan[1] | nan[2] | nan[3]) != 0)) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+              for (int st = 0; st < 4; ++st)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  uint32_t w = pw[n][st][h];
+                  if ((nan[st] >> (16 * h) & 0x80u) && (w & 0xFFFFu)) w |= 0x7E00u;
+                  if ((nan[st] >> (16 * h) & 0x8000u) && (w >> 16)) w |= 0x7E000000u;
+                  pw[n][st][h] = w;
+                }
+          }
+        }
+      }
+      auto add_values = [&](auto masked) {
+#pragma unroll
+        for (int part = 0; part < PH; ++part) {
+          wait_slots(1);
+          const uint32_t at = ring + r.slot * PIECE + g * 64 + 16 * t;
+#pragma unroll
+          for (int d = part * (D / 16 / PH); d < (part + 1) * (D / 16 / PH); ++d) {
+            const int off = (d - part * (D / 16 / PH)) * 1024;
+            const uint4 v0 = lds128(at + off), v1 = lds128(at + off + 512);
+            uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
             for (int st = 0; st < 4; ++st) {
+              if constexpr (decltype(masked)::value) {
+                w0[st] &= keep[st];
+                w1[st] &= keep[st];
+              }
               uint32_t a[4];
               e4m3x4_f16x4(w0[st], a[0], a[2]);
               e4m3x4_f16x4(w1[st], a[1], a[3]);
@@ -376,61 +550,18 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
               for (int n = 0; n < NB; ++n) mma_f16(o[n][d], a, pw[n][st][0], pw[n][st][1]);
             }
           }
-        } else {
-          // what no row sees is not looked at: those codes may be anything
-          uint32_t keep[4];
-#pragma unroll
-          for (int st = 0; st < 4; ++st)
-            keep[st] = byte_range(from - 16 * t - 4 * st, to - 16 * t - 4 * st);
-          if (several) {
-            // a NaN that only some rows see: those get it by their weight
-            uint32_t nan[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int d = 0; d < D / 8; ++d) {
-              const uint4 v0 = lds128(at + d * 512);
-              const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w};
-#pragma unroll
-              for (int st = 0; st < 4; ++st)
-                nan[st] |= ((w0[st] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u & keep[st];
-            }
-#pragma unroll
-            for (int st = 0; st < 4; ++st) {
-              nan[st] = or_g(nan[st]);
-              keep[st] &= ~((nan[st] >> 7) * 0xFFu);
-            }
-            if (__any_sync(0xFFFFFFFFu, (nan[0] | nan[1] | nan[2] | nan[3]) != 0)) {
-#pragma unroll
-              for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int st = 0; st < 4; ++st)
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    uint32_t w = pw[n][st][h];
-                    if ((nan[st] >> (16 * h) & 0x80u) && (w & 0xFFFFu)) w |= 0x7E00u;
-                    if ((nan[st] >> (16 * h) & 0x8000u) && (w >> 16)) w |= 0x7E000000u;
-                    pw[n][st][h] = w;
-                  }
-            }
-          }
-#pragma unroll
-          for (int d = 0; d < D / 16; ++d) {
-            const uint4 v0 = lds128(at + d * 1024), v1 = lds128(at + d * 1024 + 512);
-            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-            for (int st = 0; st < 4; ++st) {
-              uint32_t a[4];
-              e4m3x4_f16x4(w0[st] & keep[st], a[0], a[2]);
-              e4m3x4_f16x4(w1[st] & keep[st], a[1], a[3]);
-#pragma unroll
-              for (int n = 0; n < NB; ++n) mma_f16(o[n][d], a, pw[n][st][0], pw[n][st][1]);
-            }
-          }
+          free_slots(1);
         }
-      }
-      free_slot();
+      };
+      if (edge)
+        add_values(std::true_type{});
+      else
+        add_values(std::false_type{});
     }
+
     // ----------------------------------------------------- the segment's end
-    float* part = kv_part(p.ws, me, begins ? 1 : 0, R, D);
+    float* part = dealt.per_cta == 1 ? kv_part(p.ws, blockIdx.x, begins ? 1 : 0, R, D)
+                                     : kv_worker_part(p.ws, me, begins ? 1 : 0, R, D);
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -442,8 +573,7 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
         const int r = n * 8 + 2 * t + j;
         if (r >= it.rows) continue;
         if (begins && ends) {
-          const int64_t row = (int64_t)(it.s0 + (it.r0 + r) / p.group) * (p.c.heads * p.group) + head * p.group +
-                              (it.r0 + r) % p.group;
+          const int64_t row = kv_row(p, it, head, r);
           uint16_t* out = static_cast<uint16_t*>(p.out) + row * D + g;
 #pragma unroll
           for (int d = 0; d < D / 16; ++d)
@@ -459,82 +589,141 @@ __global__ void __launch_bounds__(32 * kWarps<D>, 1) rn_kv_attn_kernel(const KvA
           if (g == 0) part[R * D + r] = log2s;
         }
       }
-    if (at.left == cnt && lane == 0)
-      desc[me] = desc_of(dealt, me, begins && !ends ? dealt.start(me + 1) + (it.nblk - blk - cnt) : 0, at.item, it.rows,
-                         head);
+    if (lane == 0) {
+      WorkerEnd& e = ends_of[warp];
+      if (!begins) {
+        e.within = 1;
+        e.closes = ends;
+        e.item0 = at.item;
+        e.rows0 = it.rows;
+        e.head0 = head;
+      } else if (!ends) {
+        e.opens = 1;
+        e.item = at.item;
+        e.rows = it.rows;
+        e.head = head;
+        e.end = dealt.start(me + 1) + (it.nblk - blk - cnt);
+      }
+    }
     at.advance(pl, p.c.heads, cnt);
+  }
+
+  // ------------------------------------------------- the join within the CTA
+  const int n_workers = min(dealt.per_cta, dealt.workers - (int)blockIdx.x * dealt.per_cta);
+  if (dealt.per_cta == 1) {
+    if (warp == 0 && lane == 0) {
+      const WorkerEnd& e = ends_of[0];
+      desc[blockIdx.x] = desc_of(dealt, 1, e.opens ? e.end : 0, e.item, e.rows, e.head);
+    }
+    return;
+  }
+  __syncthreads();
+  const int w0 = (int)blockIdx.x * dealt.per_cta;
+  if (tid == 0) {
+    Desc d{0, 0, 0, 0};
+    const int64_t cta_end = dealt.start(w0 + n_workers);
+    for (int w = 0; w < n_workers; ++w)
+      if (ends_of[w].opens && ends_of[w].end > cta_end)
+        d = desc_of(dealt, dealt.per_cta, ends_of[w].end, ends_of[w].item, ends_of[w].rows, ends_of[w].head);
+    desc[blockIdx.x] = d;
+  }
+  // The one that the CTA begins within: its rows go to the warps.
+  if (ends_of[0].within) {
+    int n = 1;
+    while (n < n_workers && !ends_of[n - 1].closes) ++n;
+    for (int row = warp; row < ends_of[0].rows0; row += W) {
+      const Joined<D> j = join_parts<D>(n, 0, 1, lane, row, R, [&](int i) -> const float* {
+        return kv_worker_part(p.ws, w0 + i, 0, R, D);
+      });
+      store_part<D>(j, kv_part(p.ws, blockIdx.x, 0, R, D), row, R, lane);
+    }
+  }
+  // A warp joins the one that it opened, with the first parts of the warps behind it.
+  if (warp < n_workers && ends_of[warp].opens) {
+    const WorkerEnd& e = ends_of[warp];
+    int last = warp;
+    bool closed = false;
+    while (!closed && last + 1 < n_workers) closed = ends_of[++last].closes != 0;
+    const Item it = item_at<R>(pl, e.item);
+    constexpr int RB = D <= 128 ? 8 : 4;
+    for (int row0 = 0; row0 < e.rows; row0 += RB)
+      join_rows<D, RB>(
+          last - warp + 1, lane, row0, e.rows, R,
+          [&](int i) -> const float* { return kv_worker_part(p.ws, me + i, i == 0 ? 1 : 0, R, D); },
+          [&](int row, const Joined<D>& j) {
+            if (closed)
+              store_joined<D>(p, j, kv_row(p, it, e.head, row), lane);
+            else
+              store_part<D>(j, kv_part(p.ws, blockIdx.x, 1, R, D), row, R, lane);
+          });
   }
 }
 
-// Joins the parts of a (row tile, head): worker w's second part and the first
-// parts of the workers behind it, in that order.
-template <int D, int R>
+// Joins the parts of a (row tile, head) that several CTAs share: the second part
+// of the CTA that begins it and the first parts of those behind it, in that
+// order; SP warps of a CTA share the parts of a row.
+template <int D, int R, int SP>
 __global__ void __launch_bounds__(256) rn_kv_join_kernel(const KvAttnParams p) {
+  __shared__ float part_s[8][D + 2];
   pdl_launch_dependents();
   pdl_wait();
-  const int w = blockIdx.x;
-  const Desc d = static_cast<const Desc*>(p.ws)[w];
+  const int cta = blockIdx.x;
+  const Desc d = static_cast<const Desc*>(p.ws)[cta];
   if (d.parts == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto part = [&](int i) -> const float* { return kv_part(p.ws, w + i, i == 0 ? 1 : 0, R, D); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % SP;
   const Plan pl{p.q.starts, p.q.lens, p.q.B, p.q.tokens, p.group, p.causal, p.window, p.q.width * 64};
   const Item it = item_at<R>(pl, d.item);
-  for (int r = blockIdx.y * 8 + warp; r < d.rows; r += 8 * gridDim.y) {
-    float top = -INFINITY;
-    for (int i = lane; i < d.parts; i += 32) top = fmaxf(top, part(i)[R * D + r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if (top == -INFINITY) top = 0.0f;
-    float sum = 0.0f;
-    float acc[D / 32] = {};
-#pragma unroll 4
-    for (int i = 0; i < d.parts; ++i) {
-      const float wgt = ex2(part(i)[R * D + r] - top);
-      sum += wgt;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(wgt, part(i)[r * D + c * 32 + lane], acc[c]);
+  constexpr int kRows = 8 / SP;
+  for (int r0 = blockIdx.y * kRows; r0 < d.rows; r0 += kRows * gridDim.y) {
+    const int row = r0 + warp / SP;
+    Joined<D> j{};
+    j.top = -INFINITY;
+    if (row < d.rows)
+      j = join_parts<D>(d.parts, sub, SP, lane, row, R,
+                        [&](int i) -> const float* { return kv_part(p.ws, cta + i, i == 0 ? 1 : 0, R, D); });
+    if constexpr (SP > 1) {
+      store_part<D>(j, part_s[warp], 0, 1, lane);
+      __syncthreads();
+      if (sub == 0) {
+        j = join_parts<D>(SP, 0, 1, lane, 0, 1, [&](int i) -> const float* { return part_s[warp + i]; });
+      }
+      __syncthreads();
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t row = (int64_t)(it.s0 + (it.r0 + r) / p.group) * (p.c.heads * p.group) + d.head * p.group +
-                        (it.r0 + r) % p.group;
-    uint16_t* out = static_cast<uint16_t*>(p.out) + row * D + lane;
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) out[c * 32] = (uint16_t)pack_bf16x2(acc[c] * inv, 0.0f);
-    if (p.lse != nullptr && lane == 0) p.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    if (sub == 0 && row < d.rows) store_joined<D>(p, j, kv_row(p, it, d.head, row), lane);
   }
 }
 
 template <int D, int NB, bool EXTRA>
 rn_status launch_all(const KvAttnParams& p, int sms, cudaStream_t s) {
-  constexpr int R = 8 * NB, W = kWarps<D>;
-  constexpr size_t smem = (size_t)W * kSlots<D> * 64 * D;
+  constexpr int R = 8 * NB, W = kWarps;
+  constexpr size_t smem = (size_t)W * kSlots<D> * kPiece<D>;
   auto k = rn_kv_attn_kernel<D, NB, EXTRA>;
   static std::atomic<int> kept[kMaxDevices];
   if (once_per_device(kept, [&] {
         return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess ? 1 : -1;
       }) < 1)
     return RN_ERR_CUDA;
-  const int items = (int)((int64_t)p.q.tokens * p.group / R) + p.q.B;
+  const int items = (int)((int64_t)p.q.tokens * p.group.d / R) + p.q.B;
   const int grid = sms < kKvMaxCtas ? sms : kKvMaxCtas;
   rn_status st = launch_pdl<KvAttnParams, int>(k, dim3(grid), 32 * W, smem, s, p, items);
   if (st != RN_OK) return st;
-  return launch_kv_join(p, D, R, grid * W, s);
+  return launch_kv_join(p, D, R, grid, s);
 }
 
 template <int D>
-rn_status join_d(const KvAttnParams& p, int rows, int workers, cudaStream_t s) {
+rn_status join_d(const KvAttnParams& p, int rows, int ctas, cudaStream_t s) {
   switch (rows) {
-    case 8: return launch_pdl<KvAttnParams>(rn_kv_join_kernel<D, 8>, dim3(workers), 256, 0, s, p);
-    case 16: return launch_pdl<KvAttnParams>(rn_kv_join_kernel<D, 16>, dim3(workers, 2), 256, 0, s, p);
-    case 128: return launch_pdl<KvAttnParams>(rn_kv_join_kernel<D, 128>, dim3(workers, 8), 256, 0, s, p);
-    default: return launch_pdl<KvAttnParams>(rn_kv_join_kernel<D, 256>, dim3(workers, 8), 256, 0, s, p);
+    case 8: return launch_pdl<KvAttnParams>(rn_kv_join_kernel<D, 8, 4>, dim3(ctas, 4), 256, 0, s, p);
+    case 16: return launch_pdl<KvAttnParams>(rn_kv_join_kernel<D, 16, 4>, dim3(ctas, 8), 256, 0, s, p);
+    case 128: return launch_pdl<KvAttnParams>(rn_kv_join_kernel<D, 128, 1>, dim3(ctas, 8), 256, 0, s, p);
+    default: return launch_pdl<KvAttnParams>(rn_kv_join_kernel<D, 256, 1>, dim3(ctas, 16), 256, 0, s, p);
   }
 }
 
 template <int D>
 rn_status launch_d(const KvAttnParams& p, int sms, cudaStream_t s) {
   const bool extra = p.softcap > 0.0f || p.slopes != nullptr;
-  const int64_t rows = (int64_t)p.q.tokens * p.group;  // of a head, all sequences
+  const int64_t rows = (int64_t)p.q.tokens * p.group.d;  // of a head, all sequences
   if (rows > (int64_t)16 * p.q.B) return launch_kv_tile(p, D, sms, s);
   const bool one = rows <= (int64_t)8 * p.q.B;
   if (one) return extra ? launch_all<D, 1, true>(p, sms, s) : launch_all<D, 1, false>(p, sms, s);
@@ -552,18 +741,20 @@ rn_status launch_kv_attn(const KvAttnParams& p, int dim, int sms, cudaStream_t s
   }
 }
 
-rn_status launch_kv_join(const KvAttnParams& p, int dim, int rows, int workers, cudaStream_t s) {
+rn_status launch_kv_join(const KvAttnParams& p, int dim, int rows, int ctas, cudaStream_t s) {
   switch (dim) {
-    case 64: return join_d<64>(p, rows, workers, s);
-    case 128: return join_d<128>(p, rows, workers, s);
-    case 192: return join_d<192>(p, rows, workers, s);
-    default: return join_d<256>(p, rows, workers, s);
+    case 64: return join_d<64>(p, rows, ctas, s);
+    case 128: return join_d<128>(p, rows, ctas, s);
+    case 192: return join_d<192>(p, rows, ctas, s);
+    default: return join_d<256>(p, rows, ctas, s);
   }
 }
 
 size_t kv_attn_bytes(int dim) {
-  const int64_t few = kKvMaxWorkers * part_floats(16, dim), tile = kKvMaxCtas * part_floats(256, dim);
-  return sizeof(Desc) * kKvMaxWorkers + sizeof(float) * 2 * (size_t)(few > tile ? few : tile);
+  // few rows: up to 16, and partial results of every warp; many: tiles of 256 rows, or 128 where dim > 128
+  const int64_t few = (kKvMaxCtas + kKvMaxWorkers) * part_floats(16, dim);
+  const int64_t many = kKvMaxCtas * part_floats(dim > 128 ? 128 : 256, dim);
+  return sizeof(Desc) * kKvMaxCtas + sizeof(float) * 2 * (size_t)(few > many ? few : many);
 }
 
 rn_status read_clear_error_kv(unsigned* code) {

@@ -16,9 +16,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // sequences whose rows and lengths are kept in shared memory
 constexpr int kSeqsInSmem = 1024;
 
-// the (row tile, head) that a worker begins last and does not finish
+// the (row tile, head) that a CTA begins and does not finish
 struct Desc {
-  int parts;   // workers that share it, this one the first (0: none)
+  int parts;   // CTAs that share it, this one the first (0: none)
   int item, rows, head;
 };
 
@@ -36,13 +36,15 @@ struct Item {
 struct Plan {
   const int* starts;  // shared or global
   const int* lens;
-  int B, tokens, group, causal, window;
+  int B, tokens;
+  FastDiv group;
+  int causal, window;
   int reach;          // positions that the page table has room for
 };
 
 template <int R>
 __device__ __forceinline__ int item_base(const Plan& a, int b) {
-  return (int)((int64_t)min(max(a.starts[b], 0), a.tokens) * a.group / R) + b;
+  return (int)((int64_t)min(max(a.starts[b], 0), a.tokens) * a.group.d / R) + b;
 }
 
 // item i of the call; nblk = 0 where it has no rows.  The sequence with r rows
@@ -60,7 +62,7 @@ __device__ __forceinline__ Item item_at(const Plan& a, int i) {
   t.b = lo;
   const KvRows r = kv_rows(a.starts, lo, a.tokens);
   const int n = r.s1 - r.s0;
-  const int64_t all = (int64_t)n * a.group, first = (int64_t)(i - item_base<R>(a, lo)) * R;
+  const int64_t all = (int64_t)n * a.group.d, first = (int64_t)(i - item_base<R>(a, lo)) * R;
   t.s0 = r.s0;
   t.nblk = 0;
   t.rows = 0;
@@ -69,7 +71,7 @@ __device__ __forceinline__ Item item_at(const Plan& a, int i) {
   t.rows = (int)min((int64_t)R, all - first);
   t.len = max(a.lens[lo], 0);
   t.p0 = t.len - n;
-  const int i0 = t.r0 / a.group, i1 = (t.r0 + t.rows - 1) / a.group;
+  const int i0 = quot(t.r0, a.group), i1 = quot(t.r0 + t.rows - 1, a.group);
   t.hi = min(a.causal ? max(t.p0 + i1 + 1, 0) : t.len, a.reach);
   t.lo = a.window > 0 ? max(t.p0 + i0 - a.window + 1, 0) : 0;
   t.blk0 = t.lo >> 6;
@@ -107,16 +109,20 @@ struct Walk {
 template <int W, int WARPS>
 struct Ranges {
   int64_t sums[WARPS];
-  int64_t base[W];
+  int64_t from[W];   // the first page of the worker's (row tile, ...), before it is dealt to heads
+  int64_t base[W];   // where its item's pages begin
   int item[W];
   int seqs[2 * kSeqsInSmem + 1];
 };
 
+// The first `more` workers have one page more than the others.
 struct Dealt {
-  int64_t total;   // pages of the call, times heads
-  int per_cta;     // workers of a CTA; all of them are `workers`
+  int64_t total;     // pages of the call, times heads
+  int64_t each;
+  int more;
+  int per_cta;       // workers of a CTA; all of them are `workers`
   int workers;
-  __device__ __forceinline__ int64_t start(int w) const { return total * w / workers; }
+  __device__ __forceinline__ int64_t start(int w) const { return each * w + min(w, more); }
 };
 
 // Called by all NT threads: the call's plan, and the items that the CTA's
@@ -131,33 +137,54 @@ __device__ __forceinline__ Dealt deal_pages(const KvAttnParams& p, int items, Ra
     for (int i = tid; i < p.q.B; i += NT) sh.seqs[kSeqsInSmem + 1 + i] = p.q.lens[i];
     pl.starts = sh.seqs;
     pl.lens = sh.seqs + kSeqsInSmem + 1;
+    __syncthreads();
   }
-  if (tid < W) sh.item[tid] = -1;
-  __syncthreads();
-  int64_t mine = 0;
-  for (int i = tid; i < items; i += NT) mine += item_at<R>(pl, i).nblk;
+  // pages of the items up to a thread's, of the first NT items; and all pages
+  int n = tid < items ? item_at<R>(pl, tid).nblk : 0;
+  int64_t incl = n, rest = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-  if (lane == 0) sh.sums[warp] = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  for (int i = tid + NT; i < items; i += NT) rest += item_at<R>(pl, i).nblk;
+  if (items > NT) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, o);
+  }
+  if (lane == 31) sh.sums[warp] = incl + rest;
   __syncthreads();
   Dealt d;
   d.total = 0;
 #pragma unroll
   for (int i = 0; i < NT / 32; ++i) d.total += sh.sums[i];
   d.total *= p.c.heads;
-  d.per_cta = (int)min((int64_t)W, (d.total + gridDim.x - 1) / gridDim.x);
+  d.per_cta = (int)(d.total >= (int64_t)W * gridDim.x ? W : ((int)d.total + gridDim.x - 1) / gridDim.x);
   d.workers = (int)min((int64_t)d.per_cta * gridDim.x, d.total);
+  d.each = d.more = 0;
   if (d.total == 0) return d;
-  // one more pass over the sums
+  if (d.total < (int64_t(1) << 31)) {  // the usual case, without a division of 64 bits
+    d.each = (uint32_t)d.total / (uint32_t)d.workers;
+  } else {
+    d.each = d.total / d.workers;
+  }
+  d.more = (int)(d.total - d.each * d.workers);
+  const int w0 = (int)blockIdx.x * d.per_cta, mine = min(d.per_cta, d.workers - w0);
+  if (tid < mine) {
+    const int64_t f = d.start(w0 + tid);
+    sh.from[tid] = f < (int64_t(1) << 31) ? (int64_t)((uint32_t)f / (uint32_t)p.c.heads) : f / p.c.heads;
+  }
+  // where they begin, chunk after chunk of the items
   int64_t before = 0;
   for (int i0 = 0; i0 < items; i0 += NT) {
-    const int i = i0 + tid;
-    const int n = i < items ? item_at<R>(pl, i).nblk : 0;
-    int64_t incl = n;
+    if (i0 > 0) {
+      n = i0 + tid < items ? item_at<R>(pl, i0 + tid).nblk : 0;
+      incl = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += v;
+      }
     }
     __syncthreads();
     if (lane == 31) sh.sums[warp] = incl;
@@ -169,15 +196,11 @@ __device__ __forceinline__ Dealt deal_pages(const KvAttnParams& p, int items, Ra
       all += sh.sums[w];
     }
     incl += before;
-    for (int w = 0; w < d.per_cta; ++w) {
-      const int me = (int)blockIdx.x * d.per_cta + w;
-      if (me >= d.workers) break;
-      const int64_t f = d.start(me) / p.c.heads;
-      if (incl - n <= f && f < incl) {
-        sh.item[w] = i;
+    for (int w = 0; w < mine; ++w)
+      if (incl - n <= sh.from[w] && sh.from[w] < incl) {
+        sh.item[w] = i0 + tid;
         sh.base[w] = incl - n;
       }
-    }
     before += all;
   }
   __syncthreads();
@@ -192,32 +215,44 @@ __device__ __forceinline__ Walk<R> walk_of(const Plan& pl, const Dealt& d, const
   const int64_t f0 = d.start(me);
   k.item = sh.item[w];
   k.it = item_at<R>(pl, k.item);
+  // pages within the item: at most heads * nblk
   const int64_t rel = f0 - sh.base[w] * heads;
-  k.head = (int)(rel / k.it.nblk);
+  k.head = rel < (int64_t(1) << 31) ? (int)((uint32_t)rel / (uint32_t)k.it.nblk) : (int)(rel / k.it.nblk);
   k.blk = (int)(rel - (int64_t)k.head * k.it.nblk);
   k.left = d.start(me + 1) - f0;
   return k;
 }
 
-// What worker `me` leaves for the join: `end` is where the pages of the (row
-// tile, head) that it began and did not finish end, 0 if it has none.
-__device__ __forceinline__ Desc desc_of(const Dealt& d, int me, int64_t end, int item, int rows, int head) {
+// What a CTA leaves for the join: `end` is where the pages of the (row tile,
+// head) that it began and did not finish end, 0 if it has none; `per_cta`
+// workers of the deal are a CTA's.
+__device__ __forceinline__ Desc desc_of(const Dealt& d, int per_cta, int64_t end, int item, int rows, int head) {
   Desc r{0, item, rows, head};
   if (end > 0) {
-    int w = me + 1;  // the worker that holds the last page
-    while (d.start(w + 1) < end) ++w;
-    r.parts = w - me + 1;
+    int c = (int)blockIdx.x + 1;  // the CTA that holds the last page
+    while (d.start(min((c + 1) * per_cta, d.workers)) < end) ++c;
+    r.parts = c - (int)blockIdx.x + 1;
   }
   return r;
 }
 
-// Workspace: a Desc for every worker, then two partial results each: of the
-// (row tile, head) that its range begins within (0) and of the one that it
-// begins and does not finish (1): R rows of dims, then their log2 sums.
+// Workspace: a Desc for every CTA, then two partial results each: of the (row
+// tile, head) that its range begins within (0) and of the one that it begins and
+// does not finish (1): R rows of dims, then their log2 sums.  Behind them the
+// same for every worker, where a CTA has several.
 __host__ __device__ inline int64_t part_floats(int rows, int dim) { return (int64_t)rows * dim + rows; }
-__device__ __forceinline__ float* kv_part(void* ws, int worker, int which, int rows, int dim) {
-  return reinterpret_cast<float*>(static_cast<Desc*>(ws) + kKvMaxWorkers) +
-         ((int64_t)worker * 2 + which) * part_floats(rows, dim);
+__device__ __forceinline__ float* kv_part(void* ws, int cta, int which, int rows, int dim) {
+  return reinterpret_cast<float*>(static_cast<Desc*>(ws) + kKvMaxCtas) +
+         ((int64_t)cta * 2 + which) * part_floats(rows, dim);
+}
+__device__ __forceinline__ float* kv_worker_part(void* ws, int worker, int which, int rows, int dim) {
+  return kv_part(ws, kKvMaxCtas + worker, which, rows, dim);
+}
+
+// a row of the output, as an index into [tokens, query heads]
+__device__ __forceinline__ int64_t kv_row(const KvAttnParams& p, const Item& it, int head, int r) {
+  const int rr = it.r0 + r, i = quot(rr, p.group), d = p.group.d;
+  return ((int64_t)(it.s0 + i) * p.c.heads + head) * d + (rr - i * d);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -232,8 +267,8 @@ __device__ __forceinline__ float capped(float z, float cap, float two_over_cap_l
   return cap - __fdividef(2.0f * cap, ex2(x > 126.0f ? 126.0f : x) + 1.0f);
 }
 
-// joins the partial results of tiles of `rows` rows left by up to `workers` workers
-rn_status launch_kv_join(const KvAttnParams& p, int dim, int rows, int workers, cudaStream_t s);
+// joins the partial results of tiles of `rows` rows left by `ctas` CTAs
+rn_status launch_kv_join(const KvAttnParams& p, int dim, int rows, int ctas, cudaStream_t s);
 // for more than a few rows a key/value head (rn_kv_tile.cu)
 rn_status launch_kv_tile(const KvAttnParams& p, int dim, int sms, cudaStream_t s);
 

@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
         if (lane == 0) {
           const Item& it = at.it;
           const int base = (it.blk0 + at.blk) * 64;
-          const int i0 = it.r0 / p.group, i1 = (it.r0 + it.rows - 1) / p.group;
+          const int i0 = quot(it.r0, p.group), i1 = quot(it.r0 + it.rows - 1, p.group);
           const bool some = i1 > i0 && (base + 64 > (p.causal ? it.p0 + i0 + 1 : it.len) ||
                                         (p.window > 0 && base < it.p0 + i1 - p.window + 1));
           slot_info[r.slot] = SlotInfo{max(it.lo - base, 0), pg >= 0 ? min(it.hi - base, 64) : 0, some};
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
       const bool both = NG == 2 && it.rows > 128, split = NG == 2 && !both;
       const int row_in = both ? x * 128 + in_tile : in_tile;
       const int rr = it.r0 + min(row_in, it.rows - 1);
-      const int qi = rr / p.group, qh = head * p.group + rr % p.group;
+      const int qi = quot(rr, p.group), qh = head * p.group.d + rr - qi * p.group.d;
       float qs;
       {
         // the query row in f16, its largest magnitude at 2^14
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
       if (lane == 0) mbar_arrive(smem_u32(&q_b));
       const int pos0 = it.p0 + qi;
       const int row_hi = p.causal ? pos0 + 1 : it.len, row_lo = p.window > 0 ? pos0 - p.window + 1 : 0;
-      const int i0 = it.r0 / p.group, i1 = (it.r0 + it.rows - 1) / p.group;
+      const int i0 = quot(it.r0, p.group), i1 = quot(it.r0 + it.rows - 1, p.group);
       const int all_hi = p.causal ? it.p0 + i0 + 1 : it.len, all_lo = p.window > 0 ? it.p0 + i1 - p.window + 1 : 0;
       float slope = 0.0f;
       if constexpr (EXTRA)
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
         const float unit = sum == 0.0f ? 0.0f : ex2(bM - bm) / sum;
         const float fa = unit * ex2(M - bM), fb = unit * ex2(Mo - bM);
         const float log2s = sum == 0.0f ? -INFINITY : bm + log2f(sum);
-        const int64_t row = (int64_t)(it.s0 + qi) * (p.c.heads * p.group) + qh;
+        const int64_t row = (int64_t)(it.s0 + qi) * (p.c.heads * p.group.d) + qh;
         float* part = kv_part(p.ws, me, begins ? 1 : 0, R, D);
         const bool whole = begins && ends, real = row_in < it.rows;
 #pragma unroll 1
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
       }
       tc_fence_before();
       if (at.left == cnt && warp == kSoft && lane == 0)
-        desc[me] = desc_of(dealt, me, begins && !ends ? dealt.start(me + 1) + (it.nblk - at.blk - cnt) : 0, at.item,
+        desc[me] = desc_of(dealt, 1, begins && !ends ? dealt.start(me + 1) + (it.nblk - at.blk - cnt) : 0, at.item,
                            it.rows, head);
       at.advance(pl, p.c.heads, cnt);
     }
@@ -682,7 +682,7 @@ rn_status launch_e(const KvAttnParams& p, int sms, cudaStream_t s) {
         return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess ? 1 : -1;
       }) < 1)
     return RN_ERR_CUDA;
-  const int items = (int)((int64_t)p.q.tokens * p.group / kTileRows<D>) + p.q.B;
+  const int items = (int)((int64_t)p.q.tokens * p.group.d / kTileRows<D>) + p.q.B;
   const int grid = sms < kKvMaxCtas ? sms : kKvMaxCtas;
   rn_status st = launch_pdl<KvAttnParams, int>(k, dim3(grid), kTileThreads<D>, smem, s, p, items);
   if (st != RN_OK) return st;
