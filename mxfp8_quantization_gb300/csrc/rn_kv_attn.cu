@@ -112,37 +112,53 @@ __device__ __forceinline__ uint32_t byte_range(int from, int to) {
 template <int D>
 struct Joined {
   float2 acc[D / 64];
-  float top, sum;
+  float top;
 };
 
-// parts i0, i0 + step .. of n, each R rows of D and then the rows' log2 sums
+// Row `row` of the parts i0, i0 + step .. of n, each R rows of D and then the rows' log2 sums; the loads of four
+// parts are on their way together.
 template <int D, class Part>
 __device__ __forceinline__ Joined<D> join_parts(int n, int i0, int step, int lane, int row, int R, Part part) {
   Joined<D> j;
-  j.top = -INFINITY;
-  for (int i = i0 + lane * step; i < n; i += 32 * step) j.top = fmaxf(j.top, part(i)[R * D + row]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) j.top = fmaxf(j.top, __shfl_xor_sync(0xFFFFFFFFu, j.top, o));
-  const float top = j.top == -INFINITY ? 0.0f : j.top;
-  j.sum = 0.0f;
+  float top = -INFINITY, sum = 0.0f;
 #pragma unroll
   for (int c = 0; c < D / 64; ++c) j.acc[c] = make_float2(0.0f, 0.0f);
-#pragma unroll 8
-  for (int i = i0; i < n; i += step) {
-    const float* at = part(i);
-    const float w = ex2(at[R * D + row] - top);
-    j.sum += w;
+  for (int i = i0; i < n; i += 4 * step) {
+    float2 v[4][D / 64];
+    float l[4], now = top;
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-      const float2 v = *reinterpret_cast<const float2*>(at + row * D + c * 64 + 2 * lane);
-      j.acc[c].x = fmaf(w, v.x, j.acc[c].x);
-      j.acc[c].y = fmaf(w, v.y, j.acc[c].y);
+    for (int k = 0; k < 4; ++k) {
+      const float* at = part(min(i + k * step, n - 1));
+      l[k] = at[R * D + row];
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) v[k][c] = *reinterpret_cast<const float2*>(at + row * D + c * 64 + 2 * lane);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i + k * step >= n) l[k] = -INFINITY;
+      now = fmaxf(now, l[k]);
+    }
+    const float base = now == -INFINITY ? 0.0f : now, keep = ex2(top - base);
+    top = now;
+    sum *= keep;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) j.acc[c] = make_float2(j.acc[c].x * keep, j.acc[c].y * keep);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i + k * step >= n) continue;
+      const float w = ex2(l[k] - base);
+      sum += w;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        j.acc[c].x = fmaf(w, v[k][c].x, j.acc[c].x);
+        j.acc[c].y = fmaf(w, v[k][c].y, j.acc[c].y);
+      }
     }
   }
-  const float inv = j.sum == 0.0f ? 0.0f : 1.0f / j.sum;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
   for (int c = 0; c < D / 64; ++c) j.acc[c] = make_float2(j.acc[c].x * inv, j.acc[c].y * inv);
-  j.top = j.sum == 0.0f ? -INFINITY : top + log2f(j.sum);
+  j.top = sum == 0.0f ? -INFINITY : top + log2f(sum);
   return j;
 }
 // the row as a partial result again
@@ -214,9 +230,9 @@ constexpr int kNoScales = 256;  // no page
 struct WorkerEnd {
   int within, closes;        // it begins within a (row tile, head), and holds its last page
   int opens;                 // it begins one that it does not finish
-  int item, rows, head;      // of that one; of the first where it begins none
+  int s0, r0, rows, head;    // that one
   int64_t end;               // where its pages end
-  int item0, rows0, head0;   // the one that it begins within
+  int rows0;                 // of the one that it begins within
 };
 
 template <int D, int NB, bool EXTRA>
@@ -573,7 +589,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
         const int r = n * 8 + 2 * t + j;
         if (r >= it.rows) continue;
         if (begins && ends) {
-          const int64_t row = kv_row(p, it, head, r);
+          const int64_t row = kv_row(p, it.s0, it.r0, head, r);
           uint16_t* out = static_cast<uint16_t*>(p.out) + row * D + g;
 #pragma unroll
           for (int d = 0; d < D / 16; ++d)
@@ -594,12 +610,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
       if (!begins) {
         e.within = 1;
         e.closes = ends;
-        e.item0 = at.item;
         e.rows0 = it.rows;
-        e.head0 = head;
       } else if (!ends) {
         e.opens = 1;
-        e.item = at.item;
+        e.s0 = it.s0;
+        e.r0 = it.r0;
         e.rows = it.rows;
         e.head = head;
         e.end = dealt.start(me + 1) + (it.nblk - blk - cnt);
@@ -613,18 +628,19 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
   if (dealt.per_cta == 1) {
     if (warp == 0 && lane == 0) {
       const WorkerEnd& e = ends_of[0];
-      desc[blockIdx.x] = desc_of(dealt, 1, e.opens ? e.end : 0, e.item, e.rows, e.head);
+      desc[blockIdx.x] = desc_of(dealt, 1, e.opens ? e.end : 0, e.s0, e.r0, e.rows, e.head);
     }
     return;
   }
   __syncthreads();
   const int w0 = (int)blockIdx.x * dealt.per_cta;
   if (tid == 0) {
-    Desc d{0, 0, 0, 0};
+    Desc d{};
     const int64_t cta_end = dealt.start(w0 + n_workers);
-    for (int w = 0; w < n_workers; ++w)
-      if (ends_of[w].opens && ends_of[w].end > cta_end)
-        d = desc_of(dealt, dealt.per_cta, ends_of[w].end, ends_of[w].item, ends_of[w].rows, ends_of[w].head);
+    for (int w = 0; w < n_workers; ++w) {
+      const WorkerEnd& e = ends_of[w];
+      if (e.opens && e.end > cta_end) d = desc_of(dealt, dealt.per_cta, e.end, e.s0, e.r0, e.rows, e.head);
+    }
     desc[blockIdx.x] = d;
   }
   // The one that the CTA begins within: its rows go to the warps.
@@ -644,7 +660,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
     int last = warp;
     bool closed = false;
     while (!closed && last + 1 < n_workers) closed = ends_of[++last].closes != 0;
-    const Item it = item_at<R>(pl, e.item);
     constexpr int RB = D <= 128 ? 8 : 4;
     for (int row0 = 0; row0 < e.rows; row0 += RB)
       join_rows<D, RB>(
@@ -652,7 +667,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
           [&](int i) -> const float* { return kv_worker_part(p.ws, me + i, i == 0 ? 1 : 0, R, D); },
           [&](int row, const Joined<D>& j) {
             if (closed)
-              store_joined<D>(p, j, kv_row(p, it, e.head, row), lane);
+              store_joined<D>(p, j, kv_row(p, e.s0, e.r0, e.head, row), lane);
             else
               store_part<D>(j, kv_part(p.ws, blockIdx.x, 1, R, D), row, R, lane);
           });
@@ -671,13 +686,10 @@ __global__ void __launch_bounds__(256) rn_kv_join_kernel(const KvAttnParams p) {
   const Desc d = static_cast<const Desc*>(p.ws)[cta];
   if (d.parts == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % SP;
-  const Plan pl{p.q.starts, p.q.lens, p.q.B, p.q.tokens, p.group, p.causal, p.window, p.q.width * 64};
-  const Item it = item_at<R>(pl, d.item);
   constexpr int kRows = 8 / SP;
   for (int r0 = blockIdx.y * kRows; r0 < d.rows; r0 += kRows * gridDim.y) {
     const int row = r0 + warp / SP;
     Joined<D> j{};
-    j.top = -INFINITY;
     if (row < d.rows)
       j = join_parts<D>(d.parts, sub, SP, lane, row, R,
                         [&](int i) -> const float* { return kv_part(p.ws, cta + i, i == 0 ? 1 : 0, R, D); });
@@ -689,7 +701,7 @@ __global__ void __launch_bounds__(256) rn_kv_join_kernel(const KvAttnParams p) {
       }
       __syncthreads();
     }
-    if (sub == 0 && row < d.rows) store_joined<D>(p, j, kv_row(p, it, d.head, row), lane);
+    if (sub == 0 && row < d.rows) store_joined<D>(p, j, kv_row(p, d.s0, d.r0, d.head, row), lane);
   }
 }
 

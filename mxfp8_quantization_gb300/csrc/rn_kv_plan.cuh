@@ -18,8 +18,9 @@ constexpr int kSeqsInSmem = 1024;
 
 // the (row tile, head) that a CTA begins and does not finish
 struct Desc {
-  int parts;   // CTAs that share it, this one the first (0: none)
-  int item, rows, head;
+  int parts;       // CTAs that share it, this one the first (0: none)
+  int s0, r0, rows, head;
+  int unused[3];
 };
 
 // a row tile of a sequence
@@ -226,8 +227,8 @@ __device__ __forceinline__ Walk<R> walk_of(const Plan& pl, const Dealt& d, const
 // What a CTA leaves for the join: `end` is where the pages of the (row tile,
 // head) that it began and did not finish end, 0 if it has none; `per_cta`
 // workers of the deal are a CTA's.
-__device__ __forceinline__ Desc desc_of(const Dealt& d, int per_cta, int64_t end, int item, int rows, int head) {
-  Desc r{0, item, rows, head};
+__device__ __forceinline__ Desc desc_of(const Dealt& d, int per_cta, int64_t end, int s0, int r0, int rows, int head) {
+  Desc r{0, s0, r0, rows, head};
   if (end > 0) {
     int c = (int)blockIdx.x + 1;  // the CTA that holds the last page
     while (d.start(min((c + 1) * per_cta, d.workers)) < end) ++c;
@@ -250,9 +251,9 @@ __device__ __forceinline__ float* kv_worker_part(void* ws, int worker, int which
 }
 
 // a row of the output, as an index into [tokens, query heads]
-__device__ __forceinline__ int64_t kv_row(const KvAttnParams& p, const Item& it, int head, int r) {
-  const int rr = it.r0 + r, i = quot(rr, p.group), d = p.group.d;
-  return ((int64_t)(it.s0 + i) * p.c.heads + head) * d + (rr - i * d);
+__device__ __forceinline__ int64_t kv_row(const KvAttnParams& p, int s0, int r0, int head, int r) {
+  const int rr = r0 + r, i = quot(rr, p.group), d = p.group.d;
+  return ((int64_t)(s0 + i) * p.c.heads + head) * d + (rr - i * d);
 }
 
 __device__ __forceinline__ float ex2(float x) {

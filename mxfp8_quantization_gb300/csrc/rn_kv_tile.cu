@@ -662,8 +662,8 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
       }
       tc_fence_before();
       if (at.left == cnt && warp == kSoft && lane == 0)
-        desc[me] = desc_of(dealt, 1, begins && !ends ? dealt.start(me + 1) + (it.nblk - at.blk - cnt) : 0, at.item,
-                           it.rows, head);
+        desc[me] = desc_of(dealt, 1, begins && !ends ? dealt.start(me + 1) + (it.nblk - at.blk - cnt) : 0, it.s0,
+                           it.r0, it.rows, head);
       at.advance(pl, p.c.heads, cnt);
     }
   }
