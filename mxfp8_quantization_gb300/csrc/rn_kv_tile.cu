@@ -433,11 +433,14 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) +
                                                           (int64_t)(it.s0 + qi) * p.stride + (int64_t)qh * D);
         const bool real = row_in < it.rows;
+        // the whole row at once: its loads are on their way together
+        uint4 w4[D / 8];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) w4[c] = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
         uint32_t big = 0;
-#pragma unroll 4
+#pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-          const uint4 w4 = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+          const uint32_t w[4] = {w4[c].x, w4[c].y, w4[c].z, w4[c].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t lo = w[j] & 0x7FFFu, hi = w[j] >> 16 & 0x7FFFu;
@@ -447,14 +450,13 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
         }
         const int up = max((int)(big >> 7) - 127 - 14, kKvExpMin);
         const float mul = pow2i(-up);
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           uint32_t h[32];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const uint4 w4 = real ? __ldg(src + c * 8 + j) : make_uint4(0, 0, 0, 0);
             float f[8];
-            bf16x8_to_f32(w4, f);
+            bf16x8_to_f32(w4[c * 8 + j], f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) h[4 * j + i] = pack_f16x2(f[2 * i] * mul, f[2 * i + 1] * mul);
           }
