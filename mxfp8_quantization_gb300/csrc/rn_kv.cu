@@ -10,9 +10,10 @@
 // of two and rounded again, which is exact but for codes that become
 // subnormal.  Powers of two make that so, and make every cached value a bf16.
 //
-// A CTA owns the page of one head, keys or values.  The caller's arrays say on
-// the device which pages those are, so the grid holds the most there can be:
-// a sequence of n rows touches at most floor(n / 64) + 2 pages, and its units
+// A CTA owns the page of one head, keys or values; the heads of a page are
+// neighbours in the grid, as their rows are in memory.  The caller's arrays say
+// on the device which pages there are, so the grid holds the most there can
+// be: a sequence of n rows touches at most floor(n / 64) + 2 pages, and its units
 // begin at floor(starts[b] / 64) + 2 b.
 //
 // Keys lie [64, dim]: a thread takes 8 elements of a row.  Values lie
@@ -46,9 +47,23 @@ struct Unit {
 
 __device__ __forceinline__ bool find_unit(const KvSeqs& q, int64_t pages, int u, Unit* o) {
   const int lane = threadIdx.x & 31;
-  const int b = kv_find(q.B, u, lane, [&](int i) { return min(max(q.starts[i], 0), q.tokens) / 64 + 2 * i; });
-  const KvRows r = kv_rows(q.starts, b, q.tokens);
-  const int len = max(q.lens[b], 0), n = r.s1 - r.s0;
+  int b, len;
+  KvRows r;
+  if (q.B <= 32) {
+    // all sequences at once, one a lane
+    const int i = min(lane, q.B - 1);
+    const KvRows mine = kv_rows(q.starts, i, q.tokens);
+    const int mine_len = q.lens[i];
+    b = 31 - __clz(__ballot_sync(0xFFFFFFFFu, lane == 0 || (lane < q.B && mine.s0 / 64 + 2 * lane <= u)));
+    r.s0 = __shfl_sync(0xFFFFFFFFu, mine.s0, b);
+    r.s1 = __shfl_sync(0xFFFFFFFFu, mine.s1, b);
+    len = max(__shfl_sync(0xFFFFFFFFu, mine_len, b), 0);
+  } else {
+    b = kv_find(q.B, u, lane, [&](int i) { return min(max(q.starts[i], 0), q.tokens) / 64 + 2 * i; });
+    r = kv_rows(q.starts, b, q.tokens);
+    len = max(q.lens[b], 0);
+  }
+  const int n = r.s1 - r.s0;
   const int k = u - (r.s0 / 64 + 2 * b);
   const int p0 = len - n, from = max(p0, 0);
   o->b = b;
@@ -236,11 +251,11 @@ __global__ void __launch_bounds__(kNt<D>) rn_kv_write_kernel(const KvWriteParams
   pdl_launch_dependents();
   pdl_wait();
   Unit u;
-  if (!find_unit(p.q, p.c.pages, (int)blockIdx.x, &u) || u.page < 0) return;
-  const int h = blockIdx.y;
+  const int part = (int)(blockIdx.x % (2 * p.c.heads)), h = part >> 1, values = part & 1;
+  if (!find_unit(p.q, p.c.pages, (int)(blockIdx.x / (2 * p.c.heads)), &u) || u.page < 0) return;
   const int64_t ph = (int64_t)u.page * p.c.heads + h;
   constexpr int ESZ = BF16 ? 2 : 4;
-  if (blockIdx.z == 0)
+  if (!values)
     write_keys<D, BF16>(u, static_cast<const unsigned char*>(p.k) + (int64_t)h * D * ESZ, p.k_stride,
                         p.c.k + ph * 64 * D, p.c.ks + ph);
   else
@@ -267,10 +282,10 @@ __global__ void __launch_bounds__(kNt<D>) rn_kv_read_kernel(const KvReadParams p
   pdl_launch_dependents();
   pdl_wait();
   Unit u;
-  if (!find_unit(p.q, p.c.pages, (int)blockIdx.x, &u)) return;
+  const int split = (int)(blockIdx.x % (2 * p.c.heads)), h = split >> 1, values = split & 1;
+  if (!find_unit(p.q, p.c.pages, (int)(blockIdx.x / (2 * p.c.heads)), &u)) return;
   constexpr int NT = kNt<D>, ESZ = BF16 ? 2 : 4;
-  const int h = blockIdx.y;
-  unsigned char* out = static_cast<unsigned char*>(blockIdx.z == 0 ? p.k : p.v) + (int64_t)h * D * ESZ;
+  unsigned char* out = static_cast<unsigned char*>(values ? p.v : p.k) + (int64_t)h * D * ESZ;
   const int64_t stride = (int64_t)p.c.heads * D;
   const float zeros[8] = {};
   if (u.first)  // rows without a position
@@ -278,8 +293,8 @@ __global__ void __launch_bounds__(kNt<D>) rn_kv_read_kernel(const KvReadParams p
       store8<BF16>(out + ((u.s0 + at / (D / 8)) * stride + at % (D / 8) * 8) * ESZ, zeros);
   if (u.lo >= u.hi) return;
   const int64_t ph = (int64_t)max(u.page, 0) * p.c.heads + h;
-  const float s = u.page < 0 ? 0.0f : pow2i(kv_exp(blockIdx.z == 0 ? p.c.ks[ph] : p.c.vs[ph]));
-  if (blockIdx.z == 0) {
+  const float s = u.page < 0 ? 0.0f : pow2i(kv_exp(values ? p.c.vs[ph] : p.c.ks[ph]));
+  if (!values) {
     const uint8_t* page = p.c.k + ph * 64 * D;
     uint2 w[kChunks<D>];
 #pragma unroll
@@ -339,7 +354,7 @@ __global__ void __launch_bounds__(kNt<D>) rn_kv_read_kernel(const KvReadParams p
 template <class P>
 rn_status launch(void (*k)(P), int threads, const P& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.q.tokens / 64 + 2 * p.q.B), (unsigned)p.c.heads, 2);
+  cfg.gridDim = dim3((unsigned)((p.q.tokens / 64 + 2 * p.q.B) * 2 * p.c.heads));  // below 2^31: the entry points' check
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

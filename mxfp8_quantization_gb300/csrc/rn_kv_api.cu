@@ -35,6 +35,11 @@ rn_status check_seqs(const rn_kv_seqs* s, KvSeqs* o) {
 
 bool dtype_ok(rn_dtype d) { return d == RN_BF16 || d == RN_F32; }
 
+// the grid of the write and the read: units of a page, head and side
+bool grid_ok(const KvCache& c, const KvSeqs& q) {
+  return ((int64_t)q.tokens / 64 + 2 * (int64_t)q.B) * 2 * c.heads <= INT32_MAX;
+}
+
 // rows of `width` elements, `stride` apart, in whole 16-byte pieces
 rn_status check_rows(const void* p, rn_dtype d, int64_t stride, int64_t width) {
   if (stride < width) return RN_ERR_INVALID;
@@ -61,6 +66,7 @@ rn_status rn_kv_cache_write(const void* k, const void* v, rn_dtype dtype, int64_
   const int64_t width = (int64_t)p.c.heads * cache->dim;
   if ((st = check_rows(k, dtype, k_stride, width)) != RN_OK || (st = check_rows(v, dtype, v_stride, width)) != RN_OK)
     return st;
+  if (!grid_ok(p.c, p.q)) return RN_ERR_UNSUPPORTED;
   DeviceInfo di;
   if ((st = device_info(&di)) != RN_OK) return st;
   if (!any) return RN_OK;
@@ -79,7 +85,7 @@ rn_status rn_kv_cache_read(const rn_kv_cache* cache, const rn_kv_seqs* seqs, voi
   if (!dtype_ok(out_dtype)) return RN_ERR_INVALID;
   const bool any = p.q.tokens > 0 && p.q.B > 0;
   if (any && (k == nullptr || v == nullptr)) return RN_ERR_INVALID;
-  if (!aligned(k, 16) || !aligned(v, 16)) return RN_ERR_UNSUPPORTED;
+  if (!aligned(k, 16) || !aligned(v, 16) || !grid_ok(p.c, p.q)) return RN_ERR_UNSUPPORTED;
   DeviceInfo di;
   if ((st = device_info(&di)) != RN_OK) return st;
   if (!any) return RN_OK;

@@ -37,6 +37,7 @@ struct Item {
 struct Plan {
   const int* starts;  // shared or global
   const int* lens;
+  const int* bases;   // shared: item_base of every sequence, or NULL
   int B, tokens;
   FastDiv group;
   int causal, window;
@@ -56,7 +57,7 @@ __device__ __forceinline__ Item item_at(const Plan& a, int i) {
   int lo = 0, hi = a.B;  // the last b with base(b) <= i
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (item_base<R>(a, mid) <= i) lo = mid;
+    if ((a.bases != nullptr ? a.bases[mid] : item_base<R>(a, mid)) <= i) lo = mid;
     else hi = mid;
   }
   Item t;
@@ -113,7 +114,7 @@ struct Ranges {
   int64_t from[W];   // the first page of the worker's (row tile, ...), before it is dealt to heads
   int64_t base[W];   // where its item's pages begin
   int item[W];
-  int seqs[2 * kSeqsInSmem + 1];
+  int seqs[3 * kSeqsInSmem + 1];
 };
 
 // The first `more` workers have one page more than the others.
@@ -132,28 +133,35 @@ struct Dealt {
 template <int R, int W, int NT>
 __device__ __forceinline__ Dealt deal_pages(const KvAttnParams& p, int items, Ranges<W, NT / 32>& sh, Plan& pl) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pl = Plan{p.q.starts, p.q.lens, p.q.B, p.q.tokens, p.group, p.causal, p.window, p.q.width * 64};
+  pl = Plan{p.q.starts, p.q.lens, nullptr, p.q.B, p.q.tokens, p.group, p.causal, p.window, p.q.width * 64};
   if (p.q.B <= kSeqsInSmem) {
-    for (int i = tid; i <= p.q.B; i += NT) sh.seqs[i] = p.q.starts[i];
-    for (int i = tid; i < p.q.B; i += NT) sh.seqs[kSeqsInSmem + 1 + i] = p.q.lens[i];
-    pl.starts = sh.seqs;
-    pl.lens = sh.seqs + kSeqsInSmem + 1;
+    int *starts = sh.seqs, *lens = starts + kSeqsInSmem + 1, *bases = lens + kSeqsInSmem;
+    for (int i = tid; i <= p.q.B; i += NT) {
+      starts[i] = p.q.starts[i];
+      if (i < p.q.B) {
+        lens[i] = p.q.lens[i];
+        bases[i] = item_base<R>(pl, i);
+      }
+    }
+    pl.starts = starts;
+    pl.lens = lens;
+    pl.bases = bases;
     __syncthreads();
   }
-  // pages of the items up to a thread's, of the first NT items; and all pages
-  int n = tid < items ? item_at<R>(pl, tid).nblk : 0;
-  int64_t incl = n, rest = 0;
+  // pages of this thread's items: of the first kKept rounds they are kept
+  constexpr int kKept = 4;
+  int kept[kKept];
+  int64_t mine_all = 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-    if (lane >= o) incl += v;
+  for (int k = 0; k < kKept; ++k) {
+    const int i = tid + k * NT;
+    kept[k] = i < items ? item_at<R>(pl, i).nblk : 0;
+    mine_all += kept[k];
   }
-  for (int i = tid + NT; i < items; i += NT) rest += item_at<R>(pl, i).nblk;
-  if (items > NT) {
+  for (int i = tid + kKept * NT; i < items; i += NT) mine_all += item_at<R>(pl, i).nblk;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, o);
-  }
-  if (lane == 31) sh.sums[warp] = incl + rest;
+  for (int o = 16; o > 0; o >>= 1) mine_all += __shfl_xor_sync(0xFFFFFFFFu, mine_all, o);
+  if (lane == 0) sh.sums[warp] = mine_all;
   __syncthreads();
   Dealt d;
   d.total = 0;
@@ -175,17 +183,21 @@ __device__ __forceinline__ Dealt deal_pages(const KvAttnParams& p, int items, Ra
     const int64_t f = d.start(w0 + tid);
     sh.from[tid] = f < (int64_t(1) << 31) ? (int64_t)((uint32_t)f / (uint32_t)p.c.heads) : f / p.c.heads;
   }
-  // where they begin, chunk after chunk of the items
+  // where they begin, round after round of the items
   int64_t before = 0;
-  for (int i0 = 0; i0 < items; i0 += NT) {
-    if (i0 > 0) {
-      n = i0 + tid < items ? item_at<R>(pl, i0 + tid).nblk : 0;
-      incl = n;
+#pragma unroll 1
+  for (int round = 0; round * NT < items; ++round) {
+    const int i = round * NT + tid;
+    int n;
+    if (round < kKept)
+      n = round == 0 ? kept[0] : round == 1 ? kept[1] : round == 2 ? kept[2] : kept[3];
+    else
+      n = i < items ? item_at<R>(pl, i).nblk : 0;
+    int64_t incl = n;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += v;
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
     }
     __syncthreads();
     if (lane == 31) sh.sums[warp] = incl;
@@ -199,7 +211,7 @@ __device__ __forceinline__ Dealt deal_pages(const KvAttnParams& p, int items, Ra
     incl += before;
     for (int w = 0; w < mine; ++w)
       if (incl - n <= sh.from[w] && sh.from[w] < incl) {
-        sh.item[w] = i0 + tid;
+        sh.item[w] = i;
         sh.base[w] = incl - n;
       }
     before += all;
