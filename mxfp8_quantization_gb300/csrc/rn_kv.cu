@@ -143,12 +143,11 @@ __device__ __forceinline__ int page_exp(uint32_t bits, bool begun, uint32_t old_
 }
 
 template <int D, bool BF16>
-__device__ __forceinline__ void write_keys(const Unit& u, const unsigned char* x, int64_t stride, uint8_t* page,
-                                           uint8_t* scale) {
+__device__ __forceinline__ void write_keys(const Unit& u, const unsigned char* x, int64_t stride, const KvCache& cache,
+                                           int head) {
   constexpr int NT = kNt<D>, C = kChunks<D>, ESZ = BF16 ? 2 : 4;
   Eight<BF16> v[C];
   uint32_t bits = 0;
-  const uint32_t old_byte = u.lo > 0 ? *scale : 0u;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int at = i * NT + threadIdx.x, r = at / (D / 8), c = at % (D / 8);
@@ -157,6 +156,11 @@ __device__ __forceinline__ void write_keys(const Unit& u, const unsigned char* x
     else
       v[i].zero();
   }
+  // (the rows do not wait for the page's number, nor for its old scale)
+  if (u.page < 0) return;
+  const int64_t ph = (int64_t)u.page * cache.heads + head;
+  uint8_t *page = cache.k + ph * 64 * D, *scale = cache.ks + ph;
+  const uint32_t old_byte = u.lo > 0 ? *scale : 0u;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     float f[8];
@@ -186,13 +190,12 @@ __device__ __forceinline__ void write_keys(const Unit& u, const unsigned char* x
 }
 
 template <int D, bool BF16>
-__device__ __forceinline__ void write_values(const Unit& u, const unsigned char* x, int64_t stride, uint8_t* page,
-                                             uint8_t* scale) {
+__device__ __forceinline__ void write_values(const Unit& u, const unsigned char* x, int64_t stride,
+                                             const KvCache& cache, int head) {
   constexpr int NT = kNt<D>, C = kChunks<D> / 4, ESZ = BF16 ? 2 : 4;
   static_assert(C * NT == 16 * (D / 8), "whole quads of rows");
   Eight<BF16> v[C][4];
   uint32_t bits = 0;
-  const uint32_t old_byte = u.lo > 0 ? *scale : 0u;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int at = i * NT + threadIdx.x, r0 = at % 16 * 4, c = at / 16;
@@ -205,6 +208,11 @@ __device__ __forceinline__ void write_values(const Unit& u, const unsigned char*
         v[i][q].zero();
     }
   }
+  // (the rows do not wait for the page's number, nor for its old scale)
+  if (u.page < 0) return;
+  const int64_t ph = (int64_t)u.page * cache.heads + head;
+  uint8_t *page = cache.v + ph * 64 * D, *scale = cache.vs + ph;
+  const uint32_t old_byte = u.lo > 0 ? *scale : 0u;
 #pragma unroll
   for (int i = 0; i < C; ++i)
 #pragma unroll
@@ -246,21 +254,19 @@ __device__ __forceinline__ void write_values(const Unit& u, const unsigned char*
   if (threadIdx.x == 0) *scale = (uint8_t)(e + 127);
 }
 
+// 64 registers a thread for bf16 rows, so that an SM has 1024 threads with loads on their way
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kNt<D>) rn_kv_write_kernel(const KvWriteParams p) {
+__global__ void __launch_bounds__(kNt<D>, BF16 ? 1024 / kNt<D> : 640 / kNt<D>) rn_kv_write_kernel(const KvWriteParams p) {
   pdl_launch_dependents();
   pdl_wait();
   Unit u;
   const int part = (int)(blockIdx.x % (2 * p.c.heads)), h = part >> 1, values = part & 1;
-  if (!find_unit(p.q, p.c.pages, (int)(blockIdx.x / (2 * p.c.heads)), &u) || u.page < 0) return;
-  const int64_t ph = (int64_t)u.page * p.c.heads + h;
+  if (!find_unit(p.q, p.c.pages, (int)(blockIdx.x / (2 * p.c.heads)), &u) || u.lo >= u.hi) return;
   constexpr int ESZ = BF16 ? 2 : 4;
   if (!values)
-    write_keys<D, BF16>(u, static_cast<const unsigned char*>(p.k) + (int64_t)h * D * ESZ, p.k_stride,
-                        p.c.k + ph * 64 * D, p.c.ks + ph);
+    write_keys<D, BF16>(u, static_cast<const unsigned char*>(p.k) + (int64_t)h * D * ESZ, p.k_stride, p.c, h);
   else
-    write_values<D, BF16>(u, static_cast<const unsigned char*>(p.v) + (int64_t)h * D * ESZ, p.v_stride,
-                          p.c.v + ph * 64 * D, p.c.vs + ph);
+    write_values<D, BF16>(u, static_cast<const unsigned char*>(p.v) + (int64_t)h * D * ESZ, p.v_stride, p.c, h);
 }
 
 // 8 values of a row
