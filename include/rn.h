@@ -474,7 +474,7 @@ typedef struct {
  *         apart (>= heads * dim, whole 16 bytes), 16-byte aligned
  * Per page and head: e is the smallest exponent with amax <= 448 * 2^e, amax
  * the largest finite magnitude of the page's new elements, clamped to [-120,
- * 120]; code = E4M3(x * 2^-e) (to nearest even, saturating, NaN -> 0x7F).  A
+ * 119]; code = E4M3(x * 2^-e) (to nearest even, saturating, NaN -> 0x7F).  A
  * page whose block begins before the rows keeps the larger of that e and its
  * own, e'; where e is larger the codes in front of the rows become
  * E4M3(value * 2^(e' - e)), which is exact unless they become subnormal.  A

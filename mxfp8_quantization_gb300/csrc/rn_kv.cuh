@@ -11,9 +11,9 @@
 namespace rn {
 
 // The scale of a page and head is 2^e, e in [kKvExpMin, kKvExpMax], stored as
-// the E8M0 byte e + 127: 2^e, 2^-e and 448 2^e are normal floats, and every
-// finite bf16 or fp32 below 448 2^120 fits.
-constexpr int kKvExpMin = -120, kKvExpMax = 120;
+// the E8M0 byte e + 127: 2^e, 2^-e and 448 2^e are normal floats (448 2^120
+// would not be one), so magnitudes above 448 2^119 = 2.98e38 saturate.
+constexpr int kKvExpMin = -120, kKvExpMax = 119;
 
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }

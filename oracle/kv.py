@@ -7,7 +7,7 @@ codes, E8M0 scale bytes).  Readings, as include/rn.h states them:
   lens[b] - n + i; block i of 64 positions stands in page table[b, i]; a page
   number that is none, a block past the table and a negative position mean
   that the position is not cached;
-* write: e = the smallest exponent with amax <= 448 2^e, clamped to [-120, 120],
+* write: e = the smallest exponent with amax <= 448 2^e, clamped to [-120, 119],
   code = E4M3(x 2^-e); a begun page keeps the larger exponent, and its old
   codes become E4M3(value 2^(e' - e));
 * attention: s = scale q.k, c tanh(s / c), + slope (j - p); softmax over the
@@ -22,7 +22,7 @@ import numpy as np
 from .formats import e4m3_decode, e4m3_encode
 
 PAGE = 64
-E_MIN, E_MAX = -120, 120
+E_MIN, E_MAX = -120, 119
 
 
 def exponent(values) -> int:

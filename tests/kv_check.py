@@ -82,4 +82,49 @@ def check(out, lse, want, dim, softcap=0.0):
         none = want["lse"] == -np.inf
         assert np.array_equal(g == -np.inf, none)
         some = ~none & ~np.isnan(want["lse"])
-        assert np.all(np.abs(g - want["lse"])[some] <= tol_lse[some])
+        assert np.all(np.abs(g[some] - want["lse"][some]) <= tol_lse[some])
+
+
+def reference(q, c, s, scale=None, causal=True, window=0, softcap=0.0, slopes=None):
+    """K.attention in fp64 torch operations on the GPU, for longer sequences (every position cached)."""
+    T, heads, D = q.shape
+    H = c.k.shape[1]
+    G = heads // H
+    scale = D ** -0.5 if scale is None else scale
+    f = dict(dtype=torch.float64, device="cuda")
+    r = {"out": torch.full(q.shape, float("nan"), **f), "lse": torch.full((T, heads), float("nan"), **f),
+         "pv": torch.zeros(q.shape, **f), "big": torch.zeros(T, heads, **f), "spread": torch.zeros(q.shape, **f),
+         "seen": torch.zeros(T, heads, **f)}
+    table, starts, lens = (t.cpu() for t in (s.table, s.starts, s.lens))
+    for b in range(len(lens)):
+        n, a, z = int(lens[b]), int(starts[b]), int(starts[b + 1])
+        if n == 0 or a == z:
+            r["out"][a:z], r["lse"][a:z] = 0.0, -float("inf")
+            continue
+        ids = table[b, :(n + PAGE - 1) // PAGE].long().cuda()
+        unit = torch.exp2(c.v_scales[ids].double() - 127).T.repeat_interleave(PAGE, 1)[:, :n]
+        k = c.k[ids].view(torch.float8_e4m3fn).double() * torch.exp2(c.k_scales[ids].double() - 127)[..., None, None]
+        v = c.v[ids].view(torch.float8_e4m3fn).double() * torch.exp2(c.v_scales[ids].double() - 127)[..., None, None]
+        k = k.transpose(0, 1).reshape(H, -1, D)[:, :n]
+        v = v.permute(1, 0, 3, 2).reshape(H, -1, D)[:, :n]
+        p = (n - (z - a) + torch.arange(z - a, device="cuda"))[:, None]
+        j = torch.arange(n, device="cuda")[None]
+        sees = (j <= p if causal else j >= 0) & (j > p - window if window else j >= 0) & (j >= 0)
+        sees = sees.expand(z - a, n)
+        for h in range(heads):
+            qq, kk, vv = q[a:z, h].double(), k[h // G], v[h // G]
+            t = scale * (qq @ kk.T)
+            big = (scale * (qq.abs() @ kk.abs().T)).masked_fill(~sees, 0).amax(1)
+            if softcap:
+                t = softcap * torch.tanh(t / softcap)
+            if slopes is not None:
+                t = t + slopes[h].double() * (j - p)
+                big = torch.maximum(big, (slopes[h].double().abs() * (j - p).abs()).masked_fill(~sees, 0).amax(1))
+            t = t.masked_fill(~sees, -float("inf"))
+            lse = torch.logsumexp(t, 1)
+            w = torch.exp(t - lse[:, None]).nan_to_num(0.0)
+            r["lse"][a:z, h], r["out"][a:z, h], r["pv"][a:z, h], r["big"][a:z, h] = lse, w @ vv, w @ vv.abs(), big
+            u = unit[h // G]
+            r["spread"][a:z, h] = (w * u).amax(1)[:, None] * (vv.abs() / u[:, None]).sum(0)
+            r["seen"][a:z, h] = sees.sum(1).double()
+    return {n: t.cpu().numpy() for n, t in r.items()}
