@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
   pdl_wait();
 
   Plan pl;
-  const Dealt dealt = deal_pages<R, W, 32 * W>(p, items, sh, pl);
+  const Dealt dealt = deal_pages<R, 0, W, 32 * W>(p, items, sh, pl);
   const int me = (int)blockIdx.x * dealt.per_cta + warp;
   Desc* desc = static_cast<Desc*>(p.ws);
   if (me >= dealt.workers && warp == 0) {  // nothing for this CTA
@@ -267,9 +267,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
   // ------------------------------------------------------------- copies
   // Page numbers are read 32 at a time, one a lane, and the next ones while these are used; the scales of a slot's
   // page are in the lane with the slot's number.
-  Walk<R> ld{};
-  if (works) ld = walk_of<R>(pl, dealt, sh, p.c.heads, me, warp);
-  Walk<R> at = ld;
+  using Range = Walk<R, 0>;
+  Range ld{};
+  if (works) ld = walk_of<R, 0>(pl, dealt, sh, p.c.heads, me, warp);
+  Range at = ld;
   int pages = -1, pages_next = -1, batch = 0, ks = 0, vs = 0;
   auto read_pages = [&](const Item& it, int blk) {
     const int b = blk + lane;
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
     if (batch + 32 < ld.it.nblk) {
       pages_next = read_pages(ld.it, batch + 32);
     } else {
-      Walk<R> next = ld;
+      Range next = ld;
       if (next.advance(pl, p.c.heads, next.segment())) pages_next = read_pages(next.it, 0);
     }
   };

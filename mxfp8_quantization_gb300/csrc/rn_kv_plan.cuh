@@ -82,20 +82,29 @@ __device__ __forceinline__ Item item_at(const Plan& a, int i) {
 }
 
 // A range of (row tile, head, page) triples, in this order, from its first on.
-template <int R>
+// Beginning a (row tile, head) costs as much as EXTRA pages (its queries, its
+// output), so it is dealt with as many more; a range that would end or begin
+// within those ends or begins in front of them.
+template <int R, int EXTRA>
 struct Walk {
   Item it;
   int item, head, blk;  // the next page
-  int64_t left;         // pages until the range's end
+  int64_t left;         // pages, and extra ones, until the range's end
 
   // pages of the (row tile, head) that the range still has
-  __device__ __forceinline__ int segment() const { return (int)min(left, (int64_t)(it.nblk - blk)); }
+  __device__ __forceinline__ int segment() const {
+    return (int)min(left - (blk == 0 ? EXTRA : 0), (int64_t)(it.nblk - blk));
+  }
 
   // n pages further, within a segment; true where that goes on to another (row tile, head)
   __device__ __forceinline__ bool advance(const Plan& a, int heads, int n) {
-    left -= n;
+    left -= n + (blk == 0 ? EXTRA : 0);
     blk += n;
-    if (blk < it.nblk || left == 0) return false;
+    if (blk < it.nblk) return false;
+    if (left <= EXTRA) {
+      left = 0;
+      return false;
+    }
     blk = 0;
     if (++head == heads) {
       head = 0;
@@ -104,6 +113,12 @@ struct Walk {
       } while (it.nblk == 0);  // pages are left, so an item with some follows
     }
     return true;
+  }
+
+  // whether the segment of cnt pages is the range's last
+  __device__ __forceinline__ bool is_last(int cnt) const {
+    const int64_t then = left - cnt - (blk == 0 ? EXTRA : 0);
+    return blk + cnt < it.nblk || then <= EXTRA;
   }
 };
 
@@ -119,7 +134,7 @@ struct Ranges {
 
 // The first `more` workers have one page more than the others.
 struct Dealt {
-  int64_t total;     // pages of the call, times heads
+  int64_t total;     // pages of the call with the extra ones, times heads
   int64_t each;
   int more;
   int per_cta;       // workers of a CTA; all of them are `workers`
@@ -130,7 +145,7 @@ struct Dealt {
 // Called by all NT threads: the call's plan, and the items that the CTA's
 // workers begin in (up to W of them; fewer where pages are few, so that every
 // SM has some, and a worker has one page at least).
-template <int R, int W, int NT>
+template <int R, int EXTRA, int W, int NT>
 __device__ __forceinline__ Dealt deal_pages(const KvAttnParams& p, int items, Ranges<W, NT / 32>& sh, Plan& pl) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pl = Plan{p.q.starts, p.q.lens, nullptr, p.q.B, p.q.tokens, p.group, p.causal, p.window, p.q.width * 64};
@@ -152,13 +167,16 @@ __device__ __forceinline__ Dealt deal_pages(const KvAttnParams& p, int items, Ra
   constexpr int kKept = 4;
   int kept[kKept];
   int64_t mine_all = 0;
+  auto pages_of = [&](int i) {
+    const int n = i < items ? item_at<R>(pl, i).nblk : 0;
+    return n > 0 ? n + EXTRA : 0;
+  };
 #pragma unroll
   for (int k = 0; k < kKept; ++k) {
-    const int i = tid + k * NT;
-    kept[k] = i < items ? item_at<R>(pl, i).nblk : 0;
+    kept[k] = pages_of(tid + k * NT);
     mine_all += kept[k];
   }
-  for (int i = tid + kKept * NT; i < items; i += NT) mine_all += item_at<R>(pl, i).nblk;
+  for (int i = tid + kKept * NT; i < items; i += NT) mine_all += pages_of(i);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine_all += __shfl_xor_sync(0xFFFFFFFFu, mine_all, o);
   if (lane == 0) sh.sums[warp] = mine_all;
@@ -192,7 +210,7 @@ __device__ __forceinline__ Dealt deal_pages(const KvAttnParams& p, int items, Ra
     if (round < kKept)
       n = round == 0 ? kept[0] : round == 1 ? kept[1] : round == 2 ? kept[2] : kept[3];
     else
-      n = i < items ? item_at<R>(pl, i).nblk : 0;
+      n = pages_of(i);
     int64_t incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -221,18 +239,21 @@ __device__ __forceinline__ Dealt deal_pages(const KvAttnParams& p, int items, Ra
 }
 
 // the range of worker `me`, the CTA's number w
-template <int R, int W, int WARPS>
-__device__ __forceinline__ Walk<R> walk_of(const Plan& pl, const Dealt& d, const Ranges<W, WARPS>& sh, int heads,
-                                           int me, int w) {
-  Walk<R> k;
+template <int R, int EXTRA, int W, int WARPS>
+__device__ __forceinline__ Walk<R, EXTRA> walk_of(const Plan& pl, const Dealt& d, const Ranges<W, WARPS>& sh, int heads,
+                                                  int me, int w) {
+  Walk<R, EXTRA> k;
   const int64_t f0 = d.start(me);
   k.item = sh.item[w];
   k.it = item_at<R>(pl, k.item);
-  // pages within the item: at most heads * nblk
+  // pages within the item: at most heads * each
   const int64_t rel = f0 - sh.base[w] * heads;
-  k.head = rel < (int64_t(1) << 31) ? (int)((uint32_t)rel / (uint32_t)k.it.nblk) : (int)(rel / k.it.nblk);
-  k.blk = (int)(rel - (int64_t)k.head * k.it.nblk);
-  k.left = d.start(me + 1) - f0;
+  const int each = k.it.nblk + EXTRA;
+  k.head = rel < (int64_t(1) << 31) ? (int)((uint32_t)rel / (uint32_t)each) : (int)(rel / each);
+  const int at = (int)(rel - (int64_t)k.head * each);
+  k.blk = max(at - EXTRA, 0);
+  k.left = d.start(me + 1) - f0 + (k.blk == 0 ? at : 0);
+  if (k.blk == 0 && k.left <= EXTRA) k.left = 0;
   return k;
 }
 

@@ -202,6 +202,10 @@ struct Stats {
   float m, M, l;
 };
 
+// What a (row tile, head) costs besides its pages, in pages (its queries' way into tensor memory, the first page's
+// latency, the output: 11 000 cycles and more; a page 2200)
+constexpr int kExtra = 6;
+
 template <int D, bool EXTRA>
 __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const KvAttnParams p, int items) {
   constexpr int NG = kGroups<D>, R = kTileRows<D>, NT = kTileThreads<D>, NS = kStagesKv<D>;
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
   pdl_launch_dependents();
   pdl_wait();
   Plan pl;
-  const Dealt dealt = deal_pages<R, 1, NT>(p, items, sh, pl);  // has barriers
+  const Dealt dealt = deal_pages<R, kExtra, 1, NT>(p, items, sh, pl);  // has barriers
   tc_fence_after();
   const int me = (int)blockIdx.x;
   Desc* desc = static_cast<Desc*>(p.ws);
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
     if (tid == 0) desc[me].parts = 0;
   } else if (warp < kConv) {
     regs_down<kRegsRest<D>>();
-    Walk<R> at = walk_of<R>(pl, dealt, sh, p.c.heads, me, 0);
+    Walk<R, kExtra> at = walk_of<R, kExtra>(pl, dealt, sh, p.c.heads, me, 0);
     if (warp == kCopy) {
       // ---------------------------------------------------- copies
       // page numbers are read 32 at a time, one a lane
@@ -332,7 +336,8 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
     regs_down<kRegsRest<D>>();
     const int cw = warp - kConv, sub = lane & 3, row8 = lane >> 2;
     RingPos r{0, 0}, in{0, 0};
-    for (int64_t todo = dealt.start(me + 1) - dealt.start(me); todo > 0; --todo) {
+    Walk<R, kExtra> at = walk_of<R, kExtra>(pl, dealt, sh, p.c.heads, me, 0);
+    for (; at.left > 0; at.advance(pl, p.c.heads, 1)) {
       mbar_wait(smem_u32(&in_b[in.slot]), in.phase, err, kErrFullWait);
       const SlotInfo si = slot_info[in.slot];
       mbar_wait(smem_u32(&empty_b[r.slot]), r.phase ^ 1u, err, kErrEmptyWait);
@@ -412,8 +417,9 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
   } else {
     // ------------------------------------------------------ softmax
     regs_up<kRegsSoft<D>>();
-    Walk<R> at = walk_of<R>(pl, dealt, sh, p.c.heads, me, 0);
+    Walk<R, kExtra> at = walk_of<R, kExtra>(pl, dealt, sh, p.c.heads, me, 0);
     const int x = (warp - kSoft) >> 2;                   // the tile
+    if (warp == kSoft && lane == 0) desc[me].parts = 0;  // for a range without pages
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tq = lanes + x * C::kQ, to = lanes + C::kO + x * D;
     const int in_tile = (warp & 3) * 32 + lane;
@@ -663,7 +669,7 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
         }
       }
       tc_fence_before();
-      if (at.left == cnt && warp == kSoft && lane == 0)
+      if (at.is_last(cnt) && warp == kSoft && lane == 0)
         desc[me] = desc_of(dealt, 1, begins && !ends ? dealt.start(me + 1) + (it.nblk - at.blk - cnt) : 0, it.s0,
                            it.r0, it.rows, head);
       at.advance(pl, p.c.heads, cnt);
