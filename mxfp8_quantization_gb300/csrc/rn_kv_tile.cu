@@ -340,26 +340,31 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
     for (; at.left > 0; at.advance(pl, p.c.heads, 1)) {
       mbar_wait(smem_u32(&in_b[in.slot]), in.phase, err, kErrFullWait);
       const SlotInfo si = slot_info[in.slot];
-      mbar_wait(smem_u32(&empty_b[r.slot]), r.phase ^ 1u, err, kErrEmptyWait);
+      // Keys: a warp takes 8 positions x 64 dims at a time, values 8 dims x 64 positions: 8 lanes read 128 bytes of
+      // different banks and write 128 bytes of different banks (of two rows; of two blocks of 64 dims where the
+      // rows lie a multiple of 128 bytes apart).  All are read first: one after another, a page took 1300 cycles.
       const uint32_t kc = codes + in.slot * kSlotBytes<D> + sub * 16, vc = kc + 64 * D;
+      uint4 kv[D / 32], vv[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int blk = D % 128 == 0 ? (i >> 1) ^ (row8 & 1) : i >> 1;
+        kv[i] = lds128(kc + (8 * (cw + 4 * (i & 1)) + row8) * D + blk * 64);
+      }
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) vv[i] = lds128(vc + (8 * (4 * i + cw) + row8) * 64);
+      mbar_wait(smem_u32(&empty_b[r.slot]), r.phase ^ 1u, err, kErrEmptyWait);
       const uint32_t kb = ring + r.slot * kStageBytesKv<D>, vb = kb + 64 * D * 2;
       const bool plain = si.from <= 0 && si.to >= 64 && !si.some;
       if (warp == kConv && lane == 0) info[r.slot] = PageInfo{{0u, 0u}};
-      // Keys: a warp takes 8 positions x 64 dims at a time, values 8 dims x 64 positions: 8 lanes read 128 bytes of
-      // different banks and write 128 bytes of different banks (of two rows; of two blocks of 64 dims where the
-      // rows lie a multiple of 128 bytes apart).
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const int row = 8 * (cw + 4 * (i & 1)) + row8;
         const int blk = D % 128 == 0 ? (i >> 1) ^ (row8 & 1) : i >> 1;
-        store16_f16(kb + blk * 8192 + row * 128, row8, sub, lds128(kc + row * D + blk * 64));
+        store16_f16(kb + blk * 8192 + row * 128, row8, sub, kv[i]);
       }
       if (plain) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const int row = 8 * (4 * i + cw) + row8;
-          store16_f16(vb + row * 128, row8, sub, lds128(vc + row * 64));
-        }
+        for (int i = 0; i < D / 32; ++i) store16_f16(vb + (8 * (4 * i + cw) + row8) * 128, row8, sub, vv[i]);
       } else {
         // what no row sees is not looked at; a NaN that only some rows see reaches those by their weights
         uint32_t keep[4], nan[4] = {0, 0, 0, 0};
