@@ -94,6 +94,17 @@ struct Eight<true> {
   __device__ __forceinline__ void load(const void* p) { w = __ldg(static_cast<const uint4*>(p)); }
   __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void f32(float* f) const { bf16x8_to_f32(w, f); }
+  // largest magnitude as fp32 bits; NaN above infinity above all
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = max2(max2(w.x & kAbs, w.y & kAbs), max2(w.z & kAbs, w.w & kAbs));
+    return max(m << 16, m & 0xFFFF0000u);
+  }
+  static constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  __device__ __forceinline__ static uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
 };
 template <>
 struct Eight<false> {
@@ -107,12 +118,30 @@ struct Eight<false> {
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
     f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   }
+  __device__ __forceinline__ uint32_t top() const {
+    return max(max(max(abs_bits(a.x), abs_bits(a.y)), max(abs_bits(a.z), abs_bits(a.w))),
+               max(max(abs_bits(b.x), abs_bits(b.y)), max(abs_bits(b.z), abs_bits(b.w))));
+  }
 };
 
-// largest finite magnitude, as bits
-__device__ __forceinline__ uint32_t finite_bits(float v) {
-  const uint32_t b = abs_bits(v);
-  return b < 0x7F800000u ? b : 0u;
+// largest finite magnitude of n eights, as bits
+template <bool BF16>
+__device__ __forceinline__ uint32_t finite_top(const Eight<BF16>* v, int n) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < n; ++i) bits = max(bits, v[i].top());
+  if (bits >= 0x7F800000u) {
+    bits = 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      float f[8];
+      v[i].f32(f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (abs_bits(f[j]) < 0x7F800000u) bits = max(bits, abs_bits(f[j]));
+    }
+  }
+  return bits;
 }
 
 // four codes times f, rounded again
@@ -147,7 +176,6 @@ __device__ __forceinline__ void write_keys(const Unit& u, const unsigned char* x
                                            int head) {
   constexpr int NT = kNt<D>, C = kChunks<D>, ESZ = BF16 ? 2 : 4;
   Eight<BF16> v[C];
-  uint32_t bits = 0;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int at = i * NT + threadIdx.x, r = at / (D / 8), c = at % (D / 8);
@@ -161,13 +189,7 @@ __device__ __forceinline__ void write_keys(const Unit& u, const unsigned char* x
   const int64_t ph = (int64_t)u.page * cache.heads + head;
   uint8_t *page = cache.k + ph * 64 * D, *scale = cache.ks + ph;
   const uint32_t old_byte = u.lo > 0 ? *scale : 0u;
-#pragma unroll
-  for (int i = 0; i < C; ++i) {
-    float f[8];
-    v[i].f32(f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) bits = max(bits, finite_bits(f[j]));
-  }
+  const uint32_t bits = finite_top(v, C);
   float shrink;
   const int e = page_exp<NT>(bits, u.lo > 0, old_byte, &shrink);
   const float s = pow2i(-e);
@@ -195,7 +217,6 @@ __device__ __forceinline__ void write_values(const Unit& u, const unsigned char*
   constexpr int NT = kNt<D>, C = kChunks<D> / 4, ESZ = BF16 ? 2 : 4;
   static_assert(C * NT == 16 * (D / 8), "whole quads of rows");
   Eight<BF16> v[C][4];
-  uint32_t bits = 0;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int at = i * NT + threadIdx.x, r0 = at % 16 * 4, c = at / 16;
@@ -213,15 +234,7 @@ __device__ __forceinline__ void write_values(const Unit& u, const unsigned char*
   const int64_t ph = (int64_t)u.page * cache.heads + head;
   uint8_t *page = cache.v + ph * 64 * D, *scale = cache.vs + ph;
   const uint32_t old_byte = u.lo > 0 ? *scale : 0u;
-#pragma unroll
-  for (int i = 0; i < C; ++i)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float f[8];
-      v[i][q].f32(f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) bits = max(bits, finite_bits(f[j]));
-    }
+  const uint32_t bits = finite_top(&v[0][0], 4 * C);
   float shrink;
   const int e = page_exp<NT>(bits, u.lo > 0, old_byte, &shrink);
   const float s = pow2i(-e);
