@@ -13,16 +13,26 @@
 //   1 warp                 issues the products
 //   1 warp                 copies pages (bulk copies of 64 dim bytes) into a ring of codes
 //   4 warps                codes -> f16
-//   8 warps a tile         softmax: a warp owns 16 rows, a thread 16 of the 64 scores of two of them
-// The softmax of a page is a long chain of few instructions for its warps (an
-// exchange of maxima between 4 lanes, 32 exponentials a thread), so many warps
-// share it: with 4 warps a tile and a row a thread, a page of two tiles took 2220
-// cycles, the products 1024.
+//   4 warps a tile         softmax: a thread owns a row
 // dim <= 128, NG = 2: two tiles of 128 rows take turns, so the tensor cores work
-// on one while the other's scores become weights in their place.  Where a (row
-// tile, head) has 128 rows or fewer, the two tiles' warps take its even and odd
-// pages instead and the first ones add both results up at the end.  dim > 128, NG =
-// 1: the output takes half of the tensor memory; one tile, two buffers of scores.
+// on one while the other's scores become weights.  Where a (row tile, head) has
+// 128 rows or fewer, the two tiles' warps take its even and odd pages instead and
+// the first ones add both results up at the end.  dim > 128, NG = 1: the output
+// takes half of the tensor memory; one tile, two buffers of scores.
+//
+// What bounds it: 4096 new tokens on 8192, 64 query heads of 128 over 8: 1272 us,
+// 1080 TFLOP/s, 0.56 of the measured bf16 rate; a page of two tiles takes 2200
+// cycles, of which the products are 1024 (tensor pipe 46 % active).  The rest is
+// latency: a tile's page goes products -> scores -> weights -> products in turn
+// (reading scores 60 cycles, their maximum 270, the exponentials 450, storing and
+// handing on 120, the products 512), the tensor memory has no room for more than
+// one page of scores a tile, and the warps wait for instructions as much as they
+// issue them (IPC 1.8).  Tried and slower: weights beside the scores, whose buffer
+// both tiles share (1288 us); 8 softmax warps a tile with half the scores a thread
+// (1829); the products issued by one thread (2074), by two warps (1288), or by
+// several specialized instruction sequences (1477).  20 rows a head (32 x 4 tokens on
+// 6000, groups of 5) 97 us where the cache's bytes take 38: a page takes the conversion
+// 1080 cycles and the issuing warp 990 where memory would allow 700.
 //
 // The weights' reference M is not raised for less than 2^8 (weights up to 2^8
 // fit f16 as well), which leaves few rescalings of O in tensor memory.
@@ -87,8 +97,10 @@ __host__ __device__ constexpr uint32_t idesc_f16(int n) {
 
 // What the products' warp issues for a page and tile, by one election: P V into the output (o, from the weights at
 // p and the values at vd; add: not the first page), then its arrivals, then the scores of a later page (s, from the
-// queries at q and the keys at kd) with theirs.  An election for each product took 94 cycles whatever its size; so
-// a product of N columns takes its N / 2 cycles.
+// queries at q and the keys at kd) with theirs.  An election for each product took 94 cycles whatever its size; with
+// one for all, nothing else on the SM, a product of N columns takes its N / 2 cycles.  What is left out is left out by
+// predicates: a second copy of the sequence would cost more than it saves, the SM's instruction cache being what is
+// short.
 #define RN_PV(A, B, ACC) \
   "add.u32 ra, %1, " #A ";\n\tadd.u64 rb, %2, " #B ";\n\t" \
   "@po tcgen05.mma.cta_group::1.kind::f16 [%0], [ra], rb, %3, " ACC ";\n\t"
