@@ -427,7 +427,7 @@ rn_status rn_quantize_only(const float* y, int64_t N, int64_t H,
  *   k_scales  E8M0 bytes [pages, heads]: an element stands for its code's
  *   v_scales  value * 2^(byte - 127)
  * All are the caller's and need not be initialized.  k and v 16-byte aligned; dim
- * 64, 128, 192 or 256; up to 65535 heads.
+ * 64, 128, 192 or 256; up to 65535 heads and 2^31 - 1 pages.
  */
 #define RN_KV_PAGE 64
 typedef struct {
@@ -457,7 +457,8 @@ typedef struct {
  * whose position is negative.  starts are cut to [0, tokens], so that no
  * contents of the arrays lead out of the caller's memory; starts that descend
  * give unspecified results.  Up to 2^24 sequences, 2^30 - 1 rows and 2^25 - 1
- * blocks a sequence.
+ * blocks a sequence.  The write and the read launch 2 * heads * (tokens / 64 +
+ * 2 * sequences) units, which must stay below 2^31.
  */
 typedef struct {
   const int32_t* table;
@@ -509,7 +510,9 @@ rn_status rn_kv_cache_read(const rn_kv_cache* cache, const rn_kv_seqs* seqs, voi
  *        query that sees nothing gets 0
  *   lse  fp32 [tokens, q_heads] or NULL: log(sum of exp(s)), -infinity where
  *        nothing is seen
- * scale > 0.  Scores and sums are fp32; the weights are rounded once to 11
+ * 0 < scale <= 1e30; softcap 0 or in [1e-30, 1e30]; up to 4096 query heads a
+ * head of the cache, tokens * G below 2^30.  out and lse must not overlap the
+ * inputs.  Scores and sums are fp32; the weights are rounded once to 11
  * significant bits, the output once to bf16.  The sums are the tensor cores'
  * fp32, which cut off instead of rounding.  What a query does not see has no part in its
  * output, whatever it holds; outputs of queries that see a NaN, or hold a

@@ -728,10 +728,9 @@ def kv_cache_write(cache, seqs, k, v):
     slice of a joint projection) into the pages of their sequences, in place."""
     lib = _lib or _load()
     dev = torch.cuda.current_device()
-    if k is None:
-        raise RNError("k is required")
-    c, q = _kv_args(cache, seqs, k.shape[0], dev)
+    c, q = _kv_args(cache, seqs, 0, dev)
     ks = _kv_rows(k, "k", c.heads, c.dim, dev, (_BF, _FP32))
+    q.tokens = k.shape[0]
     vs = _kv_rows(v, "v", c.heads, c.dim, dev, (k.dtype,))
     if v.shape[0] != k.shape[0]:
         raise RNError(f"v must have shape {tuple(k.shape)}, got {tuple(v.shape)}")
@@ -747,6 +746,8 @@ def kv_cache_read(cache, seqs, tokens, out_dtype=torch.bfloat16):
     lib = _lib or _load()
     dev = torch.cuda.current_device()
     c, q = _kv_args(cache, seqs, int(tokens), dev)
+    if tokens < 0:
+        raise RNError(f"tokens must not be negative, got {tokens}")
     shape = (q.tokens, c.heads, c.dim)
     k = torch.empty(shape, dtype=out_dtype, device=cache.k.device)
     v = torch.empty(shape, dtype=out_dtype, device=cache.k.device)
@@ -782,13 +783,13 @@ def kv_attention(q, cache, seqs, scale=None, causal=True, window=0, softcap=0.0,
     uninitialized."""
     lib = _lib or _load()
     dev = torch.cuda.current_device()
-    if q is None:
-        raise RNError("q is required")
-    c, s = _kv_args(cache, seqs, q.shape[0], dev)
-    if q.dim() != 3 or c.heads == 0 or q.shape[1] % c.heads or q.shape[1] == 0:
-        raise RNError(f"q must have shape (tokens, a multiple of {c.heads}, {c.dim}), got {tuple(q.shape)}")
-    T, heads, D = q.shape
+    c, s = _kv_args(cache, seqs, 0, dev)
+    heads = q.shape[1] if getattr(q, "is_cuda", False) and q.dim() == 3 else c.heads
     qs = _kv_rows(q, "q", heads, c.dim, dev, (_BF,))
+    if heads == 0 or heads % c.heads:
+        raise RNError(f"q must have shape (tokens, a multiple of {c.heads}, {c.dim}), got {tuple(q.shape)}")
+    T, _, D = q.shape
+    s.tokens = T
     if slopes is not None:
         _need(slopes, "slopes", _FP32, (heads,))
     need = _kv_attention_bytes(T, heads, s.sequences, c.heads, c.dim)

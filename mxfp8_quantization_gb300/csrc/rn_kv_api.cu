@@ -102,7 +102,7 @@ rn_status rn_kv_attention(const void* q, rn_dtype dtype, int64_t q_stride, int64
   rn_status st;
   if ((st = check_cache(cache, &p.c)) != RN_OK || (st = check_seqs(seqs, &p.q)) != RN_OK) return st;
   if (!dtype_ok(dtype) || q_heads < 1 || q_heads % p.c.heads != 0 || !(scale > 0.0f) || scale > 1e30f || window < 0 ||
-      !(softcap >= 0.0f) || softcap > 1e30f)
+      !(softcap == 0.0f || softcap >= 1e-30f) || softcap > 1e30f)
     return RN_ERR_INVALID;
   const int64_t group = q_heads / p.c.heads;
   if (dtype != RN_BF16 || group > 4096 || p.q.tokens * group > INT32_MAX / 2) return RN_ERR_UNSUPPORTED;
@@ -127,7 +127,7 @@ rn_status rn_kv_attention(const void* q, rn_dtype dtype, int64_t q_stride, int64
   p.group = fast_div((int)group);
   p.scale = scale;
   p.causal = causal != 0;
-  p.window = window > INT32_MAX / 2 ? 0 : (int)window;  // no position is that far away
+  p.window = window > INT32_MAX ? 0 : (int)window;  // no position is that far away
   p.softcap = softcap;
   p.slopes = slopes;
   p.out = out;

@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
         const int rr = it.r0 + min(n * 8 + 2 * t + j, it.rows - 1), i = quot(rr, p.group);
         row_p[n][j] = it.p0 + i;
         row_hi[n][j] = p.causal ? row_p[n][j] + 1 : it.len;
-        row_lo[n][j] = p.window > 0 ? row_p[n][j] - p.window + 1 : 0;
+        row_lo[n][j] = first_seen(row_p[n][j], p.window);
         if constexpr (EXTRA)
           slope[n][j] =
               p.slopes != nullptr ? __ldg(p.slopes + head * p.group.d + rr - i * p.group.d) * kLog2e : 0.0f;
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
     // every row sees [all_lo, all_hi)
     const int i0 = quot(it.r0, p.group), i1 = quot(it.r0 + it.rows - 1, p.group);
     const int all_hi = p.causal ? it.p0 + i0 + 1 : it.len;
-    const int all_lo = p.window > 0 ? it.p0 + i1 - p.window + 1 : 0;
+    const int all_lo = first_seen(it.p0 + i1, p.window);
     const bool several = i1 > i0;
 
     float m[NB][2], M[NB][2], l[NB][2], o[NB][D / 16][4];

@@ -44,6 +44,9 @@ struct Plan {
   int reach;          // positions that the page table has room for
 };
 
+// the first position that a query at p sees
+__device__ __forceinline__ int first_seen(int p, int window) { return window > 0 && p >= window ? p - window + 1 : 0; }
+
 template <int R>
 __device__ __forceinline__ int item_base(const Plan& a, int b) {
   return (int)((int64_t)min(max(a.starts[b], 0), a.tokens) * a.group.d / R) + b;
@@ -75,7 +78,7 @@ __device__ __forceinline__ Item item_at(const Plan& a, int i) {
   t.p0 = t.len - n;
   const int i0 = quot(t.r0, a.group), i1 = quot(t.r0 + t.rows - 1, a.group);
   t.hi = min(a.causal ? max(t.p0 + i1 + 1, 0) : t.len, a.reach);
-  t.lo = a.window > 0 ? max(t.p0 + i0 - a.window + 1, 0) : 0;
+  t.lo = first_seen(t.p0 + i0, a.window);
   t.blk0 = t.lo >> 6;
   t.nblk = t.hi > t.lo ? ((t.hi - 1) >> 6) - t.blk0 + 1 : 1;
   return t;

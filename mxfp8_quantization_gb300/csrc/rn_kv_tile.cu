@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
           const int base = (it.blk0 + at.blk) * 64;
           const int i0 = quot(it.r0, p.group), i1 = quot(it.r0 + it.rows - 1, p.group);
           const bool some = i1 > i0 && (base + 64 > (p.causal ? it.p0 + i0 + 1 : it.len) ||
-                                        (p.window > 0 && base < it.p0 + i1 - p.window + 1));
+                                        base < first_seen(it.p0 + i1, p.window));
           slot_info[r.slot] = SlotInfo{max(it.lo - base, 0), pg >= 0 ? min(it.hi - base, 64) : 0, some};
           // a page that is none is masked: any other stands for it
           const int64_t ph = (int64_t)max(pg, 0) * p.c.heads + at.head;
@@ -492,9 +492,9 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&q_b));
       const int pos0 = it.p0 + qi;
-      const int row_hi = p.causal ? pos0 + 1 : it.len, row_lo = p.window > 0 ? pos0 - p.window + 1 : 0;
+      const int row_hi = p.causal ? pos0 + 1 : it.len, row_lo = first_seen(pos0, p.window);
       const int i0 = quot(it.r0, p.group), i1 = quot(it.r0 + it.rows - 1, p.group);
-      const int all_hi = p.causal ? it.p0 + i0 + 1 : it.len, all_lo = p.window > 0 ? it.p0 + i1 - p.window + 1 : 0;
+      const int all_hi = p.causal ? it.p0 + i0 + 1 : it.len, all_lo = first_seen(it.p0 + i1, p.window);
       float slope = 0.0f;
       if constexpr (EXTRA)
         if (p.slopes != nullptr) slope = __ldg(p.slopes + qh) * kLog2e;

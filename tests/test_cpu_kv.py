@@ -83,6 +83,13 @@ def test_read_refusals(lib):
     assert read(lib, c, s, k=0x10008) == 2 and read(lib, c, s, v=0x20004) == 2
 
 
+def test_grids_past_31_bits(lib):
+    for call in (write, read):
+        wide = dict(ks=1 << 24, vs=1 << 24) if call is write else {}
+        for heads, kw in ((65535, dict(sequences=8193)), (65535, dict(tokens=1 << 21)), (64, dict(tokens=(1 << 30) - 1))):
+            assert call(lib, cache(heads=heads), seqs(**kw), **wide) == 2, kw
+
+
 def test_attention_refusals(lib):
     c, s = cache(), seqs()
     nan, inf = float("nan"), float("inf")
@@ -90,7 +97,7 @@ def test_attention_refusals(lib):
     assert attend(lib, c, s, heads=7) == 1 and attend(lib, c, s, heads=0) == 1
     for scale in (0.0, -1.0, nan, inf):
         assert attend(lib, c, s, scale=scale) == 1
-    for cap in (-1.0, nan, inf):
+    for cap in (-1.0, nan, inf, 1e-38):
         assert attend(lib, c, s, cap=cap) == 1
     assert attend(lib, c, s, window=-1) == 1
     assert attend(lib, c, s, stride=1016) == 1
@@ -100,6 +107,9 @@ def test_attention_refusals(lib):
     assert attend(lib, c, s, q=0x10004) == 2 and attend(lib, c, s, out=0x20008) == 2
     assert attend(lib, c, s, lse=0x40001) == 2 and attend(lib, c, s, slopes=0x40002) == 2
     assert attend(lib, c, s, ws=0x30008) == 2
+    assert attend(lib, c, seqs(tokens=1 << 28)) == 2                         # 2^30 rows of a head
+    for kw in (dict(scale=1.1e30), dict(cap=1.1e30)):
+        assert attend(lib, c, s, **kw) == 1
     need = rn.kv_attention_workspace_bytes(7, 8, 3, 2, 128)
     assert need > 0
     assert attend(lib, c, s, ws=0) == 3 and attend(lib, c, s, n=need - 1) == 3
@@ -189,6 +199,15 @@ def test_binding_refuses_rows(lib, device0):
             rn.kv_cache_write(c, s, bad, good)
         with pytest.raises(rn.RNError, match=text):
             rn.kv_attention(bad, c, s)
+    for bad in (Fake(BF, 7), Fake(BF, 7, 2, 128, 1), "q"):
+        with pytest.raises(rn.RNError, match="shape|CUDA"):
+            rn.kv_attention(bad, c, s)
+        with pytest.raises(rn.RNError, match="shape|CUDA"):
+            rn.kv_cache_write(c, s, bad, good)
+    with pytest.raises(rn.RNError, match="multiple of 2"):
+        rn.kv_attention(Fake(BF, 7, 3, 128), c, s)
+    with pytest.raises(rn.RNError, match="negative"):
+        rn.kv_cache_read(c, s, -1)
     with pytest.raises(rn.RNError, match="v must have shape"):
         rn.kv_cache_write(c, s, good, Fake(BF, 6, 2, 128))
     with pytest.raises(rn.RNError, match="v must be"):

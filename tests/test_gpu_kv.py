@@ -323,6 +323,24 @@ def test_what_arrays_may_hold():
     assert torch.equal(c.k, clean.k) and torch.equal(c.k_scales, clean.k_scales)   # no row has a cached position
 
 
+@pytest.mark.parametrize("new", [1, 30])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 40, 2 ** 30, 300, 299])
+def test_windows_as_long_as_the_sequence(new, window):
+    c, s, T = make([300, 40], [new, new], 2, 64, seed=14)
+    q = randn(T, 4, 64)
+    out = rn.kv_attention(q, c, s, window=window)
+    check(out, None, reference(q, c, s, window=min(window, 10 ** 6)), 64)
+    if window >= 300:
+        assert torch.equal(out, rn.kv_attention(q, c, s))
+
+
+@pytest.mark.parametrize("group", [37, 100, 300])
+def test_large_groups(group):
+    c, s, T = make([200, 64, 5], [1, 2, 1], 1, 64, seed=15)
+    q = randn(T, group, 64)
+    check(rn.kv_attention(q, c, s), None, reference(q, c, s), 64)
+
+
 def test_no_rows():
     c, s, _ = make([100], [1], 2, 64)
     s.starts.zero_()
