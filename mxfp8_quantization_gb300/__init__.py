@@ -792,7 +792,7 @@ def kv_attention(q, cache, seqs, scale=None, causal=True, window=0, softcap=0.0,
     s.tokens = T
     if slopes is not None:
         _need(slopes, "slopes", _FP32, (heads,))
-    need = _kv_attention_bytes(T, heads, s.sequences, c.heads, c.dim)
+    need = _kv_attention_bytes(0, c.heads, 0, c.heads, c.dim)   # the dim decides
     if workspace is None:
         workspace = torch.empty(need, dtype=_U8, device=q.device)
     else:

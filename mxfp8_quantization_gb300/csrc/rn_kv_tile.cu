@@ -31,7 +31,7 @@
 // both tiles share (1288 us); 8 softmax warps a tile with half the scores a thread
 // (1829); the products issued by one thread (2074), by two warps (1288), or by
 // several specialized instruction sequences (1477).  20 rows a head (32 x 4 tokens on
-// 6000, groups of 5) 97 us where the cache's bytes take 38: a page takes the conversion
+// 6000, groups of 5) 98 us where the cache's bytes take 38: a page takes the conversion
 // 1080 cycles and the issuing warp 990 where memory would allow 700.
 //
 // The weights' reference M is not raised for less than 2^8 (weights up to 2^8
