@@ -439,3 +439,23 @@ def test_other_stream():
         out = rn.kv_attention(q, c, s)
     side.synchronize()
     assert big is not None and torch.equal(out, want)
+
+
+def test_calls_on_two_streams_at_once():
+    """Reads and attentions of one cache, of few and of many rows a sequence, each call with a workspace of its own."""
+    calls = []
+    for i, new in enumerate(([1, 1, 1], [40, 2, 100])):
+        c, s, T = make([3000, 150, 700], new, 2, 128, seed=20 + i)
+        calls.append((c, s, T, randn(T, 8, 128, seed=i)))
+    want = [(rn.kv_attention(q, c, s), *rn.kv_cache_read(c, s, T)) for c, s, T, q in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, s, T, q) in enumerate(calls):
+            with torch.cuda.stream(streams[i]):
+                got[i].append((rn.kv_attention(q, c, s), *rn.kv_cache_read(c, s, T)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for one in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(one, want[i]))
