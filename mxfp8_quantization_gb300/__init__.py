@@ -654,24 +654,6 @@ def kv_cache_alloc(pages, heads, dim, device=None) -> KVCache:
                    zeros((pages, heads)))
 
 
-def _kv_ok(cache, seqs, dev):
-    try:
-        k, v, ks, vs = cache.k, cache.v, cache.k_scales, cache.v_scales
-        tb, st, ln = seqs.table, seqs.starts, seqs.lens
-        P, H, n, D = k.shape
-        B, _ = tb.shape
-        return (n == KV_PAGE and v.shape == (P, H, D, KV_PAGE) and ks.shape == (P, H) and vs.shape == (P, H)
-                and st.shape == (B + 1,) and ln.shape == (B,) and k.dtype is _U8 and v.dtype is _U8
-                and ks.dtype is _U8 and vs.dtype is _U8 and tb.dtype is _I32 and st.dtype is _I32
-                and ln.dtype is _I32 and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous()
-                and vs.is_contiguous() and tb.is_contiguous() and st.is_contiguous() and ln.is_contiguous()
-                and k.is_cuda and k.device.index == dev and v.device.index == dev and ks.device.index == dev
-                and vs.device.index == dev and tb.device.index == dev and st.device.index == dev
-                and ln.device.index == dev)
-    except (AttributeError, ValueError):
-        return False
-
-
 def _refuse_kv(cache, seqs):
     if not hasattr(cache, "k_scales"):
         raise RNError(f"cache must be a KVCache, got {type(cache).__name__}")
@@ -691,36 +673,48 @@ def _refuse_kv(cache, seqs):
 
 
 def _kv_args(cache, seqs, tokens, dev):
-    if not _kv_ok(cache, seqs, dev):
-        _refuse_kv(cache, seqs)
-    k = cache.k
-    P, H, _, D = k.shape
-    B, width = seqs.table.shape
-    return (_KVCache(k.data_ptr(), cache.v.data_ptr(), cache.k_scales.data_ptr(), cache.v_scales.data_ptr(), P, H, D),
-            _KVSeqs(seqs.table.data_ptr(), seqs.starts.data_ptr(), seqs.lens.data_ptr(), B, width, tokens))
+    """The C structures of a cache and of a call's sequences."""
+    try:
+        k, v, ks, vs = cache.k, cache.v, cache.k_scales, cache.v_scales
+        tb, st, ln = seqs.table, seqs.starts, seqs.lens
+        P, H, n, D = k.shape
+        B, width = tb.shape
+        if (n == KV_PAGE and v.shape == (P, H, D, KV_PAGE) and ks.shape == (P, H) and vs.shape == (P, H)
+                and st.shape == (B + 1,) and ln.shape == (B,) and k.dtype is _U8 and v.dtype is _U8
+                and ks.dtype is _U8 and vs.dtype is _U8 and tb.dtype is _I32 and st.dtype is _I32
+                and ln.dtype is _I32 and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous()
+                and vs.is_contiguous() and tb.is_contiguous() and st.is_contiguous() and ln.is_contiguous()
+                and k.is_cuda and k.device.index == dev and v.device.index == dev and ks.device.index == dev
+                and vs.device.index == dev and tb.device.index == dev and st.device.index == dev
+                and ln.device.index == dev):
+            return (_KVCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), P, H, D),
+                    _KVSeqs(tb.data_ptr(), st.data_ptr(), ln.data_ptr(), B, width, tokens))
+    except (AttributeError, ValueError):
+        pass
+    _refuse_kv(cache, seqs)
 
 
 def _kv_rows(t, name, heads, dim, dev, dtypes):
-    """The distance of the rows of t [tokens, heads, dim], whose heads and dims are contiguous."""
+    """The distance of the rows of t [tokens, heads, dim], whose heads and dims are contiguous, and their number."""
     try:
-        ok = (t.dtype in dtypes and t.is_cuda and t.device.index == dev and t.shape[1:] == (heads, dim)
-              and t.dim() == 3 and (t.stride(2) == 1 or t.numel() == 0) and (heads == 1 or t.stride(1) == dim
-                                                                            or t.numel() == 0))
-    except AttributeError:
-        ok = False
-    if not ok:
-        if t is None:
-            raise RNError(f"{name} is required")
-        if not getattr(t, "is_cuda", False):
-            raise RNError(f"{name} must be a CUDA tensor")
-        if t.device.index != dev:
-            raise RNError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
-        if t.dtype not in dtypes:
-            raise RNError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-        if t.dim() != 3 or t.shape[1:] != (heads, dim):
-            raise RNError(f"{name} must have shape (tokens, {heads}, {dim}), got {tuple(t.shape)}")
-        raise RNError(f"the heads and dims of {name} must be contiguous (its rows may lie apart)")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+        T, h, d = t.shape
+        row, hs, ds = t.stride()
+        if (h == heads and d == dim and t.dtype in dtypes and t.is_cuda and t.device.index == dev
+                and (ds == 1 and (h == 1 or hs == d) or T == 0)):
+            return row if T > 1 else h * d, T
+    except (AttributeError, ValueError, TypeError):
+        pass
+    if t is None:
+        raise RNError(f"{name} is required")
+    if not getattr(t, "is_cuda", False):
+        raise RNError(f"{name} must be a CUDA tensor")
+    if t.device.index != dev:
+        raise RNError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+    if t.dtype not in dtypes:
+        raise RNError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1:] != (heads, dim):
+        raise RNError(f"{name} must have shape (tokens, {heads}, {dim}), got {tuple(t.shape)}")
+    raise RNError(f"the heads and dims of {name} must be contiguous (its rows may lie apart)")
 
 
 def kv_cache_write(cache, seqs, k, v):
@@ -729,10 +723,11 @@ def kv_cache_write(cache, seqs, k, v):
     lib = _lib or _load()
     dev = torch.cuda.current_device()
     c, q = _kv_args(cache, seqs, 0, dev)
-    ks = _kv_rows(k, "k", c.heads, c.dim, dev, (_BF, _FP32))
-    q.tokens = k.shape[0]
-    vs = _kv_rows(v, "v", c.heads, c.dim, dev, (k.dtype,))
-    if v.shape[0] != k.shape[0]:
+    heads, dim = c.heads, c.dim
+    ks, T = _kv_rows(k, "k", heads, dim, dev, (_BF, _FP32))
+    vs, vT = _kv_rows(v, "v", heads, dim, dev, (k.dtype,))
+    q.tokens = T
+    if vT != T:
         raise RNError(f"v must have shape {tuple(k.shape)}, got {tuple(v.shape)}")
     st = lib.rn_kv_cache_write(k.data_ptr(), v.data_ptr(), _BF16 if k.dtype is _BF else _F32, ks, vs, c, q,
                                _raw_stream(dev))
@@ -784,15 +779,15 @@ def kv_attention(q, cache, seqs, scale=None, causal=True, window=0, softcap=0.0,
     lib = _lib or _load()
     dev = torch.cuda.current_device()
     c, s = _kv_args(cache, seqs, 0, dev)
-    heads = q.shape[1] if getattr(q, "is_cuda", False) and q.dim() == 3 else c.heads
-    qs = _kv_rows(q, "q", heads, c.dim, dev, (_BF,))
-    if heads == 0 or heads % c.heads:
-        raise RNError(f"q must have shape (tokens, a multiple of {c.heads}, {c.dim}), got {tuple(q.shape)}")
-    T, _, D = q.shape
+    H, D = c.heads, c.dim
+    heads = q.shape[1] if getattr(q, "is_cuda", False) and q.dim() == 3 else H
+    qs, T = _kv_rows(q, "q", heads, D, dev, (_BF,))
+    if heads == 0 or H == 0 or heads % H:
+        raise RNError(f"q must have shape (tokens, a multiple of {H}, {D}), got {tuple(q.shape)}")
     s.tokens = T
     if slopes is not None:
         _need(slopes, "slopes", _FP32, (heads,))
-    need = _kv_attention_bytes(0, c.heads, 0, c.heads, c.dim)   # the dim decides
+    need = _kv_attention_bytes(0, H, 0, H, D)   # the dim decides
     if workspace is None:
         workspace = torch.empty(need, dtype=_U8, device=q.device)
     else:

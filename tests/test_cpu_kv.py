@@ -141,8 +141,8 @@ class Fake:
     def dim(self):
         return len(self.shape)
 
-    def stride(self, i):
-        return self._s[i]
+    def stride(self, i=None):
+        return self._s if i is None else self._s[i]
 
     def numel(self):
         return self.shape.numel()
