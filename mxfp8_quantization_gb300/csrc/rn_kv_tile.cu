@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
   __shared__ uint32_t tmem_at;
   __shared__ PageInfo info[NS];
   __shared__ SlotInfo slot_info[NC];
-  __shared__ Stats other[128];
+  __shared__ Stats other[2][128];
   __shared__ Ranges<1, NT / 32> sh;
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
@@ -442,6 +442,9 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
     const int in_tile = (warp & 3) * 32 + lane;
     uint32_t done0 = 0, done1 = 0;                       // pages of the buffers so far (NG = 2: of the tile's)
     RingPos r{0, 0};
+    // Whose turn it is of `other`: a segment of one page asks nothing of the odd warps, so they may be at the next
+    // one's statistics before the even warps have read these; they wait for them at that one's barrier.
+    int turn = 0;
     while (at.left > 0) {
       const Item& it = at.it;
       const int head = at.head, cnt = at.segment();
@@ -639,11 +642,15 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
       tc_fence_after();
       float mo = -INFINITY, Mo = -INFINITY, lo = 0.0f;   // of the odd pages
       if (split) {
-        if (x == 1) other[in_tile] = Stats{m, M, l};
+        if (x == 1) other[turn][in_tile] = Stats{m, M, l};
         tc_fence_before();
         asm volatile("bar.sync 1, 256;" ::: "memory");
         tc_fence_after();
-        if (x == 0) mo = other[in_tile].m, Mo = other[in_tile].M, lo = other[in_tile].l;
+        if (x == 0) {
+          const Stats odd_ones = other[turn][in_tile];
+          mo = odd_ones.m, Mo = odd_ones.M, lo = odd_ones.l;
+        }
+        turn ^= 1;
       }
       if (!(split && x == 1)) {
         const bool odd = split && cnt > 1;
