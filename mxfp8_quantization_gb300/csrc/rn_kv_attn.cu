@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
     for (int i = 0; i < n; ++i) issue();
   };
   if (lane == 0) ends_of[warp] = WorkerEnd{};
+  const float inv_cap = EXTRA ? 1.0f / p.softcap : 0.0f;
   while (at.left > 0) {
     const Item& it = at.it;
     const int head = at.head, blk = at.blk;
@@ -466,17 +467,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
       uint32_t pw[NB][4][2];
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        float top[2] = {-INFINITY, -INFINITY};
+        float top[2] = {-INFINITY, -INFINITY}, score[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) score[i] = s[n][i >> 2][i & 3] * (qs[n][i & 1] * unit);
+        if constexpr (EXTRA)
+          if (p.softcap > 0.0f) cap_scores(score, p.softcap, inv_cap);
 #pragma unroll
         for (int st = 0; st < 4; ++st)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = i & 1, pos = base + 16 * (g >> 1) + 4 * st + 2 * (i >> 1) + (g & 1);
-            float z = s[n][st][i] * (qs[n][j] * unit);
-            if constexpr (EXTRA) {
-              if (p.softcap > 0.0f) z = capped(z, p.softcap, 2.0f * kLog2e / p.softcap);
-              z = fmaf(slope[n][j], (float)(pos - row_p[n][j]), z * kLog2e);
-            }
+            float z = score[4 * st + i];
+            if constexpr (EXTRA) z = fmaf(slope[n][j], (float)(pos - row_p[n][j]), z * kLog2e);
             if (edge && !(there && pos >= row_lo[n][j] && pos < row_hi[n][j])) z = -INFINITY;
             s[n][st][i] = z;
             top[j] = fmaxf(top[j], z);

@@ -307,10 +307,30 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// c tanh(z / c) = c - 2 c / (e^(2 z / c) + 1): absolute error about c 2^-22
-__device__ __forceinline__ float capped(float z, float cap, float two_over_cap_log2) {
-  const float x = z * two_over_cap_log2;
-  return cap - __fdividef(2.0f * cap, ex2(x > 126.0f ? 126.0f : x) + 1.0f);
+// c tanh(z / c), its error relative to the result.  From z / c = 1/4 on c - 2 c / (e^(2 z / c) + 1), off by c 2^-21 at
+// most (e's 2^-22 and its argument's 3 2^-24, the quotient's 2^-22), 2^-19 of tanh(1/4).  Below, where that cancels,
+// the series z (1 - y^2 / 3 + 2 y^4 / 15 - 17 y^6 / 315 + 62 y^8 / 2835) in y = z / c; its next term is 2^-26.
+__device__ __forceinline__ float capped_near(float z, float inv_cap) {
+  const float y = z * inv_cap, y2 = y * y;
+  return fmaf(z, fmaf(y2, fmaf(y2, fmaf(y2, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f), -1.0f / 3.0f) * y2, z);
+}
+__device__ __forceinline__ float capped(float z, float cap, float inv_cap) {
+  const float y = fabsf(z) * inv_cap, x = y * (2.0f * kLog2e);
+  const float far = cap - __fdividef(2.0f * cap, ex2(x > 126.0f ? 126.0f : x) + 1.0f);
+  return y < 0.25f ? capped_near(z, inv_cap) : copysignf(far, z);
+}
+// 16 scores of each lane of a converged warp; the series alone where that does for all
+__device__ __forceinline__ void cap_scores(float (&z)[16], float cap, float inv_cap) {
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(z[i]));
+  if (__any_sync(0xFFFFFFFFu, top * inv_cap >= 0.25f)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = capped(z[i], cap, inv_cap);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = capped_near(z[i], inv_cap);
+  }
 }
 
 // joins the partial results of tiles of `rows` rows left by `ctas` CTAs

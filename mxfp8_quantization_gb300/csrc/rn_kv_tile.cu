@@ -166,6 +166,29 @@ __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// 16 columns of it, both ways
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_store16(uint32_t taddr, const float (&v)[16]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -533,26 +556,39 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
         mbar_wait(smem_u32(&s_b[buf]), (NG == 2 || buf == 0 ? done0 : done1) & 1, err, kErrStatsWait);
         __syncwarp();
         tc_fence_after();
+        if constexpr (EXTRA) {
+          // Capped and biased 16 at a time, back where they were: as a part of the 64 below, this would be four times
+          // the instructions, more than the SM's instruction cache holds.
+          const float inv_cap = 1.0f / p.softcap;
+#pragma unroll 1
+          for (int h = 0; h < 64; h += 16) {
+            float z[16];
+            tmem_load16(ts + h, z);
+            tmem_load_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[i] *= f;
+            if (p.softcap > 0.0f) cap_scores(z, p.softcap, inv_cap);
+            const float away = (float)(base + h - pos0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[i] = fmaf(slope, away + (float)i, z[i] * kLog2e);
+            tmem_store16(ts + h, z);
+          }
+          tmem_store_wait();
+        }
         float s[64];
         tmem_load32(ts, reinterpret_cast<float(&)[32]>(s));
         tmem_load32(ts + 32, reinterpret_cast<float(&)[32]>(s[32]));
         tmem_load_wait();
-        float mul = f;
-        if (EXTRA || edge) {
+        float mul = EXTRA ? 1.0f : f;
+        if (edge) {
           mul = 1.0f;
 #pragma unroll
           for (int i = 0; i < 64; ++i) {
             const int pos = base + i;
-            float z = s[i] * f;
-            if constexpr (EXTRA) {
-              if (p.softcap > 0.0f) z = capped(z, p.softcap, 2.0f * kLog2e / p.softcap);
-              z = fmaf(slope, (float)(pos - pos0), z * kLog2e);
-            }
-            if (edge) {
-              const bool sees = there && pos >= row_lo && pos < row_hi;
-              if (nan[i >> 5] >> (i & 31) & 1) z = __uint_as_float(0x7FC00000u);
-              if (!sees) z = -INFINITY;
-            }
+            float z = EXTRA ? s[i] : s[i] * f;
+            const bool sees = there && pos >= row_lo && pos < row_hi;
+            if (nan[i >> 5] >> (i & 31) & 1) z = __uint_as_float(0x7FC00000u);
+            if (!sees) z = -INFINITY;
             s[i] = z;
           }
         }
