@@ -595,7 +595,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
       for (int j = 0; j < 2; ++j) {
         const float sum = sum_g(l[n][j]);
         // the sum of the weights is never 0 where a row sees a position; NaN stays
-        const float inv = sum == 0.0f ? 0.0f : ex2(M[n][j] - m[n][j]) / sum;
+        // 2^(M - m) in two halves, as it may be below the normal floats where the values of the pages are least
+        const float half = sum == 0.0f ? 0.0f : ex2(0.5f * (M[n][j] - m[n][j]));
+        const float inv = sum == 0.0f ? 0.0f : half / sum;
         const float log2s = sum == 0.0f ? -INFINITY : m[n][j] + log2f(sum);
         const int r = n * 8 + 2 * t + j;
         if (r >= it.rows) continue;
@@ -606,13 +608,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
           for (int d = 0; d < D / 16; ++d)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-              out[16 * d + 8 * i] = (uint16_t)pack_bf16x2(o[n][d][2 * i + j] * inv, 0.0f);
+              out[16 * d + 8 * i] = (uint16_t)pack_bf16x2(o[n][d][2 * i + j] * inv * half, 0.0f);
           if (p.lse != nullptr && g == 0) p.lse[row] = log2s * kLn2;
         } else {
 #pragma unroll
           for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) part[r * D + 16 * d + 8 * i + g] = o[n][d][2 * i + j] * inv;
+            for (int i = 0; i < 2; ++i) part[r * D + 16 * d + 8 * i + g] = o[n][d][2 * i + j] * inv * half;
           if (g == 0) part[R * D + r] = log2s;
         }
       }

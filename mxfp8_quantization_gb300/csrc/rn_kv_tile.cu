@@ -693,7 +693,8 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
         const float mm = fmaxf(m, mo), MM = fmaxf(M, Mo);
         const float bm = mm == -INFINITY ? 0.0f : mm, bM = MM == -INFINITY ? 0.0f : MM;
         const float sum = l * ex2(m - bm) + lo * ex2(mo - bm);
-        const float unit = sum == 0.0f ? 0.0f : ex2(bM - bm) / sum;
+        // 2^(M - m) in two halves, as it may be below the normal floats where the values of the pages are least
+        const float half = sum == 0.0f ? 0.0f : ex2(0.5f * (bM - bm)), unit = sum == 0.0f ? 0.0f : half / sum;
         const float fa = unit * ex2(M - bM), fb = unit * ex2(Mo - bM);
         const float log2s = sum == 0.0f ? -INFINITY : bm + log2f(sum);
         const int64_t row = (int64_t)(it.s0 + qi) * (p.c.heads * p.group.d) + qh;
@@ -709,6 +710,7 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
           for (int i = 0; i < 32; ++i) {
             o[i] = sum == 0.0f ? 0.0f : o[i] * fa;
             if (odd) o[i] = sum == 0.0f ? 0.0f : fmaf(u[i], fb, o[i]);
+            o[i] *= half;
           }
           if (!real) continue;
           if (whole) {

@@ -54,6 +54,43 @@ def close(out, lse, want, dim, softcap=0.0):
     assert np.all(err_lse <= tol_lse), float((err_lse / tol_lse).max())
 
 
+def shared(k, v, sequences, new):
+    """A cache of the rows k, v [n, heads, dim] (fp32) that all sequences read, with `new` rows each."""
+    n, heads, dim = k.shape
+    pages = -(-n // 64)
+    c = rn.kv_cache_alloc(pages, heads, dim)
+    i32 = lambda t: torch.tensor(t, dtype=torch.int32, device="cuda")
+    table = i32([list(range(pages))])
+    rn.kv_cache_write(c, rn.KVSequences(table, i32([0, n]), i32([n])), k, v)
+    return c, rn.KVSequences(table.expand(sequences, pages).contiguous(), i32([new * b for b in range(sequences + 1)]),
+                             i32([n] * sequences))
+
+
+def shared_reference(q, c, s, new):
+    """kv_check.reference of `shared`, whose sequences all see every position, in one piece."""
+    n, H, D = int(s.lens[0]), c.k.shape[1], q.shape[2]
+    G, B = q.shape[1] // H, len(s.lens)
+    ids = s.table[0].long()
+    unit = torch.exp2(c.v_scales[ids].double() - 127).T.repeat_interleave(64, 1)[:, None, :n]     # [H, 1, n]
+    k = c.k[ids].view(torch.float8_e4m3fn).double() * torch.exp2(c.k_scales[ids].double() - 127)[..., None, None]
+    k = k.transpose(0, 1).reshape(H, -1, D)[:, :n]
+    codes = c.v[ids].view(torch.float8_e4m3fn).double().permute(1, 0, 3, 2).reshape(H, -1, D)[:, :n]
+    v = codes * unit.transpose(1, 2)
+    x = q.double().view(B * new, H, G, D).permute(1, 0, 2, 3).reshape(H, -1, D)
+    t = D ** -0.5 * (x @ k.transpose(1, 2))
+    lse = torch.logsumexp(t, 2)
+    w = torch.exp(t - lse[..., None])
+    r = {"out": w @ v, "pv": w @ v.abs(), "lse": lse, "big": D ** -0.5 * (x.abs() @ k.abs().transpose(1, 2)).amax(2),
+         "spread": (w * unit).amax(2)[..., None] * codes.abs().sum(1, keepdim=True),
+         "seen": torch.full_like(lse, n)}
+    back = lambda y: y.view(H, B * new, G, *y.shape[2:]).transpose(0, 1).reshape(B * new, H * G, *y.shape[2:])
+    return {name: back(y).cpu().numpy() for name, y in r.items()}
+
+
+# few rows a head (8 at most, 16 at most) and many: (new rows, query heads a head)
+FORMS = [(1, 4), (4, 4), (10, 8)]
+
+
 @pytest.mark.parametrize("cap", [1e-3, 1.0, 8.0, 50.0, 1e3, 1e4, 1e6, 1e12, 1e30])
 @pytest.mark.parametrize("dim,new,group", [(64, 1, 4), (64, 4, 4), (64, 10, 8), (256, 1, 4), (256, 10, 8)])
 def test_caps_of_any_size(dim, new, group, cap):
@@ -61,3 +98,21 @@ def test_caps_of_any_size(dim, new, group, cap):
     q = randn(T, 2 * group, dim, seed=2, std=2.0)
     out, lse = rn.kv_attention(q, c, s, softcap=cap, return_lse=True)
     close(out, lse, reference(q, c, s, softcap=cap), dim, cap)
+
+
+@pytest.mark.parametrize("sequences", [1, 40])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,group", FORMS + [(10, 16)])
+def test_values_at_the_least_scale(new, group, dim, sequences):
+    # scores that rise from page to page by little, values of the smallest pages there are
+    heads = 8 if sequences > 1 else 1
+    g = torch.Generator(device="cuda").manual_seed(7)
+    k, v = (torch.randn(320, heads, dim, device="cuda", generator=g) for _ in "kv")
+    k[..., 0] = (torch.arange(5, device="cuda") * 1.9 * np.log(2) * dim ** 0.5 / 8).repeat_interleave(64)[:, None]
+    v *= 2.0 ** -116
+    c, s = shared(k, v, sequences, new)
+    assert (c.v_scales == 7).all()
+    q = randn(sequences * new, heads * group, dim, seed=8, std=0.1)
+    q[..., 0] = 8.0
+    out, lse = rn.kv_attention(q, c, s, causal=False, return_lse=True)
+    close(out, lse, shared_reference(q, c, s, new), dim)
