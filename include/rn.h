@@ -512,9 +512,10 @@ rn_status rn_kv_cache_read(const rn_kv_cache* cache, const rn_kv_seqs* seqs, voi
  *        nothing is seen
  * 0 < scale <= 1e30; softcap 0 or in [1e-30, 1e30]; up to 4096 query heads a
  * head of the cache, tokens * G below 2^30.  out and lse must not overlap the
- * inputs.  Scores and sums are fp32; the weights are rounded once to 11
- * significant bits, the output once to bf16.  The sums are the tensor cores'
- * fp32, which cut off instead of rounding.  What a query does not see has no part in its
+ * inputs.  Scores and sums are fp32; the weights, times their values' scales, are
+ * rounded once to 11 significant bits (or, below 2^-23 of the row's largest, to
+ * a multiple of 2^-33 of it), the output once to bf16.  The sums are the tensor
+ * cores' fp32, which cut off instead of rounding.  What a query does not see has no part in its
  * output, whatever it holds; outputs of queries that see a NaN, or hold a
  * non-finite value themselves, are unspecified.  Results are the same from run
  * to run.  Workspace protocol as for rn_layernorm_bwd: with workspace and out

@@ -7,8 +7,8 @@
 // One pass over the pages with running maxima and sums.  A page's key scale
 // 2^eK multiplies its scores; its value scale 2^eV goes into the weights:
 // besides the maximum m of the scores a second one, M, of the scores plus eV
-// (in base 2) scales the weights w = 2^(s + eV - M) <= 1 that multiply the
-// value codes, so that no page's contribution is lost in 16 bits however far
+// (in base 2) scales the weights w = 2^(s + eV - M + 15) <= 2^15 that multiply
+// the value codes, so that no page's contribution is lost in 16 bits however far
 // the pages' scales lie apart.  The sum of exp(s - m) is kept in fp32.
 //
 // The products are mma.sync m16n8k16 on f16 with the cache as the 16 rows and
@@ -16,7 +16,8 @@
 // by one conversion a pair, exactly; a query row becomes f16 times the power of
 // two that puts its largest magnitude at 2^14 (what is 2^28 below it loses
 // bits: 2^-39 of the row's largest); weights are rounded to f16, half a step of
-// 2^-11, which the bf16 output's 2^-8 covers.  Sums are fp32.
+// 2^-11 down to 2^-29 of the largest, which the bf16 output's 2^-8 covers.  Sums
+// are fp32.
 //
 // Which positions the rows and which dims the reduction index of a fragment
 // stand for is free as long as both operands agree, so a lane reads 16
@@ -233,6 +234,11 @@ __device__ __forceinline__ void join_rows(int n, int lane, int row0, int rows, i
 }
 
 constexpr int kNoScales = 256;  // no page
+
+// log2 of the largest weight in f16, whose values end at 2^16: the others have 11 bits down to 2^-29 of it, and vanish
+// below 2^-40.  With 2^0 they had them to 2^-14 and vanished below 2^-25, which lost the output of a row whose first
+// position takes 0.995 of the weight and has values near 0.
+constexpr float kTopWeight = 15.0f;
 
 // what the join within the CTA has to know of a worker's range
 struct WorkerEnd {
@@ -492,7 +498,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
           const float base_M = M2 == -INFINITY ? 0.0f : M2;
           l[n][j] *= ex2(m[n][j] - base_m[j]);
           shrink[j] = ex2(M[n][j] - base_M);
-          add[j] = ex2(fminf(base_m[j] + ev - base_M, 126.0f));
+          add[j] = ex2(fminf(base_m[j] + ev - base_M + kTopWeight, 126.0f));
           m[n][j] = m2;
           M[n][j] = M2;
         }
@@ -595,8 +601,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
       for (int j = 0; j < 2; ++j) {
         const float sum = sum_g(l[n][j]);
         // the sum of the weights is never 0 where a row sees a position; NaN stays
-        // 2^(M - m) in two halves, as it may be below the normal floats where the values of the pages are least
-        const float half = sum == 0.0f ? 0.0f : ex2(0.5f * (M[n][j] - m[n][j]));
+        // 2^(M - 15 - m) in two halves, as it may be below the normal floats where the values of the pages are least
+        const float half = sum == 0.0f ? 0.0f : ex2(0.5f * (M[n][j] - kTopWeight - m[n][j]));
         const float inv = sum == 0.0f ? 0.0f : half / sum;
         const float log2s = sum == 0.0f ? -INFINITY : m[n][j] + log2f(sum);
         const int r = n * 8 + 2 * t + j;

@@ -34,14 +34,18 @@ def test_row_tiles_of_one_page_behind_others(dim, group):
 
 
 def bounds(want, dim, softcap=0.0):
-    """kv_check.bounds, without what grows with the cap: its error is relative to the capped score (below 2^-21 of the
-    cap where z / c is above 1/4, whose tanh is 0.245)."""
+    """kv_check.bounds, without what grows with the cap and without what a weight far below the largest loses:
+
+    cap      relative to the capped score: its error is below 2^-21 of the cap where z / c is above 1/4, whose tanh
+             is 0.245
+    weights  the largest stands at 2^9 or above in f16, so half a step of its subnormals, 2^-25, is 2^-34 of it
+    """
     seen = want["seen"].astype(np.float64)
     eps = want["big"] * ((dim + 8) * 2.0 ** -23) + 2.0 ** -20 + (seen / 64 + 2) * 2.0 ** -22
     if softcap:
         eps = eps + np.minimum(want["big"], softcap) * 2.0 ** -18
     part = 2.0 ** -11 + 2 * eps + (seen / 8 + 4) * 2.0 ** -23 + seen * 2.0 ** -24
-    out = want["pv"] * part[..., None] + want["spread"] * 2.0 ** -25
+    out = want["pv"] * part[..., None] + want["spread"] * 2.0 ** -34
     out = out + (np.abs(want["out"]) + out) * 2.0 ** -8
     lse = eps + seen * 2.0 ** -24 + (np.abs(want["lse"]) + 1) * 2.0 ** -22
     return out, lse
@@ -98,6 +102,26 @@ def test_caps_of_any_size(dim, new, group, cap):
     q = randn(T, 2 * group, dim, seed=2, std=2.0)
     out, lse = rn.kv_attention(q, c, s, softcap=cap, return_lse=True)
     close(out, lse, reference(q, c, s, softcap=cap), dim, cap)
+
+
+@pytest.mark.parametrize("at", [0, 1000])
+@pytest.mark.parametrize("nats", [13.0, 16.0, 20.0])
+@pytest.mark.parametrize("dim", [64, 256])
+@pytest.mark.parametrize("new,group", FORMS)
+def test_a_position_that_takes_most_of_the_weight(new, group, dim, nats, at):
+    # with values of 0, so that the output is what the others leave; enough heads for ranges of whole sequences
+    n, heads, B = 2000, 16, (76 if new == 1 else 40 if new == 4 else 12)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn(n, heads, dim, device="cuda", generator=g) for _ in "kv")
+    k[..., 0] = 0.0
+    k[at] = 0.0
+    k[at, :, 0] = nats * dim ** 0.5 / 8
+    v[at] = 0.0
+    c, s = shared(k, v, B, new)
+    q = randn(B * new, heads * group, dim, seed=4, std=0.4)
+    q[..., 0] = 8.0
+    out, lse = rn.kv_attention(q, c, s, causal=False, return_lse=True)
+    close(out, lse, shared_reference(q, c, s, new), dim)
 
 
 @pytest.mark.parametrize("sequences", [1, 40])
