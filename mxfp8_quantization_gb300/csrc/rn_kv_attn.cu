@@ -9,7 +9,7 @@
 // besides the maximum m of the scores a second one, M, of the scores plus eV
 // (in base 2) scales the weights w = 2^(s + eV - M + 15) <= 2^15 that multiply
 // the value codes, so that no page's contribution is lost in 16 bits however far
-// the pages' scales lie apart.  The sum of exp(s - m) is kept in fp32.
+// the pages' scales and scores lie apart.  The sum of exp(s - m) is kept in fp32.
 //
 // The products are mma.sync m16n8k16 on f16 with the cache as the 16 rows and
 // the queries as the 8 columns: S^T = K Q^T, O^T = V^T P^T.  Codes become f16
@@ -90,17 +90,20 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
+// over the lanes whose numbers differ in the bits from FROM on
+template <int FROM>
+__device__ __forceinline__ float max_from(float v) {
+#pragma unroll
+  for (int o = FROM; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+template <int FROM>
+__device__ __forceinline__ float sum_from(float v) {
+#pragma unroll
+  for (int o = FROM; o < 32; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
 // over the 8 lanes with the same t
-__device__ __forceinline__ float max_g(float v) {
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  return v;
-}
-__device__ __forceinline__ float sum_g(float v) {
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
 __device__ __forceinline__ uint32_t or_g(uint32_t v) {
 #pragma unroll
   for (int o = 4; o < 32; o <<= 1) v |= __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -124,14 +127,40 @@ struct Joined {
   float top;
 };
 
+// The root of a part's share 2^(l - top), multiplied in twice: the share may be below the normal floats, and the part's
+// values as far above 1.
+__device__ __forceinline__ float share_root(float l, float top) {
+  return ex2(0.5f * (l - (top == -INFINITY ? 0.0f : top)));
+}
+template <int D>
+__device__ __forceinline__ void add_part(float2 (&acc)[D / 64], const float2 (&v)[D / 64], float root) {
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+    acc[c].x = fmaf(v[c].x * root, root, acc[c].x);
+    acc[c].y = fmaf(v[c].y * root, root, acc[c].y);
+  }
+}
+template <int D>
+__device__ __forceinline__ void load_part(float2 (&v)[D / 64], const float* part, int row, int lane) {
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) v[c] = *reinterpret_cast<const float2*>(part + row * D + c * 64 + 2 * lane);
+}
+template <int D>
+__device__ __forceinline__ Joined<D> finish(const float2 (&acc)[D / 64], float top, float sum) {
+  Joined<D> j;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) j.acc[c] = make_float2(acc[c].x * inv, acc[c].y * inv);
+  j.top = sum == 0.0f ? -INFINITY : top + log2f(sum);
+  return j;
+}
+
 // Row `row` of the parts i0, i0 + step .. of n, each R rows of D and then the rows' log2 sums; the loads of four
 // parts are on their way together.
 template <int D, class Part>
 __device__ __forceinline__ Joined<D> join_parts(int n, int i0, int step, int lane, int row, int R, Part part) {
-  Joined<D> j;
+  float2 acc[D / 64] = {};
   float top = -INFINITY, sum = 0.0f;
-#pragma unroll
-  for (int c = 0; c < D / 64; ++c) j.acc[c] = make_float2(0.0f, 0.0f);
   for (int i = i0; i < n; i += 4 * step) {
     float2 v[4][D / 64];
     float l[4], now = top;
@@ -139,36 +168,27 @@ __device__ __forceinline__ Joined<D> join_parts(int n, int i0, int step, int lan
     for (int k = 0; k < 4; ++k) {
       const float* at = part(min(i + k * step, n - 1));
       l[k] = at[R * D + row];
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) v[k][c] = *reinterpret_cast<const float2*>(at + row * D + c * 64 + 2 * lane);
+      load_part<D>(v[k], at, row, lane);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (i + k * step >= n) l[k] = -INFINITY;
       now = fmaxf(now, l[k]);
     }
-    const float base = now == -INFINITY ? 0.0f : now, keep = ex2(top - base);
+    const float base = now == -INFINITY ? 0.0f : now, keep = ex2(0.5f * (top - base));
     top = now;
-    sum *= keep;
+    sum *= keep * keep;
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) j.acc[c] = make_float2(j.acc[c].x * keep, j.acc[c].y * keep);
+    for (int c = 0; c < D / 64; ++c) acc[c] = make_float2(acc[c].x * keep * keep, acc[c].y * keep * keep);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (i + k * step >= n) continue;
-      const float w = ex2(l[k] - base);
-      sum += w;
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        j.acc[c].x = fmaf(w, v[k][c].x, j.acc[c].x);
-        j.acc[c].y = fmaf(w, v[k][c].y, j.acc[c].y);
-      }
+      const float root = share_root(l[k], base);
+      sum = fmaf(root, root, sum);
+      add_part<D>(acc, v[k], root);
     }
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-  for (int c = 0; c < D / 64; ++c) j.acc[c] = make_float2(j.acc[c].x * inv, j.acc[c].y * inv);
-  j.top = sum == 0.0f ? -INFINITY : top + log2f(sum);
-  return j;
+  return finish<D>(acc, top, sum);
 }
 // the row as a partial result again
 template <int D>
@@ -185,51 +205,45 @@ __device__ __forceinline__ void store_joined(const KvAttnParams& p, const Joined
   if (p.lse != nullptr && lane == 0) p.lse[row] = j.top * kLn2;
 }
 
-// Rows row0 .. row0 + RB - 1 of n parts at once, for one warp: the loads of a part's rows are on their way together.
+// Rows row0 .. row0 + RB - 1 of n <= 8 parts at once, for one warp: the sums one a lane (of row lane % RB), the loads of
+// a part's rows on their way together.
 template <int D, int RB, class Part, class Store>
 __device__ __forceinline__ void join_rows(int n, int lane, int row0, int rows, int R, Part part, Store store) {
-  float2 acc[RB][D / 64];
-  float top[RB], sum[RB];
+  constexpr int kAtOnce = 32 / RB, kTimes = RB / 4;   // sums of kAtOnce parts at a time
+  static_assert(kAtOnce * kTimes == 8 && kTimes <= 2, "8 parts");
+  float2 v[RB][D / 64], acc[RB][D / 64] = {};
+  auto load = [&](int i) {
 #pragma unroll
-  for (int k = 0; k < RB; ++k) {
-    top[k] = -INFINITY;
-    sum[k] = 0.0f;
+    for (int k = 0; k < RB; ++k) load_part<D>(v[k], part(i), min(row0 + k, rows - 1), lane);
+  };
+  float root[kTimes], top = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) acc[k][c] = make_float2(0.0f, 0.0f);
+  for (int h = 0; h < kTimes; ++h) {
+    const int i = lane / RB + h * kAtOnce;
+    root[h] = i < n ? part(i)[R * D + min(row0 + lane % RB, rows - 1)] : -INFINITY;
+    top = fmaxf(top, root[h]);
   }
-  for (int i = 0; i < n; ++i) {
-    const float* at = part(i);
-    float2 v[RB][D / 64];
-    float l[RB];
+  load(0);
+  top = max_from<RB>(top);
 #pragma unroll
-    for (int k = 0; k < RB; ++k) {
-      const int row = min(row0 + k, rows - 1);
-      l[k] = at[R * D + row];
+  for (int h = 0; h < kTimes; ++h) {
+    root[h] = share_root(root[h], top);
+    sum = fmaf(root[h], root[h], sum);
+  }
+  sum = sum_from<RB>(sum);
+#pragma unroll 1
+  for (int i = 0;;) {
+    const float mine = i < kAtOnce ? root[0] : root[kTimes - 1];
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) v[k][c] = *reinterpret_cast<const float2*>(at + row * D + c * 64 + 2 * lane);
-    }
-#pragma unroll
-    for (int k = 0; k < RB; ++k) {
-      const float now = fmaxf(top[k], l[k]), base = now == -INFINITY ? 0.0f : now;
-      const float keep = ex2(top[k] - base), w = ex2(l[k] - base);
-      top[k] = now;
-      sum[k] = fmaf(sum[k], keep, w);
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        acc[k][c].x = fmaf(acc[k][c].x, keep, w * v[k][c].x);
-        acc[k][c].y = fmaf(acc[k][c].y, keep, w * v[k][c].y);
-      }
-    }
+    for (int k = 0; k < RB; ++k) add_part<D>(acc[k], v[k], __shfl_sync(0xFFFFFFFFu, mine, i % kAtOnce * RB + k));
+    if (++i >= n) break;
+    load(i);
   }
 #pragma unroll
   for (int k = 0; k < RB; ++k) {
+    const float t = __shfl_sync(0xFFFFFFFFu, top, k), of_row = __shfl_sync(0xFFFFFFFFu, sum, k);
     if (row0 + k >= rows) break;
-    Joined<D> j;
-    const float inv = sum[k] == 0.0f ? 0.0f : 1.0f / sum[k];
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) j.acc[c] = make_float2(acc[k][c].x * inv, acc[k][c].y * inv);
-    j.top = sum[k] == 0.0f ? -INFINITY : top[k] + log2f(sum[k]);
-    store(row0 + k, j);
+    store(row0 + k, finish<D>(acc[k], t, of_row));
   }
 }
 
@@ -489,16 +503,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
             s[n][st][i] = z;
             top[j] = fmaxf(top[j], z);
           }
-        float add[2], base_m[2], shrink[2];
+        float unit_w[2], to_l[2], shrink[2], sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          top[j] = max_g(top[j]);
+          top[j] = max_from<4>(top[j]);
           const float m2 = fmaxf(m[n][j], top[j]), M2 = fmaxf(M[n][j], top[j] + ev);
-          base_m[j] = m2 == -INFINITY ? 0.0f : m2;
-          const float base_M = M2 == -INFINITY ? 0.0f : M2;
-          l[n][j] *= ex2(m[n][j] - base_m[j]);
+          const float base_m = m2 == -INFINITY ? 0.0f : m2, base_M = M2 == -INFINITY ? 0.0f : M2;
+          l[n][j] *= ex2(m[n][j] - base_m);
           shrink[j] = ex2(M[n][j] - base_M);
-          add[j] = ex2(fminf(base_m[j] + ev - base_M + kTopWeight, 126.0f));
+          // 2^unit: the unit of this page's weights.  Where the values are so small that no weight reaches f16, a
+          // finer one, in which the sum of the weights loses nothing.
+          unit_w[j] = top[j] == -INFINITY ? 0.0f : fminf(M2 - ev - kTopWeight, top[j] + 90.0f);
+          to_l[j] = ex2(fminf(unit_w[j] - base_m, 126.0f));
           m[n][j] = m2;
           M[n][j] = M2;
         }
@@ -513,13 +529,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
           float w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            w[i] = ex2(s[n][st][i] - base_m[i & 1]);
-            l[n][i & 1] += w[i];
-            w[i] *= add[i & 1];
+            w[i] = ex2(s[n][st][i] - unit_w[i & 1]);
+            sum[i & 1] += w[i];
           }
           pw[n][st][0] = turn8x8(pack_f16x2(w[0], w[1]));
           pw[n][st][1] = turn8x8(pack_f16x2(w[2], w[3]));
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) l[n][j] = fmaf(sum[j], to_l[j], l[n][j]);
       }
 
       uint32_t keep[4];
@@ -599,7 +616,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
     for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float sum = sum_g(l[n][j]);
+        const float sum = sum_from<4>(l[n][j]);
         // the sum of the weights is never 0 where a row sees a position; NaN stays
         // 2^(M - 15 - m) in two halves, as it may be below the normal floats where the values of the pages are least
         const float half = sum == 0.0f ? 0.0f : ex2(0.5f * (M[n][j] - kTopWeight - m[n][j]));

@@ -124,6 +124,28 @@ def test_a_position_that_takes_most_of_the_weight(new, group, dim, nats, at):
     close(out, lse, shared_reference(q, c, s, new), dim)
 
 
+@pytest.mark.parametrize("sequences", [2, 80])       # a page a worker, and several
+@pytest.mark.parametrize("first", [0, 1])            # which page has the weight
+@pytest.mark.parametrize("bits", [100, 161, 201])    # how far the other's scores lie below
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,group", FORMS)
+def test_little_weight_on_very_large_values(new, group, dim, bits, first, sequences):
+    # values of 2^-120 where the weight is, of 2^119 elsewhere: those decide the output
+    heads = 16 if sequences > 2 else 2
+    g = torch.Generator(device="cuda").manual_seed(5)
+    k, v = (torch.randn(128, heads, dim, device="cuda", generator=g) for _ in "kv")
+    there, far = slice(64 * first, 64 * first + 64), slice(64 - 64 * first, 128 - 64 * first)
+    k[..., 0] = 0.0
+    k[far, :, 0] = -bits * np.log(2) * dim ** 0.5 / 64
+    v[there] *= 2.0 ** -116
+    v[far] *= 2.0 ** 124
+    c, s = shared(k, v, sequences, new)
+    q = randn(sequences * new, heads * group, dim, seed=6, std=0.5)
+    q[..., 0] = 64.0
+    out, lse = rn.kv_attention(q, c, s, causal=False, return_lse=True)
+    close(out, lse, shared_reference(q, c, s, new), dim)
+
+
 @pytest.mark.parametrize("sequences", [1, 40])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("new,group", FORMS + [(10, 16)])
