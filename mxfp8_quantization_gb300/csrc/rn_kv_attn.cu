@@ -610,6 +610,20 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
     }
 
     // ----------------------------------------------------- the segment's end
+    // 2^(M - 15 - m) in two halves, as it may be below the normal floats where the values of the pages are least
+    float half[NB][2];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) half[n][j] = m[n][j] == -INFINITY ? 0.0f : ex2(0.5f * (M[n][j] - kTopWeight - m[n][j]));
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float2 v = mul2(make_float2(o[n][d][i], o[n][d][i + 1]), make_float2(half[n][0], half[n][1]));
+          o[n][d][i] = v.x, o[n][d][i + 1] = v.y;
+        }
+    }
     float* part = dealt.per_cta == 1 ? kv_part(p.ws, blockIdx.x, begins ? 1 : 0, R, D)
                                      : kv_worker_part(p.ws, me, begins ? 1 : 0, R, D);
 #pragma unroll
@@ -618,9 +632,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
       for (int j = 0; j < 2; ++j) {
         const float sum = sum_from<4>(l[n][j]);
         // the sum of the weights is never 0 where a row sees a position; NaN stays
-        // 2^(M - 15 - m) in two halves, as it may be below the normal floats where the values of the pages are least
-        const float half = sum == 0.0f ? 0.0f : ex2(0.5f * (M[n][j] - kTopWeight - m[n][j]));
-        const float inv = sum == 0.0f ? 0.0f : half / sum;
+        const float inv = sum == 0.0f ? 0.0f : __fdividef(half[n][j], sum);
         const float log2s = sum == 0.0f ? -INFINITY : m[n][j] + log2f(sum);
         const int r = n * 8 + 2 * t + j;
         if (r >= it.rows) continue;
@@ -631,13 +643,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rn_kv_attn_kernel(const KvAttn
           for (int d = 0; d < D / 16; ++d)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-              out[16 * d + 8 * i] = (uint16_t)pack_bf16x2(o[n][d][2 * i + j] * inv * half, 0.0f);
+              out[16 * d + 8 * i] = (uint16_t)pack_bf16x2(o[n][d][2 * i + j] * inv, 0.0f);
           if (p.lse != nullptr && g == 0) p.lse[row] = log2s * kLn2;
         } else {
 #pragma unroll
           for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) part[r * D + 16 * d + 8 * i + g] = o[n][d][2 * i + j] * inv * half;
+            for (int i = 0; i < 2; ++i) part[r * D + 16 * d + 8 * i + g] = o[n][d][2 * i + j] * inv;
           if (g == 0) part[R * D + r] = log2s;
         }
       }

@@ -699,8 +699,11 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
         const float mm = fmaxf(m, mo), MM = fmaxf(M, Mo);
         const float bm = mm == -INFINITY ? 0.0f : mm, bM = MM == -INFINITY ? 0.0f : MM;
         const float sum = l * ex2(m - bm) + lo * ex2(mo - bm);
-        // 2^(M - 9 - m) in two halves, as it may be below the normal floats where the values of the pages are least
-        const float half = sum == 0.0f ? 0.0f : ex2(0.5f * (bM - kTopWeight - bm)), unit = sum == 0.0f ? 0.0f : half / sum;
+        // 2^(M - 9 - m); in two halves where it may be below the normal floats, as the values of the pages are least
+        float power = bM - kTopWeight - bm;
+        const bool halves = __any_sync(0xFFFFFFFFu, power < -90.0f);
+        if (halves) power *= 0.5f;
+        const float unit = sum == 0.0f ? 0.0f : ex2(power) / sum;
         const float fa = unit * ex2(M - bM), fb = unit * ex2(Mo - bM);
         const float log2s = sum == 0.0f ? -INFINITY : bm + log2f(sum);
         const int64_t row = (int64_t)(it.s0 + qi) * (p.c.heads * p.group.d) + qh;
@@ -716,7 +719,10 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
           for (int i = 0; i < 32; ++i) {
             o[i] = sum == 0.0f ? 0.0f : o[i] * fa;
             if (odd) o[i] = sum == 0.0f ? 0.0f : fmaf(u[i], fb, o[i]);
-            o[i] *= half;
+          }
+          if (halves) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= ex2(power);
           }
           if (!real) continue;
           if (whole) {
