@@ -424,8 +424,11 @@ rn_status rn_quantize_only(const float* y, int64_t N, int64_t H,
  * blocks of RN_KV_PAGE = 64; block i of sequence b is page table[b, i] of
  *   k         E4M3 codes [pages, heads, 64, dim]
  *   v         E4M3 codes [pages, heads, dim, 64] (values transposed)
- *   k_scales  E8M0 bytes [pages, heads]: an element stands for its code's
- *   v_scales  value * 2^(byte - 127)
+ *   k_scales  E8M0 bytes [pages, heads] from 7 to 246: an element stands for
+ *   v_scales  its code's value * 2^(byte - 127)
+ * 448 * 2^119 is the last that is finite in bf16, and every element is a bf16
+ * then; the write leaves no other bytes, and what the read and the attention find
+ * below 7 counts as 7, above 246 as 246.
  * All are the caller's and need not be initialized.  k and v 16-byte aligned; dim
  * 64, 128, 192 or 256; up to 65535 heads and 2^31 - 1 pages.
  */
@@ -453,12 +456,13 @@ typedef struct {
  * Rows outside every sequence (before starts[0], from starts[sequences] on)
  * are neither read nor written.  A page number outside [0, pages) and a block
  * past table_width mean that the block's positions are not cached: they are
- * not written, read as 0, and no query sees them; the same holds for a row
- * whose position is negative.  starts are cut to [0, tokens], so that no
- * contents of the arrays lead out of the caller's memory; starts that descend
- * give unspecified results.  Up to 2^24 sequences, 2^30 - 1 rows and 2^25 - 1
- * blocks a sequence.  The write and the read launch 2 * heads * (tokens / 64 +
- * 2 * sequences) units, which must stay below 2^31.
+ * not written, read as 0, and no query sees them.  A row whose position is
+ * negative is not written and reads as 0; its query sees nothing if causal, else
+ * the whole sequence.  starts are cut to [0, tokens], so that no contents of the
+ * arrays lead out of the caller's memory; starts that descend give unspecified
+ * results.  Up to 2^24 sequences, 2^30 - 1 rows and 2^25 - 1 blocks a sequence.
+ * The write and the read launch 2 * heads * (tokens / 64 + 2 * sequences) units,
+ * which must stay below 2^31.
  */
 typedef struct {
   const int32_t* table;

@@ -629,7 +629,7 @@ _I32 = torch.int32
 @dataclass
 class KVCache:
     """A paged 8-bit key/value cache (``kv_cache_alloc``): an element stands for its code's value times
-    2 ** (scale - 127) of its page and head."""
+    2 ** (scale - 127) of its page and head (scales below 7 count as 7, above 246 as 246)."""
     k: torch.Tensor         # uint8 E4M3 [pages, heads, 64, dim]
     v: torch.Tensor         # uint8 E4M3 [pages, heads, dim, 64] (transposed)
     k_scales: torch.Tensor  # uint8 E8M0 [pages, heads]

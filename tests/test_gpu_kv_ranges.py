@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import mxfp8_quantization_gb300 as rn
-from kv_check import check, make, randn, reference
+from kv_check import arrays, check, make, oracle_cache, randn, reference
+from oracle import kv as K
 
 pytestmark = pytest.mark.gpu
 
@@ -162,3 +163,24 @@ def test_values_at_the_least_scale(new, group, dim, sequences):
     q[..., 0] = 8.0
     out, lse = rn.kv_attention(q, c, s, causal=False, return_lse=True)
     close(out, lse, shared_reference(q, c, s, new), dim)
+
+
+@pytest.mark.parametrize("new,group", FORMS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_scale_bytes_that_no_write_leaves(new, group, dim):
+    c, s, T = make([64 * 7] * 3, [new] * 3, 2, dim, seed=9)
+    for i, byte in enumerate((0, 6, 7, 246, 247, 255)):
+        pages = s.table[:, i].long()
+        c.v_scales[pages] = byte
+        c.k_scales[pages] = min(byte, 7)     # (scores of 2^119 would be none)
+    near = rn.KVCache(c.k, c.v, c.k_scales.clamp(7, 246), c.v_scales.clamp(7, 246))
+    q = randn(T, 2 * group, dim, seed=9)
+    for kw in (dict(), dict(causal=False, window=200)):
+        got, want = (rn.kv_attention(q, x, s, return_lse=True, **kw) for x in (c, near))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    c.k_scales[:] = c.v_scales
+    every = rn.KVSequences(s.table, torch.arange(4, dtype=torch.int32, device="cuda") * 64 * 7, s.lens)
+    for dtype in (torch.bfloat16, torch.float32):
+        got = rn.kv_cache_read(c, every, 3 * 64 * 7, out_dtype=dtype)
+        want = K.read(oracle_cache(c), *arrays(every), 3 * 64 * 7)
+        assert all(np.array_equal(f64(x), y) for x, y in zip(got, want))
