@@ -740,9 +740,11 @@ def kv_cache_read(cache, seqs, tokens, out_dtype=torch.bfloat16):
     bfloat16 or float32, both exact.  Rows outside every sequence are left uninitialized."""
     lib = _lib or _load()
     dev = torch.cuda.current_device()
-    c, q = _kv_args(cache, seqs, int(tokens), dev)
     if tokens < 0:
         raise RNError(f"tokens must not be negative, got {tokens}")
+    if tokens >= 1 << 30:
+        raise RNError(f"tokens must be below 2**30, got {tokens}")
+    c, q = _kv_args(cache, seqs, int(tokens), dev)
     shape = (q.tokens, c.heads, c.dim)
     k = torch.empty(shape, dtype=out_dtype, device=cache.k.device)
     v = torch.empty(shape, dtype=out_dtype, device=cache.k.device)
@@ -796,7 +798,7 @@ def kv_attention(q, cache, seqs, scale=None, causal=True, window=0, softcap=0.0,
     out = torch.empty((T, heads, D), dtype=_BF, device=q.device)
     lse = torch.empty((T, heads), dtype=_FP32, device=q.device) if return_lse else None
     st = lib.rn_kv_attention(q.data_ptr(), _BF16, qs, heads, c, s, D ** -0.5 if scale is None else float(scale),
-                             int(bool(causal)), int(window), float(softcap), _addr(slopes), out.data_ptr(),
+                             int(bool(causal)), min(max(int(window), -1), (1 << 63) - 1), float(softcap), _addr(slopes), out.data_ptr(),
                              _addr(lse), workspace.data_ptr(), ctypes.byref(n), _raw_stream(dev))
     if st:
         _check(st, "rn_kv_attention")
