@@ -519,13 +519,19 @@ rn_status rn_kv_cache_read(const rn_kv_cache* cache, const rn_kv_seqs* seqs, voi
  * inputs.  Scores and sums are fp32; the weights, times their values' scales, are
  * rounded once to 11 significant bits (or, below 2^-23 of the row's largest, to
  * a multiple of 2^-33 of it), the output once to bf16.  The sums are the tensor
- * cores' fp32, which cut off instead of rounding.  What a query does not see has no part in its
- * output, whatever it holds; outputs of queries that see a NaN, or hold a
- * non-finite value themselves, are unspecified.  Results are the same from run
- * to run.  Workspace protocol as for rn_layernorm_bwd: with workspace and out
- * NULL the call stores the required byte count in *workspace_bytes.  It depends
- * on dim only; the workspace need not be initialized and must not be shared
- * by calls that may run concurrently.
+ * cores' fp32, which cut off instead of rounding.  What a query does not see has
+ * no part in its output, whatever it holds; outputs of queries that see a NaN,
+ * hold a non-finite value themselves or have scores outside fp32's range are
+ * unspecified.  Results are the same from run to run.
+ * One form serves the whole call, chosen by the mean number of rows a sequence
+ * (tokens * G / sequences, those without rows counted): up to 16 the one for
+ * single tokens, else the one for prompts, each 2 to 6 times slower at the
+ * other's work.  Prompts and single tokens are faster in two calls, and
+ * `sequences` should not be padded.
+ * Workspace protocol as for rn_layernorm_bwd: with workspace and out NULL the
+ * call stores the required byte count in *workspace_bytes.  It depends on dim
+ * only; the workspace need not be initialized and must not be shared by calls
+ * that may run concurrently.
  */
 rn_status rn_kv_attention(const void* q, rn_dtype dtype, int64_t q_stride, int64_t q_heads,
                           const rn_kv_cache* cache, const rn_kv_seqs* seqs, float scale,

@@ -777,7 +777,7 @@ def kv_attention(q, cache, seqs, scale=None, causal=True, window=0, softcap=0.0,
     ``return_lse``.  ``scale``: 1 / sqrt(dim) by default; ``causal``: positions up to the query's own;
     ``window`` > 0: the last ``window`` of those; ``softcap`` > 0: softcap * tanh(score / softcap);
     ``slopes`` fp32 [q_heads]: + slope * (position - the query's).  Rows outside every sequence are left
-    uninitialized."""
+    uninitialized.  Prompts and single tokens are faster in two calls than in one."""
     lib = _lib or _load()
     dev = torch.cuda.current_device()
     c, s = _kv_args(cache, seqs, 0, dev)

@@ -35,13 +35,13 @@
 // their partial results in the workers' order: by their CTA, and where it goes
 // beyond one CTA, by a second kernel.
 //
-// What bounds it: the cache's bytes, with about 12 us around them.  64 sequences
-// of up to 16384, 8 heads of 128, groups of 8 (1.24 GB): 208 us, 5.96 TB/s, 0.89 of
-// the measured copy rate; one of 131072 (268 MB) 56 us, 4.8 TB/s: pages stream at
-// 6.7 TB/s for 36 us, the dealing takes 2, the first pages 3, the joins 6.  The rest of a
-// small call (1000 positions: 9.4 us) is latency: the call's arrays, the page
-// table, the page, the join.  9 to 16 rows double the products and exponentials of a
-// page: 32 sequences of 8192, 4 heads, groups of 16 72 us (floor 40).
+// What bounds it: the cache's bytes, with about 15 us around them.  64 sequences
+// of up to 16384, 8 heads of 128, groups of 8 (1.24 GB): 206 us, 6.02 TB/s, 0.90 of
+// the measured copy rate; one of 131072 (268 MB, 40 us at that rate) 55 us, 4.9 TB/s:
+// besides the bytes the launches, the dealing, the first pages' latency and two
+// joins.  The rest of a small call (1000 positions: 9.4 us) is latency: the call's
+// arrays, the page table, the page, the join.  9 to 16 rows double the products and
+// exponentials of a page: 32 sequences of 8192, 4 heads, groups of 16 69 us (floor 40).
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -785,7 +785,9 @@ rn_status launch_d(const KvAttnParams& p, int sms, cudaStream_t s) {
   const bool extra = p.softcap > 0.0f || p.slopes != nullptr;
   // By the mean rows of a sequence and head; no more is known on the host.  us, this kernel against the tiles: 16 rows,
   // 32 x 8192, dim 64 86 / 128, dim 128 72 / 89, dim 192 134 / 141, dim 256 174 / 174; 20 rows, dim 128 105 / 99;
-  // 24 rows, dim 64 147 / 132, dim 128 188 / 168; 32 rows, dim 128 191 / 168.
+  // 24 rows, dim 64 147 / 132, dim 128 188 / 168; 32 rows, dim 128 191 / 168.  Those are batches of one kind; where both
+  // are mixed, one kind gets the other's kernel (60 x 1 on up to 16384 and a prompt of 512, groups of 8: 697, apart 206
+  // and 36; 512 x 1 on 1000 and a prompt of 4096, groups of 1: 666, apart 182 and 79).
   const int64_t rows = (int64_t)p.q.tokens * p.group.d;  // of a head, all sequences
   if (rows > (int64_t)16 * p.q.B) return launch_kv_tile(p, D, sms, s);
   const bool one = rows <= (int64_t)8 * p.q.B;

@@ -20,8 +20,8 @@
 // the first ones add both results up at the end.  dim > 128, NG = 1: the output
 // takes half of the tensor memory; one tile, two buffers of scores.
 //
-// What bounds it: 4096 new tokens on 8192, 64 query heads of 128 over 8: 1272 us,
-// 1080 TFLOP/s, 0.56 of the measured bf16 rate; a page of two tiles takes 2200
+// What bounds it: 4096 new tokens on 8192, 64 query heads of 128 over 8: 1279 us,
+// 1075 TFLOP/s, 0.56 of the measured bf16 rate; a page of two tiles takes 2200
 // cycles, of which the products are 1024 (tensor pipe 46 % active).  The rest is
 // latency: a tile's page goes products -> scores -> weights -> products in turn
 // (reading scores 60 cycles, their maximum 270, the exponentials 450, storing and
@@ -31,7 +31,7 @@
 // both tiles share (1288 us); 8 softmax warps a tile with half the scores a thread
 // (1829); the products issued by one thread (2074), by two warps (1288), or by
 // several specialized instruction sequences (1477).  20 rows a head (32 x 4 tokens on
-// 6000, groups of 5) 98 us where the cache's bytes take 38: a page takes the conversion
+// 6000, groups of 5) 97 us where the cache's bytes take 38: a page takes the conversion
 // 1080 cycles and the issuing warp 990 where memory would allow 700.
 //
 // The weights' reference M, whose weight is 2^9, is not raised for less than 2^6.5
@@ -240,7 +240,7 @@ struct Stats {
 };
 
 // What a (row tile, head) costs besides its pages, in pages (its queries' way into tensor memory, the first page's
-// latency, the output: 11 000 cycles and more; a page 2200)
+// latency, the output: 11 000 cycles and more; a page 2200, both at dim 128 without options, the only ones measured)
 constexpr int kExtra = 6;
 
 // log2 of the weight at the reference M, and how far weights may go above it before M is raised: f16 ends at 2^16,
@@ -564,7 +564,8 @@ __global__ void __launch_bounds__(kTileThreads<D>, 1) rn_kv_tile_kernel(const Kv
         tc_fence_after();
         if constexpr (EXTRA) {
           // Capped and biased 16 at a time, back where they were: as a part of the 64 below, this would be four times
-          // the instructions, more than the SM's instruction cache holds.
+          // the instructions, more than the SM's instruction cache holds (4 x 1024, groups of 4, biased 230 us, now 104;
+          // 4096 on 8192 with a cap 5970, now 2577, without one 1279).
           const float inv_cap = 1.0f / p.softcap;
 #pragma unroll 1
           for (int h = 0; h < 64; h += 16) {
