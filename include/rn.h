@@ -521,8 +521,9 @@ rn_status rn_kv_cache_read(const rn_kv_cache* cache, const rn_kv_seqs* seqs, voi
  * a multiple of 2^-33 of it), the output once to bf16.  The sums are the tensor
  * cores' fp32, which cut off instead of rounding.  What a query does not see has
  * no part in its output, whatever it holds; outputs of queries that see a NaN,
- * hold a non-finite value themselves or have scores outside fp32's range are
- * unspecified.  Results are the same from run to run.
+ * hold a non-finite value themselves or have scores of more than 2^22 in
+ * magnitude (whose fp32 steps are 1/2) are unspecified.  Results are the same
+ * from run to run.
  * One form serves the whole call, chosen by the mean number of rows a sequence
  * (tokens * G / sequences, those without rows counted): up to 16 the one for
  * single tokens, else the one for prompts, each 2 to 6 times slower at the

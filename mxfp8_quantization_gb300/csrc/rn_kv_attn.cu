@@ -17,7 +17,8 @@
 // two that puts its largest magnitude at 2^14 (what is 2^28 below it loses
 // bits: 2^-39 of the row's largest); weights are rounded to f16, half a step of
 // 2^-11 down to 2^-29 of the largest, which the bf16 output's 2^-8 covers.  Sums
-// are fp32.
+// are fp32.  m + eV and the like are exact up to |m| = 2^23: whole numbers on
+// multiples of 1/2.
 //
 // Which positions the rows and which dims the reduction index of a fragment
 // stand for is free as long as both operands agree, so a lane reads 16
@@ -79,15 +80,6 @@ __device__ __forceinline__ uint32_t turn8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
 }
 
 // over the lanes whose numbers differ in the bits from FROM on

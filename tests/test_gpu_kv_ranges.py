@@ -184,3 +184,34 @@ def test_scale_bytes_that_no_write_leaves(new, group, dim):
         got = rn.kv_cache_read(c, every, 3 * 64 * 7, out_dtype=dtype)
         want = K.read(oracle_cache(c), *arrays(every), 3 * 64 * 7)
         assert all(np.array_equal(f64(x), y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("bits", [8, 13, 19])     # (8 * 2^19 is the largest score there may be)
+@pytest.mark.parametrize("sequences", [1, 60])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,group", FORMS + [(10, 16)])
+def test_scores_up_to_the_largest(new, group, dim, sequences, bits, sign):
+    # exact multiples of 2^bits, so that all weight is at the two positions of the largest; pages of different size
+    n, heads, at = 330, 2, [70, 75]
+    g = torch.Generator(device="cuda").manual_seed(10)
+    k, v = (torch.randn(n, heads, dim, device="cuda", generator=g) for _ in "kv")
+    k[..., 0] = torch.randint(-7, 1, (n, heads), device="cuda", generator=g) - (1.0 if sign < 0 else 0.0)
+    k[at, :, 0] = 8.0 if sign > 0 else -0.5
+    v *= torch.exp2(torch.tensor([0.0, -15.0, 5.0, 1.0, -60.0, 3.0], device="cuda").repeat_interleave(64)[:n, None, None])
+    c, s = shared(k, v, sequences, new)
+    q = torch.zeros(sequences * new, heads * group, dim, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 2.0 ** bits
+    out, lse = rn.kv_attention(q, c, s, scale=1.0, causal=False, return_lse=True)
+    every = rn.KVSequences(s.table[:1], torch.tensor([0, n], dtype=torch.int32, device="cuda"), s.lens[:1])
+    kk, vv = rn.kv_cache_read(c, every, n, out_dtype=torch.float32)
+    assert (kk[at, :, 0] == k[at, :, 0]).all()
+    want = f64(vv[at].double().mean(0).repeat_interleave(group, 0))
+    size = f64(vv[at].double().abs().mean(0).repeat_interleave(group, 0))
+    # the others are e^-128 and less, and 2^20 larger at most.  Two equal weights, each rounded once to f16 (2^-11);
+    # exponentials and divisions 2^-20; the output bf16
+    tol = size * (2.0 ** -11 + 2.0 ** -20) + np.abs(want) * 2.0 ** -8 + 2.0 ** -60
+    assert np.all(np.abs(f64(out) - want) <= tol), float((np.abs(f64(out) - want) / tol).max())
+    top = 2.0 ** bits * float(k[at[0], 0, 0])
+    # the maximum in base 2, its unit and back: four roundings of 2^-24 and the exponential's 2^-22
+    assert np.all(np.abs(f64(lse) - top - np.log(2)) <= abs(top) * 2.0 ** -22 + 2.0 ** -20)
